@@ -527,6 +527,104 @@ w4a8_status w4a8_mxfp4_gemm_prepared_noalloc(const uint8_t *d_x_fp8, const float
 size_t      w4a8_mxfp4_gemm_prepared_noalloc_max_scratch(void);
 
 /* ---------------------------------------------------------------------------
+ * Attention block on a 4-bit cache: norms of queries and keys for each head
+ * with the position rotation, the paged MXFP4 key/value cache, and softmax
+ * attention over it.  Not on the pages: these calls are what a serving program
+ * needs between this library's linears, on the library's own MXFP4 format.
+ *
+ * 16-bit activations are bf16 or fp16 (w4a8_float); strides are in elements,
+ * the head_dim values of a head are contiguous.  head_dim is 64, 128 or 256
+ * (else UNSUPPORTED_SHAPE), heads at most 1024, tokens x heads < 2^30.
+ * Inputs may be non-finite here: see each call. */
+typedef enum { W4A8_BF16 = 0, W4A8_FP16 = 1 } w4a8_float;
+
+/* The cache, in caller-owned device memory (16-byte aligned):
+ *   k_codes, v_codes  uint8 [pages][kv_heads][page][head_dim / 2]: e2m1 codes,
+ *                     the even element in the low nibble
+ *   k_e8m0, v_e8m0    uint8 [pages][kv_heads][head_dim / 32][page]: exponent
+ *                     bytes of the 32-blocks along head_dim
+ * page: rows per page, a power of two from 16 to 1024; pages >= 1 and
+ * pages * page < 2^40.  Token i of a sequence lies in row i % page of the page
+ * that entry i / page of its block table names.  An exponent byte 255 marks a
+ * block that held a non-finite value: it reads as NaN. */
+typedef struct {
+    uint8_t *k_codes, *k_e8m0, *v_codes, *v_e8m0;
+    int64_t pages;
+    int kv_heads, page, head_dim;
+} w4a8_kv_cache;
+
+/* For queries [tokens][q_heads][head_dim] and keys [tokens][k_heads][head_dim]:
+ *   x <- x (mean(x^2) + eps)^-1/2 w      where the weight (fp32 [head_dim]) is given
+ *   (a, b) <- (a c - b s, b c + a s)     for the pairs (i, i + rot/2) of the first
+ *       rot values, (2i, 2i + 1) with interleaved != 0; c = row[i], s = row[rot/2 + i],
+ *       row = cos_sin[position] of the fp32 [cos_rows][rot] table
+ * in fp32, rounded once.  d_q or d_k may be NULL with 0 heads (not both); rot = 0:
+ * no rotation (table and positions unused), else a multiple of 16 up to head_dim
+ * (else UNSUPPORTED_SHAPE).  Outputs are contiguous, 16-byte aligned, and must not
+ * overlap inputs unless they are the same contiguous tensor.  The turned values of
+ * a token whose position lies outside the table are NaN. */
+w4a8_status w4a8_qk_norm_rope(w4a8_float type, const uint16_t *d_q, int64_t q_stride_token, int64_t q_stride_head,
+                              int q_heads, const uint16_t *d_k, int64_t k_stride_token, int64_t k_stride_head,
+                              int k_heads, int64_t tokens, int head_dim, const float *d_q_weight,
+                              const float *d_k_weight, float eps, const float *d_cos_sin, int64_t cos_rows,
+                              const int64_t *d_positions, int rot, int interleaved, uint16_t *d_q_out,
+                              uint16_t *d_k_out, void *stream);
+
+/* Keys and values of `tokens` tokens into the cache rows d_slots (int64 [tokens]:
+ * page * cache.page + row, each row at most once; a slot outside the cache, as -1
+ * for padding, is skipped).  Keys are normed and turned as above on the way, in
+ * fp64 and rounded once to fp32; per 32 values the exponent by `mode`
+ * (W4A8_EXP_OCP or W4A8_EXP_NOCLIP) and the nearest codes, exactly as
+ * w4a8_quant_bf16_to_mxfp4 encodes.  A block with a NaN or infinite value is
+ * stored as NaN.  With q_heads > 0 the tokens' queries are normed and turned in
+ * the same launch (fp32, into d_q_out). */
+w4a8_status w4a8_kv_append_mxfp4(const w4a8_kv_cache *cache, w4a8_float type, const uint16_t *d_k,
+                                 int64_t k_stride_token, int64_t k_stride_head, const uint16_t *d_v,
+                                 int64_t v_stride_token, int64_t v_stride_head, int64_t tokens,
+                                 const int64_t *d_slots, w4a8_exp_mode mode, const float *d_k_weight, float eps,
+                                 const float *d_cos_sin, int64_t cos_rows, const int64_t *d_positions, int rot,
+                                 int interleaved, const uint16_t *d_q, int64_t q_stride_token,
+                                 int64_t q_stride_head, int q_heads, const float *d_q_weight, uint16_t *d_q_out,
+                                 void *stream);
+
+/* The cache's rows at d_slots as bf16 [tokens][kv_heads][head_dim] (exact); zeros
+ * for a slot outside the cache. */
+w4a8_status w4a8_kv_read_mxfp4(const w4a8_kv_cache *cache, int64_t tokens, const int64_t *d_slots,
+                               uint16_t *d_k_out, uint16_t *d_v_out, void *stream);
+
+/* out[t] = softmax(scale q[t] . k + mask) v over the cached keys of t's sequence,
+ * for queries [tokens][q_heads][head_dim] (q_heads a multiple of kv_heads: head h
+ * reads key head h / (q_heads / kv_heads)); out contiguous, of the queries' type.
+ *   d_cu_q          int32 [seqs + 1], sequence s has the query tokens cu_q[s] ..
+ *                   cu_q[s+1]-1, at most max_q; NULL: one token each (tokens == seqs,
+ *                   max_q == 1)
+ *   d_context_lens  int32 [seqs]: cached tokens, the new ones (already appended)
+ *                   among them: query i of n stands at position context - n + i
+ *   d_block_table   int32 [seqs][table_stride], table_width entries used; entries
+ *                   past a sequence's context are not read
+ *   causal          a query sees the keys up to its own position, with window > 0
+ *                   the last `window` of these; not causal: all (window must be 0)
+ * A query that sees no key (context 0, or more query tokens than context) gives
+ * zeros.  Lengths are clamped to the tensors they index (context to the table,
+ * queries to `tokens` and max_q: rows past max_q are not written).  A table entry
+ * outside the cache, a NaN block, or a value block whose exponent byte is 253 or
+ * 254 makes the scores of its keys NaN; keys that a query does not see never
+ * reach its output, whatever the cache holds there.  Scores and sums are fp32, the
+ * probabilities are rounded to bf16 (fp16 queries: to two bf16 pieces).
+ *
+ * d_ws: w4a8_attention_workspace_bytes(seqs, max_q, ...) bytes, 256-byte aligned,
+ * needing no initialization; one sized for more sequences and query tokens of
+ * the same heads serves smaller calls too.  UNSUPPORTED_SHAPE: seqs * kv_heads * the table's keys / 64, or
+ * seqs * q_heads * max_q, of 2^30 and more. */
+size_t      w4a8_attention_workspace_bytes(int64_t seqs, int64_t max_q, int q_heads, int kv_heads, int head_dim);
+w4a8_status w4a8_attention_mxfp4(const w4a8_kv_cache *cache, w4a8_float type, const uint16_t *d_q,
+                                 int64_t q_stride_token, int64_t q_stride_head, int q_heads, int64_t tokens,
+                                 int64_t seqs, const int32_t *d_cu_q, int64_t max_q,
+                                 const int32_t *d_block_table, int64_t table_stride, int64_t table_width,
+                                 const int32_t *d_context_lens, float scale, int causal, int window,
+                                 uint16_t *d_out, void *d_ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Decode band with an explicit plan, for tile-size sweeps (the two GEMM entry
  * points above pick these parameters themselves).  Computes exactly what
  * w4a8_mxfp4_gemm (kind MXFP4: d_w = packed codes, d_w_scale = e8m0) or

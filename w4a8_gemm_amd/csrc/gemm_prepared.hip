@@ -3540,7 +3540,7 @@ size_t tiled_workspace_bytes(int64_t M, int64_t N, int64_t K, bool int4, int for
 // 128 x 128) it lost 9 %: the short last round of the single launch runs on
 // a quarter of the CUs at a higher clock, and the narrow tiles' copy feed per
 // product is twice that of the wide ones.
-static int device_cus();
+
 struct PfTail {
     int64_t n_main;   // leading columns on 256 x 256 tiles (a multiple of 256)
     int bm, bn;       // the tail's tile
@@ -3953,7 +3953,7 @@ hipError_t launch_dtile(const DtPlan& p, const uint8_t* x8, const float* xs, con
 
 
 // CUs of the current device (cached per device)
-static int device_cus() {
+int device_cus() {
     static int cache[64] = {};
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;

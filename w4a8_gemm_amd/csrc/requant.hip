@@ -32,24 +32,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Block exponent from amax (>= 0), exact integer forms of the closed rules:
-//   ocp     floor(log2 a) - 2
-//   noclip  the least e with a <= 6 * 2^e
-// amax below the smallest normal is raised to it; amax == 0 gives 0; the result
-// is clamped to [-127, 127].
-__device__ __forceinline__ int block_exponent(float amax, int mode) {
-    if (!(amax > 0.0f)) return 0;
-    const float safe = fmaxf(amax, 0x1p-126f);
-    const uint32_t bits = __float_as_uint(safe);
-    const int p = (int)(bits >> 23) - 127;  // floor(log2 safe)
-    int e;
-    if (mode == W4A8_EXP_OCP)
-        e = p - 2;
-    else  // mantissa <= 1.5 fits under 6 * 2^(p-2), otherwise one binade up
-        e = p - 2 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    return max(-127, min(127, e));
-}
-
 // Encode one block at exponent e: the e2m1 codes of w / 2^e and, if ERR, the
 // fp32 squared error of the block summed in element order.  The codes come
 // from the matrix-format conversion instruction, whose rounding is the page's
@@ -59,16 +41,6 @@ __device__ __forceinline__ int block_exponent(float amax, int mode) {
 // input's sign in bit 3.  A negative value that rounds to zero therefore comes
 // out as code 8 (-0), which is folded to code 0: the page sets the sign only on
 // nonzero codes.
-template <int T>
-__device__ __forceinline__ uint32_t to_e2m1(uint32_t old, float a0, float a1) {
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a0, a1, 1.0f, T);   // byte T <- codes of a0, a1
-}
-// the sign bit of every nibble whose magnitude bits are zero cleared (8 -> 0)
-__device__ __forceinline__ uint32_t fold_neg_zero(uint32_t x) {
-    const uint32_t m = x & 0x77777777u;
-    const uint32_t nz = (m | (m >> 1) | (m >> 2)) & 0x11111111u;   // nibble bit 0: magnitude != 0
-    return m | (x & (nz << 3));
-}
 // squared errors of the two elements of byte T, added to err in element order.
 // The grid value q has the sign of w (or is zero), so q - w = +-(|q| - |w|) and
 // its square is that of |q| - |w|: the difference is exact (the magnitudes are

@@ -113,6 +113,37 @@ __device__ __forceinline__ uint32_t f32_to_e4m3_rne_sat(float y) {
     return sign | code;
 }
 
+// Block exponent from amax (>= 0), exact integer forms of the closed rules:
+//   ocp     floor(log2 a) - 2
+//   noclip  the least e with a <= 6 * 2^e
+// amax below the smallest normal is raised to it; amax == 0 gives 0; the result
+// is clamped to [-127, 127].
+__device__ __forceinline__ int block_exponent(float amax, int mode) {
+    if (!(amax > 0.0f)) return 0;
+    const float safe = fmaxf(amax, 0x1p-126f);
+    const uint32_t bits = __float_as_uint(safe);
+    const int p = (int)(bits >> 23) - 127;  // floor(log2 safe)
+    int e;
+    if (mode == W4A8_EXP_OCP)
+        e = p - 2;
+    else  // mantissa <= 1.5 fits under 6 * 2^(p-2), otherwise one binade up
+        e = p - 2 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+    return max(-127, min(127, e));
+}
+
+// The e2m1 codes of two values (already divided by the block's 2^e), by the
+// matrix-format conversion instruction: nearest grid point, ties to the even
+// index, magnitudes above 6 saturating at 6, the input's sign in bit 3.
+template <int T>
+__device__ __forceinline__ uint32_t to_e2m1(uint32_t old, float a0, float a1) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a0, a1, 1.0f, T);   // byte T <- codes of a0, a1
+}
+// the sign bit of every nibble whose magnitude bits are zero cleared (8 -> 0)
+__device__ __forceinline__ uint32_t fold_neg_zero(uint32_t x) {
+    const uint32_t m = x & 0x77777777u;
+    const uint32_t nz = (m | (m >> 1) | (m >> 2)) & 0x11111111u;   // nibble bit 0: magnitude != 0
+    return m | (x & (nz << 3));
+}
 // ---------------------------------------------------------------------------
 // launchers (host side; each returns a hipError_t from the launch)
 // ---------------------------------------------------------------------------
@@ -148,6 +179,55 @@ hipError_t launch_act_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx
 bool act_quant_sm_fits(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* x8);
 hipError_t launch_act_quant_sm(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, uint8_t* x8, float* xs,
                                uint8_t* x8s, hipStream_t stream);
+
+// Heads of a batch of tokens (kv_cache.hip): hq query, hk key and hv value
+// heads per token; strides in elements.  slots == NULL: queries and keys are
+// normed, turned and written to q_out / k_out ([tokens][heads][head_dim]); else
+// keys and values go to the cache rows that slots names.
+struct HeadRows {
+    const uint16_t *q, *k, *v;
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+    int hq, hk, hv;
+    int64_t tokens;
+    const float *q_weight, *k_weight;   // NULL: no norm
+    float eps;
+    const float* cos_sin;               // [cs_rows][rot]
+    int64_t cs_rows;
+    const int64_t* positions;
+    int rot;                            // 0: no rotation
+    bool interleaved;
+    uint16_t *q_out, *k_out;
+    w4a8_kv_cache cache;                // head_dim is read without slots too
+    int page_shift;
+    const int64_t* slots;
+    int mode;
+};
+hipError_t launch_head_rows(const HeadRows& a, bool fp16, hipStream_t stream);
+hipError_t launch_kv_read(const w4a8_kv_cache& c, int page_shift, int64_t tokens, const int64_t* slots, uint16_t* k_out,
+                          uint16_t* v_out, hipStream_t stream);
+
+// Attention of new tokens over the paged MXFP4 cache (attention.hip).
+struct AttnArgs {
+    w4a8_kv_cache cache;
+    int page_shift;
+    const uint16_t* q;
+    int64_t q_st, q_sh;                 // elements
+    uint16_t* out;                      // [tokens][hq][head_dim]
+    int hq, group;                      // group = hq / kv_heads
+    int64_t tokens;
+    int seqs, max_q;
+    const int32_t* cu_q;                // NULL: one token per sequence
+    const int32_t* table;
+    int64_t table_stride;
+    int table_width;
+    const int32_t* context;
+    float scale;
+    int causal, window;                 // window 0: none
+    uint8_t* ws;
+};
+size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, int head_dim);
+hipError_t launch_attention(const AttnArgs& a, bool fp16, hipStream_t stream);
+int device_cus();   // CUs of the current device (cached per device)
 
 // GEMM plans: the host picks the band, the tile and the K split.
 struct GemmPlan {
