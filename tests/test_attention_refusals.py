@@ -1,26 +1,43 @@
 """CPU: what the attention block's calls refuse, at the C entry points (before any device
-work: the fake pointers are never touched) and in the binding."""
+work: the fake pointers are never touched) and in their Python interface."""
 import ctypes
 
 import pytest
 import torch
 
 import w4a8_gemm_amd as w4
-from w4a8_gemm_amd import attention as at
+from w4a8_gemm_amd import binding
 
 OK, INVALID, SHAPE, WORKSPACE, ASYM, HIP = range(6)
 FAKE = 0x100000
 
 
+_vp, _i64, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k_codes", _vp), ("k_e8m0", _vp), ("v_codes", _vp), ("v_e8m0", _vp), ("pages", _i64),
+                ("kv_heads", _int), ("page", _int), ("head_dim", _int)]
+
+
 @pytest.fixture(scope="module")
 def L():
-    return at._lib()
+    """The library with the calls' signatures set, on a handle of its own."""
+    lib = ctypes.CDLL(binding.LIB_PATH)
+    cache, heads, turn = ctypes.POINTER(_Cache), [_vp, _i64, _i64], [_vp, _i64, _vp, _int, _int]
+    lib.w4a8_qk_norm_rope.argtypes = [_int, *heads, _int, *heads, _int, _i64, _int, _vp, _vp, _f32, *turn, _vp, _vp, _vp]
+    lib.w4a8_kv_append_mxfp4.argtypes = [cache, _int, *heads, *heads, _i64, _vp, _int, _vp, _f32, *turn, *heads, _int, _vp,
+                                         _vp, _vp]
+    lib.w4a8_kv_read_mxfp4.argtypes = [cache, _i64, _vp, _vp, _vp, _vp]
+    lib.w4a8_attention_mxfp4.argtypes = [cache, _int, *heads, _int, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _f32, _int,
+                                         _int, _vp, _vp, ctypes.c_size_t, _vp]
+    return lib
 
 
 def _cache(**kw):
     v = dict(k_codes=FAKE, k_e8m0=FAKE, v_codes=FAKE, v_e8m0=FAKE, pages=4, kv_heads=2, page=16, head_dim=128)
     v.update(kw)
-    return ctypes.byref(at._Cache(*v.values()))
+    return ctypes.byref(_Cache(*v.values()))
 
 
 BAD_CACHES = [(dict(k_codes=None), INVALID), (dict(v_e8m0=None), INVALID), (dict(k_codes=FAKE + 8), INVALID),
@@ -111,49 +128,97 @@ def test_workspace_bytes(L):
         assert need[0] > 0 and need == sorted(need)
 
 
-def test_binding_refusals():
-    bf = torch.bfloat16
-    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
-    good = [u8(3, 2, 16, 64), u8(3, 2, 4, 16), u8(3, 2, 16, 64), u8(3, 2, 4, 16)]
+BF, I32, I64 = torch.bfloat16, torch.int32, torch.int64
+
+
+def _u8(*s):
+    return torch.zeros(s, dtype=torch.uint8)
+
+
+def _tensors():
+    return [_u8(3, 2, 16, 64), _u8(3, 2, 4, 16), _u8(3, 2, 16, 64), _u8(3, 2, 4, 16)]
+
+
+def test_cache_and_workspace_refusals():
+    good = _tensors()
     cache = w4.KVCacheMXFP4(*good)
     assert (cache.pages, cache.kv_heads, cache.page, cache.head_dim) == (3, 2, 16, 128)
-    for i, t in ((0, u8(3, 2, 16, 48)), (0, u8(3, 2, 24, 64)), (1, u8(3, 2, 16, 4)), (2, u8(2, 2, 16, 64)),
-                 (3, u8(3, 2, 4, 16, 1)), (0, u8(3, 2, 64, 16).transpose(2, 3))):
+    assert cache.k_codes is good[0] and cache.v_e8m0 is good[3]
+    for i, t in ((0, _u8(3, 2, 16, 48)), (0, _u8(3, 2, 24, 64)), (1, _u8(3, 2, 16, 4)), (2, _u8(2, 2, 16, 64)),
+                 (3, _u8(3, 2, 4, 16, 1)), (0, _u8(3, 2, 64, 16).transpose(2, 3))):
         bad = list(good)
         bad[i] = t
         with pytest.raises(ValueError):
             w4.KVCacheMXFP4(*bad)
-    with pytest.raises(TypeError):
-        w4.KVCacheMXFP4(good[0].float(), *good[1:])
+    for bad in (good[0].float(), None, "codes"):
+        with pytest.raises(TypeError):
+            w4.KVCacheMXFP4(bad, *good[1:])
     with pytest.raises(ValueError):
         w4.KVCacheMXFP4.empty(2, 2, 96, device="cpu")
-    x = torch.zeros(2, 4, 128, dtype=bf)
-    with pytest.raises(ValueError, match="GPU"):
-        w4.qk_norm_rope(x, x)
-    with pytest.raises(TypeError):
-        w4.qk_norm_rope(x.float(), None)
-    with pytest.raises(ValueError, match="GPU"):
-        w4.kv_append_mxfp4(cache, x[:, :2], x[:, :2], torch.zeros(2, dtype=torch.int64))
-    with pytest.raises(TypeError):
-        w4.kv_read_mxfp4(good, torch.zeros(2, dtype=torch.int64))
-    with pytest.raises(ValueError, match="GPU"):
-        w4.attention_mxfp4(x, cache, torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32))
-    with pytest.raises(ValueError):
-        at._mode("mse")
-    for args in ((0, 1, 4, 2, 128), (1, 1, 4, 3, 128), (1, 1, 4, 2, 80)):
+    for args in ((0, 1, 4, 2, 128), (1, 1, 4, 3, 128), (1, 1, 4, 2, 80), (1 << 29, 1, 4, 2, 128)):
         with pytest.raises(ValueError):
             w4.AttentionWorkspace(*args, device="cpu")
-    cpu = torch.device("cpu")
-    cs = torch.zeros(5, 24)
-    with pytest.raises(ValueError, match="multiple of 16"):
-        at._turn(cs, None, cpu, 2, 128)
-    with pytest.raises(ValueError, match="positions"):
-        at._turn(cs[:, :16].contiguous(), None, cpu, 2, 128)
-    with pytest.raises(TypeError):
-        at._turn(cs.double(), None, cpu, 2, 128)
-    with pytest.raises(ValueError):
-        at._heads(x[:, :, ::2], "q", bf, cpu, 64)
-    with pytest.raises(ValueError):
-        at._heads(x, "q", bf, cpu, 128, tokens=3)
-    with pytest.raises(ValueError):
-        at._weight(torch.zeros(64), "q_weight", cpu, 128)
+
+
+# Every other check comes before the one for a GPU, so that all of them show on CPU tensors.
+X = torch.zeros(3, 4, 128, dtype=BF)
+CS, POS, W = torch.zeros(5, 64), torch.zeros(3, dtype=I64), torch.ones(128)
+
+
+@pytest.mark.parametrize("error,match,kw", [
+    (ValueError, "GPU", {}), (ValueError, "GPU", dict(q=None)), (ValueError, "GPU", dict(cos_sin=None, positions=None)),
+    (TypeError, "float", dict(q=X.float())), (TypeError, "k must", dict(k=X.half())), (TypeError, "tensor", dict(q=None, k=None)),
+    (ValueError, "head_dim", dict(q=X[:, :, :96])), (ValueError, "head_dim", dict(q=X[0])),
+    (ValueError, "k must", dict(k=X[:2])), (ValueError, "contiguous heads", dict(q=X.repeat(1, 1, 2)[:, :, ::2])),
+    (ValueError, "multiple of 16", dict(cos_sin=torch.zeros(5, 24))), (ValueError, "multiple of 16", dict(cos_sin=torch.zeros(5, 144))),
+    (ValueError, "cos_sin", dict(cos_sin=CS[:, ::2])), (ValueError, "cos_sin", dict(cos_sin=CS[:0])),
+    (TypeError, "cos_sin", dict(cos_sin=CS.double())), (ValueError, "positions", dict(positions=None)),
+    (TypeError, "positions", dict(positions=POS.int())), (ValueError, "positions", dict(positions=POS[:2])),
+    (ValueError, "q_weight", dict(q_weight=W[:64])), (TypeError, "k_weight", dict(k_weight=W.to(BF))),
+    (TypeError, "real number", dict(eps="small"))])
+def test_norm_rope_arguments(error, match, kw):
+    a = dict(q=X, k=X[:, :2], cos_sin=CS, positions=POS, q_weight=W, k_weight=W)
+    a.update(kw)
+    with pytest.raises(error, match=match):
+        w4.qk_norm_rope(**a)
+
+
+@pytest.mark.parametrize("error,match,kw", [
+    (ValueError, "GPU", {}), (ValueError, "GPU", dict(q=X, cos_sin=CS, positions=POS)), (TypeError, "cache", dict(cache=None)),
+    (TypeError, "cache", dict(cache=_tensors())), (ValueError, "k must", dict(k=X)), (ValueError, "v must", dict(v=X[:2, :2])),
+    (TypeError, "v must", dict(v=X[:, :2].half())), (TypeError, "slots", dict(slots=POS.int())),
+    (ValueError, "slots", dict(slots=POS[:2])), (ValueError, "mode", dict(mode="mse")), (ValueError, "mode", dict(mode=0)),
+    (ValueError, "q must", dict(q=X[:2])), (TypeError, "q must", dict(q=X.float())), (ValueError, "positions", dict(cos_sin=CS))])
+def test_append_arguments(error, match, kw):
+    a = dict(cache=w4.KVCacheMXFP4(*_tensors()), k=X[:, :2], v=X[:, 2:], slots=POS)
+    a.update(kw)
+    with pytest.raises(error, match=match):
+        w4.kv_append_mxfp4(**a)
+
+
+def test_read_arguments():
+    cache = w4.KVCacheMXFP4(*_tensors())
+    for error, args in ((ValueError, (cache, POS)), (TypeError, (_tensors(), POS)), (TypeError, (cache, POS.int())),
+                        (ValueError, (cache, POS[None])), (TypeError, (cache, [0, 1]))):
+        with pytest.raises(error):
+            w4.kv_read_mxfp4(*args)
+
+
+@pytest.mark.parametrize("error,match,kw", [
+    (ValueError, "GPU", {}), (TypeError, "cache", dict(cache=None)), (TypeError, "q must", dict(q=X.float())),
+    (ValueError, "q must", dict(q=X[:, :, :64])), (ValueError, "multiple", dict(q=X[:, :3])),
+    (ValueError, "one query token", dict(q=X[:2])), (ValueError, "one query token", dict(max_q=2)),
+    (ValueError, "max_q", dict(max_q=0)), (TypeError, "context_lens", dict(context_lens=POS)),
+    (ValueError, "context_lens", dict(context_lens=torch.ones(3, 1, dtype=I32))),
+    (ValueError, "block_table", dict(block_table=torch.zeros(2, 4, dtype=I32))),
+    (ValueError, "block_table", dict(block_table=torch.zeros(4, 3, dtype=I32).T)),
+    (ValueError, "block_table", dict(block_table=torch.zeros(3, 0, dtype=I32))),
+    (TypeError, "block_table", dict(block_table=torch.zeros(3, 4))), (ValueError, "cu_q", dict(cu_q=torch.zeros(3, dtype=I32))),
+    (TypeError, "cu_q", dict(cu_q=torch.zeros(4, dtype=I64))), (ValueError, "window", dict(window=-1)),
+    (ValueError, "window", dict(window=4, causal=False)), (TypeError, "real number", dict(scale="1"))])
+def test_attention_arguments(error, match, kw):
+    a = dict(q=X, cache=w4.KVCacheMXFP4(*_tensors()), block_table=torch.zeros(3, 4, dtype=I32),
+             context_lens=torch.ones(3, dtype=I32))
+    a.update(kw)
+    with pytest.raises(error, match=match):
+        w4.attention_mxfp4(**a)

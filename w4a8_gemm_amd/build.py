@@ -1,4 +1,5 @@
-"""Build libw4a8.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libw4a8.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+_attention.so, the compiled Python entry of the attention block, with g++ (host code only).
 
 Compiles every ``csrc/*.hip`` into one shared library next to this file.  Flags:
   -O3 --offload-arch=gfx950      CDNA4 only
@@ -13,12 +14,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libw4a8.so")
+MODULE = os.path.join(HERE, "_attention.so")
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -30,6 +33,28 @@ COMMON = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-ffp-contract=
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+
+
+def build_module(verbose: bool = False) -> str:
+    """Compile _attention.so against torch's headers and libw4a8.so beside it."""
+    import torch
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    inc = [os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(rocm, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    out = MODULE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc),
+           os.path.join(CSRC, "attention_bind.cpp"), "-o", out, f"-L{HERE}", "-l:libw4a8.so",
+           f"-L{os.path.join(tdir, 'lib')}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on attention_bind.cpp:\n{r.stderr}")
+    os.replace(out, MODULE)
+    return MODULE
 
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
@@ -52,6 +77,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(out, LIB)
+    build_module(verbose)
     return LIB
 
 
