@@ -178,12 +178,15 @@ def test_workspace_is_reused_and_results_repeat():
     c = Case([(1, 3000), (1, 10)], 8, 2, 128, 64, BF, seed=5)
     ws = w4.AttentionWorkspace(4, 1, 8, 2, 128)
     say("attention workspace")
-    ws.buf.fill_(255)                                # NaN bytes: nothing of it is read before it is written
+    head = int(w4.lib().w4a8_attention_counter_bytes())
+    assert (ws.buf[:head] == 0).all()
+    ws.buf[head:].fill_(255)                         # NaN bytes: nothing of it is read before it is written
     cache, first = c.cache(), None
     for _ in range(3):
         got = c.run(cache=cache, workspace=ws)
         assert first is None or torch.equal(got, first)
         first = got
+    assert (ws.buf[:head] == 0).all()                # every call leaves its counters at zero
     small = Case([(1, 40)], 8, 2, 128, 64, BF, seed=6)
     got = small.run(workspace=ws).cpu().double()
     want, tol = small.want()

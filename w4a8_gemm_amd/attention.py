@@ -122,8 +122,10 @@ def attention_workspace_bytes(seqs: int, max_q: int, q_heads: int, kv_heads: int
 
 class AttentionWorkspace:
     """Caller-owned workspace of attention_mxfp4: partial results of sequences whose keys
-    are shared by several workgroups.  It serves every call of at most these sequences and
-    query tokens with these heads.  Calls that share one must not overlap in time."""
+    are shared by several workgroups, and the counters of their joins.  It serves every call
+    of at most these sequences and query tokens with these heads.  Allocated by torch and its
+    counters zeroed once; every call leaves them at zero.  Calls that share one must not
+    overlap in time."""
 
     def __init__(self, seqs: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int, device="cuda"):
         if min(seqs, max_q, q_heads, kv_heads) < 1 or q_heads % kv_heads or head_dim not in HEAD_DIMS:
@@ -133,6 +135,7 @@ class AttentionWorkspace:
         if not self.nbytes:
             raise ValueError("sizes beyond what the attention serves")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.buf[:binding.lib().w4a8_attention_counter_bytes()].zero_()
 
 
 def attention_mxfp4(q: torch.Tensor, cache: KVCacheMXFP4, block_table: torch.Tensor, context_lens: torch.Tensor,

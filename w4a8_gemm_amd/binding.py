@@ -119,6 +119,8 @@ def lib() -> ctypes.CDLL:
         L.w4a8_int4g128_gemm_prepared.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp,
                                                   _size, _vp]
         L.w4a8_int4g128_gemm_prepared.restype = _int
+        L.w4a8_attention_counter_bytes.argtypes = []
+        L.w4a8_attention_counter_bytes.restype = _size
         L.w4a8_attention_workspace_bytes.argtypes = [_i64, _i64, _int, _int, _int]
         L.w4a8_attention_workspace_bytes.restype = _size
         L.w4a8_status_string.argtypes = [_int]

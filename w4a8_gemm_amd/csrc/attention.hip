@@ -168,8 +168,9 @@ __device__ __forceinline__ uint32_t out_pair(float a, float b) {
 //
 // All sequences' tiles of 64 keys, head after head, form one line that is cut
 // into equal runs, one per workgroup; a run may cross segments (one sequence's
-// one head), and a segment cut by runs is joined by a second kernel.  The cut
-// follows the lengths in device memory, so the grid depends on none of them.
+// one head), and a segment that several runs share is joined by the last of
+// them to arrive (below).  The cut follows the lengths in device memory, so the
+// grid depends on none of them.
 //
 // A wave takes every fourth tile of its workgroup's run.  Rows of 16 queries are
 // the columns of the 16x16 products:
@@ -179,6 +180,10 @@ __device__ __forceinline__ uint32_t out_pair(float a, float b) {
 //   O^T = V^T P^T: the product's k-slots are filled in that order, so P moves
 //     between no lanes, and lane (n, g) reads from keys 16g .. 16g+15 the D/16
 //     values of dims n D/16 ..: the transpose happens in its own registers.
+// The next tile's loads are issued as soon as this one's registers are free:
+// exponents and keys after the scores, values after the products.  Loads return
+// in order, so nothing that is needed early is asked for late: the block-table
+// entries of a run lie in LDS.
 // ===========================================================================
 template <int D>
 struct VWord;   // D/16 e2m1 codes
@@ -196,131 +201,288 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int s) {
     const Seq q = seq_of(a, s);
     return q.qlen ? max(1, (q.ctx + kTile - 1) / kTile - first_tile(a, q)) : 0;
 }
-
-struct Line {       // the cut: total tiles over heads, tiles per workgroup
-    int total, run;
-};
-__device__ __forceinline__ Line line_of(const AttnArgs& a, int workgroups) {
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive
     const int lane = threadIdx.x & 63;
-    int t = 0;
-    for (int s = lane; s < a.seqs; s += 64) t += tiles_of(a, s);
 #pragma unroll
-    for (int off = 32; off; off >>= 1) t += __shfl_xor(t, off);
-    Line l;
-    l.total = t * a.cache.kv_heads;
-    // a run gives every wave a tile
-    l.run = max((l.total + workgroups - 1) / workgroups, 4);
-    return l;
+    for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(v, off);
+        if (lane >= off) v += o;
+    }
+    return v;
 }
-// The sequence whose tiles hold position `at` of the line, its first position
-// and tiles per head (at < total).
-__device__ __forceinline__ void seq_at(const AttnArgs& a, int at, int* seq, int* start, int* tiles) {
-    const int lane = threadIdx.x & 63;
+
+// A workgroup's run [pos, end) of the line, and the sequence that holds its
+// start: first position and tiles per head.
+struct Run {
+    int total, run;          // of the line; per workgroup
+    int pos, end;
+    int seq, start, tiles;
+};
+__device__ __forceinline__ Run run_of(const AttnArgs& a, int workgroups) {
+    const int lane = threadIdx.x & 63, hk = a.cache.kv_heads;
+    Run r;
+    int n = lane < a.seqs ? tiles_of(a, lane) : 0;
+    int incl = wave_scan(n);
+    const int64_t head = (int64_t)__shfl(incl, 63);
+    int64_t t = head;
+    for (int s0 = 64; s0 < a.seqs; s0 += 64) t += __shfl(wave_scan(s0 + lane < a.seqs ? tiles_of(a, s0 + lane) : 0), 63);
+    const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    r.total = uniform((int)t * hk);
+    r.run = uniform(max((r.total + workgroups - 1) / workgroups, 4));   // a tile for every wave
+    const int64_t pos = (int64_t)blockIdx.x * r.run;
+    r.pos = (int)min(pos, (int64_t)r.total);
+    r.end = min(r.pos + r.run, r.total);
+    r.seq = a.seqs;
+    r.start = r.tiles = 0;
+    if (r.pos >= r.total) return r;
     int base = 0;
     for (int s0 = 0; s0 < a.seqs; s0 += 64) {
-        const int n = s0 + lane < a.seqs ? tiles_of(a, s0 + lane) : 0;
-        int incl = n;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int o = __shfl_up(incl, off);
-            if (lane >= off) incl += o;
+        if (s0) {
+            n = s0 + lane < a.seqs ? tiles_of(a, s0 + lane) : 0;
+            incl = wave_scan(n);
         }
-        const int first = base + (incl - n) * a.cache.kv_heads;
-        const uint64_t hit = __ballot(n > 0 && at >= first && at < first + n * a.cache.kv_heads);
+        const int first = base + (incl - n) * hk;
+        const uint64_t hit = __ballot(n > 0 && r.pos >= first && r.pos < first + n * hk);
         if (hit) {
             const int l = __ffsll((unsigned long long)hit) - 1;
-            *seq = s0 + l;
-            *start = __shfl(first, l);
-            *tiles = __shfl(n, l);
-            return;
+            r.seq = s0 + l;
+            r.start = uniform(__shfl(first, l));
+            r.tiles = uniform(__shfl(n, l));
+            break;
         }
-        base += __shfl(incl, 63) * a.cache.kv_heads;
+        base += uniform(__shfl(incl, 63)) * hk;
     }
-    *seq = a.seqs;
-    *start = base;
-    *tiles = 0;
+    return r;
 }
 
-// floats of one partial result: rows x (D outputs, then maximum and sum)
+// ---- joining the pieces of a segment ----
+//
+// Piece i of a segment belongs to workgroup w0 + i; its result (rows x D
+// unnormalized outputs, the rows' maxima, their sums) lies in slot 2 w + 1 of
+// the workspace where the segment begins in that run, else in slot 2 w.  Eight
+// pieces are joined by the last of the eight to arrive, into the first one's
+// slot, eight such results by the last of these, and so on: a segment of 512
+// pieces takes three rounds.  Always in the pieces' order, so the result does
+// not depend on which came last.  Nobody waits: a workgroup that is not last
+// goes on.
+constexpr int kJoin = 8, kLevels = 4;   // 8^4 pieces
 __host__ __device__ constexpr int64_t part_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
+__host__ __device__ constexpr int64_t counter_words(int workgroups) { return (int64_t)kLevels * 2 * workgroups; }
+
+// Joins `count` results (the j-th at slot(j)) of `rows` live rows: into slot(0),
+// or normalized into the output.  R = rows of a slot.
+template <int D, int R, bool FP16, typename SLOT, typename OUT>
+__device__ __forceinline__ void join_pieces(__amdgpu_buffer_rsrc_t ws, SLOT slot, int count, int rows, bool final, OUT out,
+                                            float* sm) {
+    constexpr int C = D / 4;                // threads per row
+    constexpr int RG = 256 / C;
+    float* weight = sm;                     // [kJoin][R]
+    float* inv = sm + kJoin * R;            // [R]
+    const int tid = threadIdx.x;
+    if (tid < rows) {
+        float m[kJoin], l[kJoin], mx = neg_inf(), sum = 0.0f;
+        auto word = [&](int j, int k) {
+            return __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, (int)(slot(j) + 4u * (uint32_t)(R * D + k * R + tid)), 0, 16));
+        };
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            m[j] = j < count ? word(j, 0) : neg_inf();
+            l[j] = j < count ? word(j, 1) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) mx = fmaxf(mx, m[j]);
+        const float u = mx == neg_inf() ? 0.0f : mx;
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            const float w = exp2f(m[j] - u);
+            if (j < count) weight[j * R + tid] = w;
+            sum += l[j] * w;
+        }
+        inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (!final) {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(mx), ws, (int)(slot(0) + 4u * (uint32_t)(R * D + tid)), 0, 16);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(sum), ws, (int)(slot(0) + 4u * (uint32_t)(R * D + R + tid)), 0, 16);
+        }
+    }
+    __syncthreads();
+    const int c = tid % C;
+    for (int row = tid / C; row < rows; row += RG) {
+        sk_i32x4 v[kJoin];
+        const uint32_t at = 4u * (uint32_t)(row * D + 4 * c);
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j)
+            if (j < count) v[j] = sk_get4(ws, slot(j) + at);
+        float acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j)
+            if (j < count) {
+                const float w = weight[j * R + row];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] += __int_as_float(v[j][i]) * w;
+            }
+        if (final) {
+            const float f = inv[row];
+            *reinterpret_cast<uint2*>(out(row) + 4 * c) =
+                make_uint2(out_pair<FP16>(acc[0] * f, acc[1] * f), out_pair<FP16>(acc[2] * f, acc[3] * f));
+        } else {
+            sk_put4(ws, slot(0) + at, acc[0], acc[1], acc[2], acc[3]);
+        }
+    }
+}
 
 template <int D, int NT, int PC>
 __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const int workgroups) {
     constexpr int KS = D >= 128 ? D / 128 : 1;      // 128-deep products per score
     constexpr int QP = D >= 128 ? PC : PC - 1;      // q operands per 128 (D = 64: pieces side by side)
     constexpr int DT = D / 16;                      // output tiles
+    constexpr int C = D / 64;                       // runs of 16 query values per lane
+    constexpr int R = NT * 16;
     typedef typename VWord<D>::T VT;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int hk = a.cache.kv_heads, ps = a.page_shift;
-    __shared__ float sm_m[4][NT * 16], sm_l[4][NT * 16];
-    __shared__ v4f sm_o[2][NT * DT][64];
+    // queries while the keys stream, then the waves' results
+    constexpr int kQBytes = NT * KS * QP * 2048, kOBytes = 2 * NT * DT * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kQBytes > kOBytes ? kQBytes : kOBytes];
+    __shared__ float sm_m[4][R], sm_l[4][R], sm_j[(kJoin + 1) * R];
+    __shared__ uint32_t sm_flag;
+    __shared__ int32_t sm_table[16 * kTile + 1];
+    uint4* const sm_q = reinterpret_cast<uint4*>(smem);                 // [nt][k][p][half][lane]
+    v4f* const sm_o = reinterpret_cast<v4f*>(smem);                     // [wave][nt][tile][lane]
+    uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws);
+    float* const parts = reinterpret_cast<float*>(a.ws) + counter_words(workgroups);
 
-    const Line line = line_of(a, workgroups);
-    int pos = (int)blockIdx.x * line.run;
-    if ((int64_t)blockIdx.x * line.run >= line.total) return;
-    const int end = min(pos + line.run, line.total);
-    int sq, start, tiles;
-    seq_at(a, pos, &sq, &start, &tiles);
-    if (sq >= a.seqs) return;
+    Run r = run_of(a, workgroups);
+    if (r.seq >= a.seqs) return;
 
-    while (pos < end) {
-        const int head = (pos - start) / tiles;
-        const int t0 = (pos - start) - head * tiles;
-        const int cnt = min(tiles - t0, end - pos);
-        const Seq s = seq_of(a, sq);
+    while (r.pos < r.end) {
+        const int head = (r.pos - r.start) / r.tiles;
+        const int t0 = (r.pos - r.start) - head * r.tiles;
+        const int cnt = min(r.tiles - t0, r.end - r.pos);
+        const Seq s = seq_of(a, r.seq);
         const int rows = s.qlen * a.group;
         const int first = first_tile(a, s);
-        const int32_t* table = a.table + (int64_t)sq * a.table_stride;
+        const int32_t* table = a.table + (int64_t)r.seq * a.table_stride;
+        const int t_end = s.ctx > 0 ? first + t0 + cnt : 0;
+        int t = first + t0 + wave;
 
-        // ---- queries ----
-        v8i qf[NT][KS][QP];
-        float mult[NT];
+        uint4 kc[KS][4];
+        uint32_t ke[KS], k_bad = 0;
+        VT vc[16];
+        uint4 ve_next;
+        const int last_key = s.ctx - 1;             // ctx >= 1 wherever it is used
+        int page0 = 0;                              // the first of the block-table entries in LDS
+        auto fill_table = [&](int from, int to) {   // those of tiles [from, to)
+            page0 = (from * kTile) >> ps;
+            const int count = (min(to * kTile - 1, last_key) >> ps) - page0 + 1;
+            for (int i = threadIdx.x; i < count; i += 256) sm_table[i] = table[page0 + i];
+        };
+        // the page of a lane's four keys, and of its sixteen values; keys past the
+        // context take the last one's (they are masked).  An entry outside the cache
+        // makes its keys' scales NaN, at the product: a select here would wait for them.
+        auto load_k = [&](int at) {
+            const int pk = sm_table[(min(at * kTile + 4 * n, last_key) >> ps) - page0];
+            const int pv = sm_table[(min(at * kTile + 16 * g, last_key) >> ps) - page0];
+            {
+                const int64_t ph = (int64_t)((uint32_t)pv < (uint64_t)a.cache.pages ? pv : 0) * hk + head;
+                const int row = (at * kTile + 16 * g) & ((1 << ps) - 1);
+                ve_next = *reinterpret_cast<const uint4*>(a.cache.v_e8m0 + ((ph * (D / 32) + n / (512 / D)) << ps) + row);
+            }
+            const bool ok = (uint32_t)pk < (uint64_t)a.cache.pages;
+            k_bad = ok ? 0u : 0xFFFFFFFFu;
+            const int64_t ph = (int64_t)(ok ? pk : 0) * hk + head;
+            const int row = (at * kTile + 4 * n) & ((1 << ps) - 1);
+            const uint8_t* c = a.cache.k_codes + ((ph << ps) + row) * (D / 2) + 16 * (D == 64 ? g & 1 : g);
+            const uint8_t* e = a.cache.k_e8m0 + ((ph * (D / 32) + (D == 64 ? g & 1 : g)) << ps) + row;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) ke[k] = *reinterpret_cast<const uint32_t*>(e + ((int64_t)(4 * k) << ps));
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int k = 0; k < KS; ++k) kc[k][u] = *reinterpret_cast<const uint4*>(c + 64 * k + u * (D / 2));
+        };
+        auto load_v = [&](int at) {
+            const int pv = sm_table[(min(at * kTile + 16 * g, last_key) >> ps) - page0];
+            const int64_t ph = (int64_t)((uint32_t)pv < (uint64_t)a.cache.pages ? pv : 0) * hk + head;
+            const int row = (at * kTile + 16 * g) & ((1 << ps) - 1);
+            const uint8_t* c = a.cache.v_codes + ((ph << ps) + row) * (D / 2) + n * (D / 32);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) vc[k] = *reinterpret_cast<const VT*>(c + k * (D / 2));
+        };
+        // tiles whose entries are in LDS together
+        const int chunk = 16 << ps;
+        int c_end = min(t_end, first + t0 + chunk);
+        if (first + t0 < t_end) fill_table(first + t0, c_end);
+
+        // ---- queries: every wave finds its rows' powers, and converts its share ----
+        float mult[NT], up[NT];
         int hi[NT], lo[NT];
         const bool vec = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_st) | (uintptr_t)(2 * a.q_sh)) & 15) == 0;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        auto q_row = [&](int nt) {
             const int row = min(nt * 16 + n, rows - 1);
             const int tok = row / a.group, h = row - tok * a.group;
             hi[nt] = key_hi(a, s, tok);
             lo[nt] = key_lo(a, s, tok);
-            const uint16_t* src = a.q + (int64_t)(s.q0 + tok) * a.q_st + (int64_t)(head * a.group + h) * a.q_sh;
-            constexpr int C = D / 64;               // runs of 16 values per lane
-            float x[C][16];
+            return a.q + (int64_t)(s.q0 + tok) * a.q_st + (int64_t)(head * a.group + h) * a.q_sh + 16 * g;
+        };
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint16_t* src = q_row(nt);
             uint32_t most = 0;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                load_q16<PC == 3>(src + 64 * c + 16 * g, vec, x[c]);
+                float x[16];
+                load_q16<PC == 3>(src + 64 * c, vec, x);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) most = max(most, __float_as_uint(x[c][j]) & 0x7FFFFFFFu);
+                for (int j = 0; j < 16; ++j) most = max(most, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+            }
+            if (nt == 0) {
+                __syncthreads();
+                if (t < c_end) {                    // the first tile's loads run meanwhile
+                    load_k(t);
+                    load_v(t);
+                }
             }
             most = max(most, (uint32_t)__shfl_xor((int)most, 16));
             most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-            const float up = row_power(most, a.scale, &mult[nt]);
+            up[nt] = row_power(most, a.scale, &mult[nt]);
+        }
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (((nt * C + c) & 3) != wave) continue;
+                float x[16];
+                load_q16<PC == 3>(q_row(nt) + 64 * c, vec, x);
+                uint32_t w[PC][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float y[4];
-                    uint32_t w[PC];
+                    uint32_t v[PC];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = up != 0.0f ? x[c][4 * j + i] * up : 0.0f;
-                    pieces4<PC>(y, w);
-                    if constexpr (D >= 128) {
-                        // run c: bytes 0-15 (d = 128 s + 16 g ..) or 16-31 (128 s + 64 + 16 g ..)
+                    for (int i = 0; i < 4; ++i) y[i] = up[nt] != 0.0f ? x[4 * j + i] * up[nt] : 0.0f;
+                    pieces4<PC>(y, v);
 #pragma unroll
-                        for (int p = 0; p < PC; ++p) qf[nt][c >> 1][p][4 * (c & 1) + j] = (int)w[p];
-                    } else {
-                        // k < 64: the first piece, k >= 64: the second; then the third alone
-                        qf[nt][0][0][j] = (int)w[0];
-                        qf[nt][0][0][4 + j] = (int)w[1];
-                        if constexpr (PC == 3) {
-                            qf[nt][0][1][j] = (int)w[2];
-                            qf[nt][0][1][4 + j] = 0;
-                        }
+                    for (int p = 0; p < PC; ++p) w[p][j] = v[p];
+                }
+                auto put = [&](int k, int p, int half, const uint32_t* v) {
+                    sm_q[(((nt * KS + k) * QP + p) * 2 + half) * 64 + lane] = make_uint4(v[0], v[1], v[2], v[3]);
+                };
+                if constexpr (D >= 128) {
+                    // run c: bytes 0-15 (d = 128 k + 16 g ..) or 16-31 (128 k + 64 + 16 g ..)
+#pragma unroll
+                    for (int p = 0; p < PC; ++p) put(c >> 1, p, c & 1, w[p]);
+                } else {
+                    // k < 64: the first piece, k >= 64: the second; then the third alone
+                    put(0, 0, 0, w[0]);
+                    put(0, 0, 1, w[1]);
+                    if constexpr (PC == 3) {
+                        const uint32_t zero[4] = {0, 0, 0, 0};
+                        put(0, 1, 0, w[2]);
+                        put(0, 1, 1, zero);
                     }
                 }
-        }
+            }
 
         v4f o[NT][DT];
         float m[NT], mu[NT], l[NT];
@@ -332,62 +494,34 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
 #pragma unroll
             for (int j = 0; j < DT; ++j) o[nt][j] = v4f{0, 0, 0, 0};
         }
+        __syncthreads();
 
         // ---- keys ----
-        uint4 kc[KS][4];
-        uint32_t ke[KS];
-        VT vc[16];
-        uint4 ve;
-        const int last_key = s.ctx - 1;             // ctx >= 1 wherever it is used
-        int pk = 0, pv = 0;                         // block-table entries of the next tile
-        // the page of a lane's four keys, and of its sixteen values; keys past the
-        // context take the last one's (they are masked)
-        auto load_pages = [&](int t) {
-            pk = table[min(t * kTile + 4 * n, last_key) >> ps];
-            pv = table[min(t * kTile + 16 * g, last_key) >> ps];
-        };
-        auto load_k = [&](int t) {
-            const bool ok = (uint32_t)pk < (uint64_t)a.cache.pages;
-            const int64_t ph = (int64_t)(ok ? pk : 0) * hk + head;
-            const int row = (t * kTile + 4 * n) & ((1 << ps) - 1);
-            const uint8_t* c = a.cache.k_codes + ((ph << ps) + row) * (D / 2) + 16 * (D == 64 ? g & 1 : g);
-            const uint8_t* e = a.cache.k_e8m0 + ((ph * (D / 32) + (D == 64 ? g & 1 : g)) << ps) + row;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) kc[k][u] = *reinterpret_cast<const uint4*>(c + 64 * k + u * (D / 2));
-                ke[k] = *reinterpret_cast<const uint32_t*>(e + ((int64_t)(4 * k) << ps));
-                if (!ok) ke[k] = 0xFFFFFFFFu;
-            }
-        };
-        auto load_v = [&](int t) {
-            const bool ok = (uint32_t)pv < (uint64_t)a.cache.pages;
-            const int64_t ph = (int64_t)(ok ? pv : 0) * hk + head;
-            const int row = (t * kTile + 16 * g) & ((1 << ps) - 1);
-            const uint8_t* c = a.cache.v_codes + ((ph << ps) + row) * (D / 2) + n * (D / 32);
-            const uint8_t* e = a.cache.v_e8m0 + ((ph * (D / 32) + n / (512 / D)) << ps) + row;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) vc[k] = *reinterpret_cast<const VT*>(c + k * (D / 2));
-            ve = *reinterpret_cast<const uint4*>(e);
-        };
-
-        const int t_end = first + t0 + cnt;
-        int t = first + t0 + wave;
-        const bool any = s.ctx > 0;
         // every row sees all keys of [all_lo, all_hi)
         const int all_hi = a.causal ? s.ctx - s.q_all + 1 : s.ctx;
         const int all_lo = key_lo(a, s, s.qlen - 1);
-        if (any && t < t_end) {
-            load_pages(t);
-            load_k(t);
-            load_v(t);
-            if (t + 4 < t_end) load_pages(t + 4);
-        }
-        for (; any && t < t_end; t += 4) {
-            const bool more = t + 4 < t_end;
-            float sc[NT][4][4];                     // [tile u][i]: key 16 g + 4 i + u
+        auto step = [&](auto MORE) {                // tile t; the wave's next one is in LDS's table
+            constexpr bool more = decltype(MORE)::value;
+            const int key0 = t * kTile;
+            const bool masked = key0 + kTile > all_hi || key0 < all_lo;
+            uint4 ve = ve_next;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) ke[k] |= k_bad;
+            // value blocks that count as NaN are rare, so found for the wave at once; then over
+            // the head's blocks, the 16 lanes of g
+            uint32_t bad[4] = {bad_bytes(ve.x), bad_bytes(ve.y), bad_bytes(ve.z), bad_bytes(ve.w)};
+            const bool any_bad = __any((bad[0] | bad[1] | bad[2] | bad[3]) != 0);
+            if (any_bad) {
+                ve.x &= ~bad[0], ve.y &= ~bad[1], ve.z &= ~bad[2], ve.w &= ~bad[3];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int off = 1; off < 16; off <<= 1) bad[i] |= (uint32_t)__shfl_xor((int)bad[i], off);
+            }
+            uint32_t pf[NT][2][4], pl[NT][2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                // ---- scores [tile u][i]: key 16 g + 4 i + u ----
                 v4f acc[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) acc[u] = v4f{0, 0, 0, 0};
@@ -397,64 +531,48 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
                     for (int p = 0; p < QP; ++p) {
                         // D = 64: k >= 64 holds the next piece, its scale comes from lanes g = 2, 3
                         const int qs = D == 64 ? (p ? 119 : g < 2 ? 127 : 123) : 127 - 4 * p;
+                        const uint4* qp = sm_q + ((nt * KS + k) * QP + p) * 128 + lane;
+                        const uint4 q0 = qp[0], q1 = qp[64];
+                        const v8i qf = {(int)q0.x, (int)q0.y, (int)q0.z, (int)q0.w, (int)q1.x, (int)q1.y, (int)q1.z, (int)q1.w};
                         auto dot = [&](auto U) {
                             constexpr int u = decltype(U)::value;
                             const v8i kf = {(int)kc[k][u].x, (int)kc[k][u].y, (int)kc[k][u].z, (int)kc[k][u].w, 0, 0, 0, 0};
-                            acc[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, qf[nt][k][p], acc[u], kFmtFp4,
-                                                                                      kFmtFp8, u, (int)ke[k], 0, qs);
+                            acc[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, qf, acc[u], kFmtFp4, kFmtFp8, u,
+                                                                                      (int)ke[k], 0, qs);
                         };
                         dot(std::integral_constant<int, 0>{});
                         dot(std::integral_constant<int, 1>{});
                         dot(std::integral_constant<int, 2>{});
                         dot(std::integral_constant<int, 3>{});
                     }
+                __builtin_amdgcn_sched_barrier(0);
+                if (nt == NT - 1 && more) load_k(t + 4);
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[nt][u][i] = acc[u][i] * mult[nt];
-            }
-            if (more) load_k(t + 4);
-
-            // value blocks that count as NaN: rare, so found for the wave at once
-            const uint32_t bad[4] = {bad_bytes(ve.x), bad_bytes(ve.y), bad_bytes(ve.z), bad_bytes(ve.w)};
-            if (__any((bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
-                uint32_t b[4];
+                    for (int i = 0; i < 4; ++i) acc[u][i] *= mult[nt];
+                if (any_bad) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {       // over the head's blocks: the 16 lanes of g
-                    b[i] = bad[i];
+                    for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int off = 1; off < 16; off <<= 1) b[i] |= (uint32_t)__shfl_xor((int)b[i], off);
+                        for (int i = 0; i < 4; ++i)
+                            if ((bad[i] >> (8 * u)) & 1u) acc[u][i] = __builtin_nanf("");
                 }
-                ve.x &= ~bad[0], ve.y &= ~bad[1], ve.z &= ~bad[2], ve.w &= ~bad[3];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if ((b[i] >> (8 * u)) & 1u) sc[nt][u][i] = __builtin_nanf("");
-            }
-            const int key0 = t * kTile;
-            if (key0 + kTile > all_hi || key0 < all_lo) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                if (masked) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int key = key0 + 16 * g + 4 * i + u;
-                            if (key >= hi[nt] || key < lo[nt]) sc[nt][u][i] = neg_inf();
+                            if (key >= hi[nt] || key < lo[nt]) acc[u][i] = neg_inf();
                         }
-            }
-            // ---- running maximum, probabilities ----
-            uint32_t pf[NT][2][4], pl[NT][2][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+                }
+                // ---- running maximum, probabilities ----
                 float mx = neg_inf();
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[nt][u][i]);
+                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, acc[u][i]);
                 if (__any(mx > m[nt] + kLazy)) {
                     mx = fmaxf(mx, __shfl_xor(mx, 16));
                     mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -474,13 +592,14 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
                     float p[8];                     // slots: tile 2 st (i = 0..3), tile 2 st + 1
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        p[e] = __builtin_amdgcn_exp2f(sc[nt][2 * st + e / 4][e % 4] - mu[nt]);
+                        p[e] = __builtin_amdgcn_exp2f(acc[2 * st + e / 4][e % 4] - mu[nt]);
                         l[nt] += p[e];
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) pack_p<PC>(p + 2 * e, &pf[nt][st][e], &pl[nt][st][e]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
             // ---- values ----
             const uint32_t vs[4] = {ve.x, ve.y, ve.z, ve.w};
 #pragma unroll
@@ -513,6 +632,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
                                     av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pl[nt][st])), o[nt][j], 0, 0, 0);
                         }
                     }
+                    __builtin_amdgcn_sched_barrier(0);   // one pair's words at a time, or they fill the registers
                 };
 #pragma unroll
                 for (int word = 0; word < VWord<D>::N; ++word) {
@@ -525,7 +645,23 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
                 }
             }
             if (more) load_v(t + 4);
-            if (t + 8 < t_end) load_pages(t + 8);
+        };
+        while (true) {
+            if (t < c_end) {
+                for (; t + 4 < c_end; t += 4) step(std::true_type{});
+                step(std::false_type{});
+                t += 4;
+            }
+            if (c_end >= t_end) break;
+            __syncthreads();                        // the next tiles' entries
+            const int c0 = c_end;
+            c_end = min(t_end, c0 + chunk);
+            fill_table(c0, c_end);
+            __syncthreads();
+            if (t < c_end) {
+                load_k(t);
+                load_v(t);
+            }
         }
 
         // ---- the four waves' results ----
@@ -560,56 +696,80 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < DT; ++j) sm_o[wave - half][nt * DT + j][lane] = o[nt][j];
+                    for (int j = 0; j < DT; ++j) sm_o[((wave - half) * NT * DT + nt * DT + j) * 64 + lane] = o[nt][j];
             }
             __syncthreads();
             if (wave < half) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < DT; ++j) o[nt][j] += sm_o[wave][nt * DT + j][lane];
+                    for (int j = 0; j < DT; ++j) o[nt][j] += sm_o[(wave * NT * DT + nt * DT + j) * 64 + lane];
             }
             __syncthreads();
         }
+        const bool whole = cnt == r.tiles;
+        auto out_row = [&](int row) {
+            const int tok = row / a.group, h = row - tok * a.group;
+            return a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
+        };
+        constexpr uint32_t kPart = (uint32_t)(4 * part_floats(R, D));
+        const __amdgpu_buffer_rsrc_t ws = sk_rsrc(parts);
+        const uint32_t mine = (2u * blockIdx.x + (t0 == 0 ? 1u : 0u)) * kPart;
         if (wave == 0) {
-            const bool whole = cnt == tiles;
-            // partial results: slot 0 of a workgroup continues a segment, slot 1 begins one
-            float* part = reinterpret_cast<float*>(a.ws) + (2 * (int64_t)blockIdx.x + (t0 == 0 ? 1 : 0)) * part_floats(NT * 16, D);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int row = nt * 16 + n;
                 if (row >= rows) continue;
                 if (whole) {
-                    const int tok = row / a.group, h = row - tok * a.group;
-                    uint16_t* dst = a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
+                    uint16_t* dst = out_row(row);
                     const float inv = lt[nt] == 0.0f ? 0.0f : 1.0f / lt[nt];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < DT; j += 2)
-                            *reinterpret_cast<uint32_t*>(dst + DT * (4 * g + i) + j) =
-                                out_pair<PC == 3>(o[nt][j][i] * inv, o[nt][j + 1][i] * inv);
+                        for (int j = 0; j < DT; j += 4)
+                            *reinterpret_cast<uint2*>(dst + DT * (4 * g + i) + j) =
+                                make_uint2(out_pair<PC == 3>(o[nt][j][i] * inv, o[nt][j + 1][i] * inv),
+                                           out_pair<PC == 3>(o[nt][j + 2][i] * inv, o[nt][j + 3][i] * inv));
                 } else {
-                    float* dst = part + (int64_t)row * D;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int j = 0; j < DT; j += 4)
-                            *reinterpret_cast<v4f*>(dst + DT * (4 * g + i) + j) =
-                                v4f{o[nt][j][i], o[nt][j + 1][i], o[nt][j + 2][i], o[nt][j + 3][i]};
+                            sk_put4(ws, mine + 4u * (uint32_t)(row * D + DT * (4 * g + i) + j), o[nt][j][i], o[nt][j + 1][i],
+                                    o[nt][j + 2][i], o[nt][j + 3][i]);
                     if (g == 0) {
-                        part[(int64_t)NT * 16 * D + row] = mt[nt];
-                        part[(int64_t)NT * 16 * (D + 1) + row] = lt[nt];
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(mt[nt]), ws, (int)(mine + 4u * (uint32_t)(R * D + row)), 0, 16);
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(lt[nt]), ws, (int)(mine + 4u * (uint32_t)(R * D + R + row)), 0, 16);
                     }
                 }
             }
         }
-        pos += cnt;
-        if (pos < end && t0 + cnt == tiles && head == hk - 1) {
-            start += tiles * hk;
-            for (tiles = 0; tiles == 0;) {
-                if (++sq >= a.seqs) return;
-                tiles = tiles_of(a, sq);
+        if (!whole) {
+            const int g0 = r.start + head * r.tiles, w0 = g0 / r.run;
+            int pieces = (g0 + r.tiles - 1) / r.run - w0 + 1, mine_at = (int)blockIdx.x - w0, step = 1;
+            for (int level = 0; pieces > 1; ++level) {
+                const int lead = mine_at / kJoin * kJoin;           // in this level's pieces
+                const int count = min(kJoin, pieces - lead);
+                // the j-th piece's slot: its first run's
+                auto id = [&](int j) {
+                    const int p = (lead + j) * step;
+                    return 2u * (uint32_t)(w0 + p) + (p == 0 ? 1u : 0u);
+                };
+                if (!sk_arrive(counters + (int64_t)level * 2 * workgroups + id(0), count, &sm_flag)) break;
+                const bool final = pieces <= kJoin;
+                join_pieces<D, R, PC == 3>(ws, [&](int j) { return id(j) * kPart; }, count, rows, final, out_row, sm_j);
+                pieces = (pieces + kJoin - 1) / kJoin;
+                mine_at /= kJoin;
+                step *= kJoin;
+            }
+            __syncthreads();
+        }
+        r.pos += cnt;
+        if (r.pos < r.end && t0 + cnt == r.tiles && head == hk - 1) {
+            r.start += r.tiles * hk;
+            for (r.tiles = 0; r.tiles == 0;) {
+                if (++r.seq >= a.seqs) return;
+                r.tiles = tiles_of(a, r.seq);
             }
         }
     }
@@ -654,32 +814,6 @@ __device__ __forceinline__ void join_row(int pieces, int rows, int row, uint16_t
             dst[at] = (uint16_t)out_pair<FP16>(v, v);
         }
     }
-}
-
-// one workgroup per segment (sequence and head) and row
-template <int D, bool FP16>
-__global__ __launch_bounds__(256) void decode_join_kernel(const AttnArgs a, const int workgroups, const int nt16) {
-    const uint32_t pair = blockIdx.x / (uint32_t)(a.max_q * a.group);
-    const int row = (int)(blockIdx.x - pair * (uint32_t)(a.max_q * a.group));
-    const int sq = pair / a.cache.kv_heads, head = pair - sq * a.cache.kv_heads;
-    const Seq s = seq_of(a, sq);
-    if (row >= s.qlen * a.group) return;
-    const Line line = line_of(a, workgroups);
-    // the segment's place in the line
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int i = lane; i < sq; i += 64) before += tiles_of(a, i);
-#pragma unroll
-    for (int off = 32; off; off >>= 1) before += __shfl_xor(before, off);
-    const int tiles = tiles_of(a, sq);
-    const int g0 = before * a.cache.kv_heads + head * tiles, g1 = g0 + tiles;
-    const int w0 = g0 / line.run, w1 = (g1 - 1) / line.run;
-    if (w0 == w1) return;   // written whole
-    const int tok = row / a.group, h = row - tok * a.group;
-    uint16_t* dst = a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
-    const float* ws = reinterpret_cast<const float*>(a.ws);
-    const int64_t size = part_floats(nt16, D);
-    join_row<D, FP16>(w1 - w0 + 1, nt16, row, dst, [&](int i) { return ws + (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * size; });
 }
 
 // ===========================================================================
@@ -981,7 +1115,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
                     make_uint2(out_pair<PC == 3>(o[j][4 * i] * inv, o[j][4 * i + 1] * inv),
                                out_pair<PC == 3>(o[j][4 * i + 2] * inv, o[j][4 * i + 3] * inv));
     } else {
-        float* p = reinterpret_cast<float*>(a.ws) +
+        float* p = reinterpret_cast<float*>(a.ws) + a.ws_skip +
                    (((int64_t)pair * tiles_max + tile) * ks + part) * part_floats(32 * NW, D);
         const int r = 32 * wave + n;
 #pragma unroll
@@ -1007,7 +1141,7 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(const AttnArgs a, con
     const int tile = row / tile_rows;
     const int tok = row / a.group, h = row - tok * a.group;
     uint16_t* dst = a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
-    const float* ws = reinterpret_cast<const float*>(a.ws);
+    const float* ws = reinterpret_cast<const float*>(a.ws) + a.ws_skip;
     const int64_t size = part_floats(tile_rows, D);
     join_row<D, FP16>(ks, tile_rows, row - tile * tile_rows, dst,
                       [&](int i) { return ws + (((int64_t)pair * tiles_max + tile) * ks + i) * size; });
@@ -1058,14 +1192,10 @@ hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
     hipError_t e;
     const dim3 join((unsigned)((int64_t)a.seqs * a.cache.kv_heads * a.max_q * a.group));
     if (p.decode) {
-        if (p.nt == 1) e = go_decode<D, 1>(a, p, fp16, st);
-        else if (p.nt == 2) e = go_decode<D, 2>(a, p, fp16, st);
-        else if constexpr (D < 256) e = go_decode<D, 4>(a, p, fp16, st);
-        else e = hipErrorInvalidValue;
-        if (e != hipSuccess) return e;
-        if (fp16) decode_join_kernel<D, true><<<join, 256, 0, st>>>(a, p.workgroups, 16 * p.nt);
-        else decode_join_kernel<D, false><<<join, 256, 0, st>>>(a, p.workgroups, 16 * p.nt);
-        return hipGetLastError();
+        if (p.nt == 1) return go_decode<D, 1>(a, p, fp16, st);
+        if (p.nt == 2) return go_decode<D, 2>(a, p, fp16, st);
+        if constexpr (D < 256) return go_decode<D, 4>(a, p, fp16, st);
+        return hipErrorInvalidValue;
     }
     const dim3 grid((unsigned)((int64_t)a.seqs * a.cache.kv_heads * p.tiles * p.ks));
     if (fp16) prefill_kernel<D, 3, D == 256 ? 4 : 8><<<grid, 64 * p.nw, 0, st>>>(a, p.tiles, p.ks);
@@ -1079,9 +1209,10 @@ hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
 
 }  // namespace
 
-// Enough for every call of at most these sizes: fewer queries take the decode
-// kernel (two partial results per run), fewer row tiles are split over the keys
-// (at most one partial result per CU).
+// The joins' counters, then enough for every call of at most these sizes: fewer
+// queries take the decode kernel (two partial results per run), fewer row tiles
+// are split over the keys (at most one partial result per CU).
+size_t attention_counter_bytes() { return (size_t)(4 * counter_words(decode_workgroups())); }
 size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, int D) {
     const int64_t rows = max_q * (hq / hk), most = decode_rows(D);
     int64_t floats = 2 * (int64_t)decode_workgroups() * part_floats(16 * decode_tiles(rows < most ? rows : most), D);
@@ -1089,10 +1220,12 @@ size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, in
         const int64_t split = (int64_t)device_cus() * part_floats(32 * prefill_waves(D, false), D);
         if (split > floats) floats = split;
     }
-    return (size_t)floats * 4;
+    return attention_counter_bytes() + (size_t)floats * 4;
 }
 
-hipError_t launch_attention(const AttnArgs& a, bool fp16, hipStream_t stream) {
+hipError_t launch_attention(const AttnArgs& args, bool fp16, hipStream_t stream) {
+    AttnArgs a = args;
+    a.ws_skip = (int64_t)attention_counter_bytes() / 4;
     const Plan p = plan_attention(a.seqs, a.max_q, a.hq, a.cache.kv_heads, a.cache.head_dim, fp16);
     switch (a.cache.head_dim) {
         case 64: return go_dim<64>(a, p, fp16, stream);

@@ -144,6 +144,8 @@ size_t w4a8_attention_workspace_bytes(int64_t seqs, int64_t max_q, int q_heads, 
     return attention_workspace_bytes(seqs, max_q, q_heads, kv_heads, head_dim);
 }
 
+size_t w4a8_attention_counter_bytes(void) { return attention_counter_bytes(); }
+
 w4a8_status w4a8_attention_mxfp4(const w4a8_kv_cache* cache, w4a8_float type, const uint16_t* d_q,
                                  int64_t q_stride_token, int64_t q_stride_head, int q_heads, int64_t tokens,
                                  int64_t seqs, const int32_t* d_cu_q, int64_t max_q, const int32_t* d_block_table,

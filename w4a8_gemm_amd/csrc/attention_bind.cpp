@@ -347,6 +347,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
     } else {
         const size_t need = w4a8_attention_workspace_bytes(seqs, max_q, q.n, view.kv_heads, view.head_dim);
         ws = at::empty({(int64_t)need}, qt.options().dtype(at::kByte));
+        check(w4a8_workspace_init(ws.data_ptr(), w4a8_attention_counter_bytes(), stream(c.dev)), "w4a8_workspace_init");
     }
     check(w4a8_attention_mxfp4(&view, type, q.p, q.st, q.sh, q.n, tokens, seqs, cu, max_q, table.const_data_ptr<int32_t>(),
                                seqs > 1 ? table.stride(0) : width, width, ct.const_data_ptr<int32_t>(), (float)scale, causal,

@@ -224,7 +224,9 @@ struct AttnArgs {
     float scale;
     int causal, window;                 // window 0: none
     uint8_t* ws;
+    int64_t ws_skip;                    // floats of the counters at its start (set by the launcher)
 };
+size_t attention_counter_bytes();
 size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, int head_dim);
 hipError_t launch_attention(const AttnArgs& a, bool fp16, hipStream_t stream);
 int device_cus();   // CUs of the current device (cached per device)
