@@ -95,19 +95,29 @@ __device__ __forceinline__ void pieces4(const float* x, uint32_t* out) {
     }
 }
 
-// sixteen 16-bit query values from p
+// Sixteen 16-bit query values from p, in 8 dwords: 16-byte loads at any 2-byte
+// alignment (strided views of a fused projection may start anywhere).
+struct __attribute__((packed, aligned(2))) Half8 {
+    uint32_t d[4];
+};
+__device__ __forceinline__ void load_q16(const uint16_t* p, uint32_t* d) {
+    const Half8 u = reinterpret_cast<const Half8*>(p)[0], v = reinterpret_cast<const Half8*>(p)[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = u.d[j], d[4 + j] = v.d[j];
+}
+// the largest magnitude among 8 dwords of values, as fp32 bits
 template <bool FP16>
-__device__ __forceinline__ void load_q16(const uint16_t* p, bool vec, float* x) {
-    uint32_t d[8];
-    if (vec) {
-        const uint4 u = reinterpret_cast<const uint4*>(p)[0], v = reinterpret_cast<const uint4*>(p)[1];
-        d[0] = u.x, d[1] = u.y, d[2] = u.z, d[3] = u.w, d[4] = v.x, d[5] = v.y, d[6] = v.z, d[7] = v.w;
-    } else {
+__device__ __forceinline__ uint32_t most_of(const uint32_t* d, uint32_t most) {
+    uint32_t m = 0;   // 16-bit patterns order like the magnitudes, NaN above infinity
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = (uint32_t)p[2 * j] | ((uint32_t)p[2 * j + 1] << 16);
-    }
+    for (int j = 0; j < 8; ++j) m = max(m, max(d[j] & 0x7FFFu, (d[j] >> 16) & 0x7FFFu));
+    if (FP16 && m >= 0x7C00u) return 0x7F800000u;
+    return max(most, FP16 ? __float_as_uint(f16_to_f32(m)) : m << 16);
+}
+template <bool FP16>
+__device__ __forceinline__ void widen4(const uint32_t* d, float* x) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 2; ++j) {
         x[2 * j] = FP16 ? f16_to_f32(d[j] & 0xFFFFu) : bf16_to_f32(d[j] & 0xFFFFu);
         x[2 * j + 1] = FP16 ? f16_to_f32(d[j] >> 16) : bf16_to_f32(d[j] >> 16);
     }
@@ -194,12 +204,19 @@ __device__ __forceinline__ uint32_t vword(uint16_t v, int) { return v; }
 __device__ __forceinline__ uint32_t vword(uint32_t v, int) { return v; }
 __device__ __forceinline__ uint32_t vword(uint2 v, int i) { return i ? v.y : v.x; }
 
-// tiles of a sequence: at least one while it has queries, so that rows without
-// a key are written
+// Tiles of a sequence: at least one while it has queries, so that rows without
+// a key are written.  Its place on the line is longer by what a segment costs
+// beside its tiles (queries in, results out: about the time of kSegment tiles),
+// in whole steps of the four waves: short segments then get workgroups of their
+// own, and a run through several of them takes no longer than the others.
+constexpr int kSegment = 8;
 __device__ __forceinline__ int first_tile(const AttnArgs& a, const Seq& s) { return key_lo(a, s, 0) / kTile; }
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, int s) {
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, const Seq& q) {
+    return max(1, (q.ctx + kTile - 1) / kTile - first_tile(a, q));
+}
+__device__ __forceinline__ int place_of(const AttnArgs& a, int s) {
     const Seq q = seq_of(a, s);
-    return q.qlen ? max(1, (q.ctx + kTile - 1) / kTile - first_tile(a, q)) : 0;
+    return q.qlen ? (tiles_of(a, q) + kSegment + 3) & ~3 : 0;
 }
 __device__ __forceinline__ int wave_scan(int v) {   // inclusive
     const int lane = threadIdx.x & 63;
@@ -212,20 +229,20 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive
 }
 
 // A workgroup's run [pos, end) of the line, and the sequence that holds its
-// start: first position and tiles per head.
+// start: first position and length per head.
 struct Run {
     int total, run;          // of the line; per workgroup
     int pos, end;
-    int seq, start, tiles;
+    int seq, start, place;
 };
 __device__ __forceinline__ Run run_of(const AttnArgs& a, int workgroups) {
     const int lane = threadIdx.x & 63, hk = a.cache.kv_heads;
     Run r;
-    int n = lane < a.seqs ? tiles_of(a, lane) : 0;
+    int n = lane < a.seqs ? place_of(a, lane) : 0;
     int incl = wave_scan(n);
     const int64_t head = (int64_t)__shfl(incl, 63);
     int64_t t = head;
-    for (int s0 = 64; s0 < a.seqs; s0 += 64) t += __shfl(wave_scan(s0 + lane < a.seqs ? tiles_of(a, s0 + lane) : 0), 63);
+    for (int s0 = 64; s0 < a.seqs; s0 += 64) t += __shfl(wave_scan(s0 + lane < a.seqs ? place_of(a, s0 + lane) : 0), 63);
     const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     r.total = uniform((int)t * hk);
     r.run = uniform(max((r.total + workgroups - 1) / workgroups, 4));   // a tile for every wave
@@ -233,12 +250,12 @@ __device__ __forceinline__ Run run_of(const AttnArgs& a, int workgroups) {
     r.pos = (int)min(pos, (int64_t)r.total);
     r.end = min(r.pos + r.run, r.total);
     r.seq = a.seqs;
-    r.start = r.tiles = 0;
+    r.start = r.place = 0;
     if (r.pos >= r.total) return r;
     int base = 0;
     for (int s0 = 0; s0 < a.seqs; s0 += 64) {
         if (s0) {
-            n = s0 + lane < a.seqs ? tiles_of(a, s0 + lane) : 0;
+            n = s0 + lane < a.seqs ? place_of(a, s0 + lane) : 0;
             incl = wave_scan(n);
         }
         const int first = base + (incl - n) * hk;
@@ -247,7 +264,7 @@ __device__ __forceinline__ Run run_of(const AttnArgs& a, int workgroups) {
             const int l = __ffsll((unsigned long long)hit) - 1;
             r.seq = s0 + l;
             r.start = uniform(__shfl(first, l));
-            r.tiles = uniform(__shfl(n, l));
+            r.place = uniform(__shfl(n, l));
             break;
         }
         base += uniform(__shfl(incl, 63)) * hk;
@@ -259,79 +276,84 @@ __device__ __forceinline__ Run run_of(const AttnArgs& a, int workgroups) {
 //
 // Piece i of a segment belongs to workgroup w0 + i; its result (rows x D
 // unnormalized outputs, the rows' maxima, their sums) lies in slot 2 w + 1 of
-// the workspace where the segment begins in that run, else in slot 2 w.  Eight
-// pieces are joined by the last of the eight to arrive, into the first one's
-// slot, eight such results by the last of these, and so on: a segment of 512
-// pieces takes three rounds.  Always in the pieces' order, so the result does
-// not depend on which came last.  Nobody waits: a workgroup that is not last
+// the workspace where the segment begins in that run, else in slot 2 w.  Up to
+// kJoin pieces are joined by the last of them to arrive, more in two rounds of
+// about the root of their number.  Always in the pieces' order, so the result
+// does not depend on which came last.  Nobody waits: a workgroup that is not last
 // goes on.
-constexpr int kJoin = 8, kLevels = 4;   // 8^4 pieces
+constexpr int kJoin = 16;
+constexpr int kJoinMost = 64;           // of one round: two rounds join 4096
 __host__ __device__ constexpr int64_t part_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
-__host__ __device__ constexpr int64_t counter_words(int workgroups) { return (int64_t)kLevels * 2 * workgroups; }
+__host__ __device__ constexpr int64_t counter_words(int workgroups) { return (int64_t)2 * 2 * workgroups; }
+
+__device__ __forceinline__ float ws_get(__amdgpu_buffer_rsrc_t ws, uint32_t at) {
+    return __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, (int)at, 0, 16));
+}
+__device__ __forceinline__ void ws_put(__amdgpu_buffer_rsrc_t ws, uint32_t at, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), ws, (int)at, 0, 16);
+}
 
 // Joins `count` results (the j-th at slot(j)) of `rows` live rows: into slot(0),
-// or normalized into the output.  R = rows of a slot.
+// or normalized into the output.  R = rows of a slot; ml: 2 R kJoinMost floats.
 template <int D, int R, bool FP16, typename SLOT, typename OUT>
 __device__ __forceinline__ void join_pieces(__amdgpu_buffer_rsrc_t ws, SLOT slot, int count, int rows, bool final, OUT out,
-                                            float* sm) {
+                                            float* ml) {
     constexpr int C = D / 4;                // threads per row
     constexpr int RG = 256 / C;
-    float* weight = sm;                     // [kJoin][R]
-    float* inv = sm + kJoin * R;            // [R]
-    const int tid = threadIdx.x;
-    if (tid < rows) {
-        float m[kJoin], l[kJoin], mx = neg_inf(), sum = 0.0f;
-        auto word = [&](int j, int k) {
-            return __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(ws, (int)(slot(j) + 4u * (uint32_t)(R * D + k * R + tid)), 0, 16));
-        };
+    constexpr int B = 8;                    // results in flight
+    const int tid = threadIdx.x, c = tid % C;
+    auto fetch = [&](sk_i32x4* v, int row, int j0) {
 #pragma unroll
-        for (int j = 0; j < kJoin; ++j) {
-            m[j] = j < count ? word(j, 0) : neg_inf();
-            l[j] = j < count ? word(j, 1) : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < kJoin; ++j) mx = fmaxf(mx, m[j]);
-        const float u = mx == neg_inf() ? 0.0f : mx;
-#pragma unroll
-        for (int j = 0; j < kJoin; ++j) {
-            const float w = exp2f(m[j] - u);
-            if (j < count) weight[j * R + tid] = w;
-            sum += l[j] * w;
-        }
-        inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (!final) {
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(mx), ws, (int)(slot(0) + 4u * (uint32_t)(R * D + tid)), 0, 16);
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(sum), ws, (int)(slot(0) + 4u * (uint32_t)(R * D + R + tid)), 0, 16);
-        }
+        for (int j = 0; j < B; ++j)
+            if (j0 + j < count) v[j] = sk_get4(ws, slot(j0 + j) + 4u * (uint32_t)(row * D + 4 * c));
+    };
+    int row = tid / C;
+    sk_i32x4 v[B];
+    if (row < rows) fetch(v, row, 0);
+    for (int i = tid; i < rows * count; i += 256) {
+        const int j = i / rows, r = i - j * rows;
+        ml[j * R + r] = ws_get(ws, slot(j) + 4u * (uint32_t)(R * D + r));
+        ml[(kJoinMost + j) * R + r] = ws_get(ws, slot(j) + 4u * (uint32_t)(R * D + R + r));
     }
     __syncthreads();
-    const int c = tid % C;
-    for (int row = tid / C; row < rows; row += RG) {
-        sk_i32x4 v[kJoin];
-        const uint32_t at = 4u * (uint32_t)(row * D + 4 * c);
+    for (; row < rows; row += RG) {
+        float mx = neg_inf(), sum = 0.0f, acc[4] = {0, 0, 0, 0};
+        for (int j = 0; j < count; ++j) mx = fmaxf(mx, ml[j * R + row]);
+        const float u = mx == neg_inf() ? 0.0f : mx;
+        for (int j0 = 0; j0 < count; j0 += B) {
+            sk_i32x4 x[B];
 #pragma unroll
-        for (int j = 0; j < kJoin; ++j)
-            if (j < count) v[j] = sk_get4(ws, slot(j) + at);
-        float acc[4] = {0, 0, 0, 0};
+            for (int j = 0; j < B; ++j) x[j] = v[j];
+            if (j0 + B < count) fetch(v, row, j0 + B);
+            else if (row + RG < rows) fetch(v, row + RG, 0);
 #pragma unroll
-        for (int j = 0; j < kJoin; ++j)
-            if (j < count) {
-                const float w = weight[j * R + row];
+            for (int j = 0; j < B; ++j)
+                if (j0 + j < count) {
+                    const float w = exp2f(ml[(j0 + j) * R + row] - u);
+                    sum += ml[(kJoinMost + j0 + j) * R + row] * w;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] += __int_as_float(v[j][i]) * w;
-            }
+                    for (int i = 0; i < 4; ++i) acc[i] += __int_as_float(x[j][i]) * w;
+                }
+        }
         if (final) {
-            const float f = inv[row];
+            const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
             *reinterpret_cast<uint2*>(out(row) + 4 * c) =
                 make_uint2(out_pair<FP16>(acc[0] * f, acc[1] * f), out_pair<FP16>(acc[2] * f, acc[3] * f));
         } else {
-            sk_put4(ws, slot(0) + at, acc[0], acc[1], acc[2], acc[3]);
+            sk_put4(ws, slot(0) + 4u * (uint32_t)(row * D + 4 * c), acc[0], acc[1], acc[2], acc[3]);
+            if (c == 0) {
+                ws_put(ws, slot(0) + 4u * (uint32_t)(R * D + row), mx);
+                ws_put(ws, slot(0) + 4u * (uint32_t)(R * D + R + row), sum);
+            }
         }
     }
 }
 
+// waves per SIMD: the outputs of many rows need the registers of two
+constexpr int decode_waves(int D, int NT) { return NT * (D / 16) > 16 ? 1 : 2; }
+
 template <int D, int NT, int PC>
-__global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const int workgroups) {
+__global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const AttnArgs a, const int workgroups) {
     constexpr int KS = D >= 128 ? D / 128 : 1;      // 128-deep products per score
     constexpr int QP = D >= 128 ? PC : PC - 1;      // q operands per 128 (D = 64: pieces side by side)
     constexpr int DT = D / 16;                      // output tiles
@@ -341,28 +363,41 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int hk = a.cache.kv_heads, ps = a.page_shift;
-    // queries while the keys stream, then the waves' results
-    constexpr int kQBytes = NT * KS * QP * 2048, kOBytes = 2 * NT * DT * 1024;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kQBytes > kOBytes ? kQBytes : kOBytes];
-    __shared__ float sm_m[4][R], sm_l[4][R], sm_j[(kJoin + 1) * R];
+    // queries while the keys stream; then the waves' results, rows padded by 16
+    // bytes; then the joined pieces' maxima and sums
+    constexpr int kRow = D + 4;
+    constexpr int kQBytes = NT * KS * QP * 2048, kOBytes = 4 * R * kRow * 4, kMBytes = 2 * R * kJoinMost * 4;
+    constexpr int kBytes = kQBytes > kOBytes ? (kQBytes > kMBytes ? kQBytes : kMBytes) : (kOBytes > kMBytes ? kOBytes : kMBytes);
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kBytes];
+    __shared__ float sm_m[4][R], sm_l[4][R];
     __shared__ uint32_t sm_flag;
     __shared__ int32_t sm_table[16 * kTile + 1];
     uint4* const sm_q = reinterpret_cast<uint4*>(smem);                 // [nt][k][p][half][lane]
-    v4f* const sm_o = reinterpret_cast<v4f*>(smem);                     // [wave][nt][tile][lane]
+    float* const sm_o = reinterpret_cast<float*>(smem);                 // [wave][row][kRow]
     uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws);
-    float* const parts = reinterpret_cast<float*>(a.ws) + counter_words(workgroups);
+    float* const parts = reinterpret_cast<float*>(a.ws) + a.ws_skip;
 
     Run r = run_of(a, workgroups);
     if (r.seq >= a.seqs) return;
 
     while (r.pos < r.end) {
-        const int head = (r.pos - r.start) / r.tiles;
-        const int t0 = (r.pos - r.start) - head * r.tiles;
-        const int cnt = min(r.tiles - t0, r.end - r.pos);
+        const int head = (r.pos - r.start) / r.place;
+        const int t0 = (r.pos - r.start) - head * r.place;
+        const int span = min(r.place - t0, r.end - r.pos);      // on the line
         const Seq s = seq_of(a, r.seq);
+        const int tiles = tiles_of(a, s);
+        const int cnt = min(span, tiles - t0);                  // tiles among it
+        r.pos += span;
+        const int seq = r.seq, start = r.start, r_place = r.place;
+        if (t0 + span == r.place && head == hk - 1) {           // the next sequence with queries
+            r.start += r.place * hk;
+            for (r.place = 0; r.place == 0 && ++r.seq < a.seqs;) r.place = place_of(a, r.seq);
+            if (r.seq >= a.seqs) r.end = r.pos;
+        }
+        if (cnt <= 0) continue;
         const int rows = s.qlen * a.group;
         const int first = first_tile(a, s);
-        const int32_t* table = a.table + (int64_t)r.seq * a.table_stride;
+        const int32_t* table = a.table + (int64_t)seq * a.table_stride;
         const int t_end = s.ctx > 0 ? first + t0 + cnt : 0;
         int t = first + t0 + wave;
 
@@ -415,52 +450,41 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
         if (first + t0 < t_end) fill_table(first + t0, c_end);
 
         // ---- queries: every wave finds its rows' powers, and converts its share ----
-        float mult[NT], up[NT];
+        float mult[NT];
         int hi[NT], lo[NT];
-        const bool vec = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_st) | (uintptr_t)(2 * a.q_sh)) & 15) == 0;
-        auto q_row = [&](int nt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             const int row = min(nt * 16 + n, rows - 1);
             const int tok = row / a.group, h = row - tok * a.group;
             hi[nt] = key_hi(a, s, tok);
             lo[nt] = key_lo(a, s, tok);
-            return a.q + (int64_t)(s.q0 + tok) * a.q_st + (int64_t)(head * a.group + h) * a.q_sh + 16 * g;
-        };
+            const uint16_t* src = a.q + (int64_t)(s.q0 + tok) * a.q_st + (int64_t)(head * a.group + h) * a.q_sh + 16 * g;
+            uint32_t x[C][8], most = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint16_t* src = q_row(nt);
-            uint32_t most = 0;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float x[16];
-                load_q16<PC == 3>(src + 64 * c, vec, x);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) most = max(most, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-            }
+            for (int c = 0; c < C; ++c) load_q16(src + 64 * c, x[c]);
             if (nt == 0) {
-                __syncthreads();
+                __syncthreads();                    // the table; the last segment's results are out
                 if (t < c_end) {                    // the first tile's loads run meanwhile
                     load_k(t);
                     load_v(t);
                 }
             }
+#pragma unroll
+            for (int c = 0; c < C; ++c) most = most_of<PC == 3>(x[c], most);
             most = max(most, (uint32_t)__shfl_xor((int)most, 16));
             most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-            up[nt] = row_power(most, a.scale, &mult[nt]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            const float up = row_power(most, a.scale, &mult[nt]);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 if (((nt * C + c) & 3) != wave) continue;
-                float x[16];
-                load_q16<PC == 3>(q_row(nt) + 64 * c, vec, x);
                 uint32_t w[PC][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float y[4];
                     uint32_t v[PC];
+                    widen4<PC == 3>(x[c] + 2 * j, y);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = up[nt] != 0.0f ? x[4 * j + i] * up[nt] : 0.0f;
+                    for (int i = 0; i < 4; ++i) y[i] = up != 0.0f ? y[i] * up : 0.0f;
                     pieces4<PC>(y, v);
 #pragma unroll
                     for (int p = 0; p < PC; ++p) w[p][j] = v[p];
@@ -483,6 +507,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
                     }
                 }
             }
+        }
 
         v4f o[NT][DT];
         float m[NT], mu[NT], l[NT];
@@ -665,49 +690,27 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
         }
 
         // ---- the four waves' results ----
+        __syncthreads();                            // the queries are read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] += __shfl_xor(l[nt], 16);
             l[nt] += __shfl_xor(l[nt], 32);
-            if (g == 0) {
-                sm_m[wave][nt * 16 + n] = m[nt];
-                sm_l[wave][nt * 16 + n] = l[nt];
+            const int row = nt * 16 + n;
+            if (row < rows) {
+                if (g == 0) {
+                    sm_m[wave][row] = m[nt];
+                    sm_l[wave][row] = l[nt];
+                }
+                float* dst = sm_o + (wave * R + row) * kRow + 4 * DT * g;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < DT; j += 4)
+                        *reinterpret_cast<v4f*>(dst + DT * i + j) = v4f{o[nt][j][i], o[nt][j + 1][i], o[nt][j + 2][i], o[nt][j + 3][i]};
             }
         }
         __syncthreads();
-        float mt[NT], lt[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            mt[nt] = neg_inf();
-#pragma unroll
-            for (int w = 0; w < 4; ++w) mt[nt] = fmaxf(mt[nt], sm_m[w][nt * 16 + n]);
-            const float u = mt[nt] == neg_inf() ? 0.0f : mt[nt];
-            lt[nt] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) lt[nt] += sm_l[w][nt * 16 + n] * exp2f(sm_m[w][nt * 16 + n] - u);
-            const float f = exp2f(m[nt] - u);   // 0 without a key (NaN outputs stay NaN)
-#pragma unroll
-            for (int j = 0; j < DT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[nt][j][i] *= f;
-        }
-        for (int half = 2; half; half >>= 1) {
-            if (wave >= half && wave < 2 * half) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < DT; ++j) sm_o[((wave - half) * NT * DT + nt * DT + j) * 64 + lane] = o[nt][j];
-            }
-            __syncthreads();
-            if (wave < half) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < DT; ++j) o[nt][j] += sm_o[(wave * NT * DT + nt * DT + j) * 64 + lane];
-            }
-            __syncthreads();
-        }
-        const bool whole = cnt == r.tiles;
+        const bool whole = cnt == tiles;
         auto out_row = [&](int row) {
             const int tok = row / a.group, h = row - tok * a.group;
             return a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
@@ -715,62 +718,54 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(const AttnArgs a, const 
         constexpr uint32_t kPart = (uint32_t)(4 * part_floats(R, D));
         const __amdgpu_buffer_rsrc_t ws = sk_rsrc(parts);
         const uint32_t mine = (2u * blockIdx.x + (t0 == 0 ? 1u : 0u)) * kPart;
-        if (wave == 0) {
+        for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+            const int row = i / (D / 4), c = i - row * (D / 4);
+            float mx = neg_inf(), sum = 0.0f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int row = nt * 16 + n;
-                if (row >= rows) continue;
-                if (whole) {
-                    uint16_t* dst = out_row(row);
-                    const float inv = lt[nt] == 0.0f ? 0.0f : 1.0f / lt[nt];
+            for (int w = 0; w < 4; ++w) mx = fmaxf(mx, sm_m[w][row]);
+            const float u = mx == neg_inf() ? 0.0f : mx;
+            v4f acc = {0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < DT; j += 4)
-                            *reinterpret_cast<uint2*>(dst + DT * (4 * g + i) + j) =
-                                make_uint2(out_pair<PC == 3>(o[nt][j][i] * inv, o[nt][j + 1][i] * inv),
-                                           out_pair<PC == 3>(o[nt][j + 2][i] * inv, o[nt][j + 3][i] * inv));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < DT; j += 4)
-                            sk_put4(ws, mine + 4u * (uint32_t)(row * D + DT * (4 * g + i) + j), o[nt][j][i], o[nt][j + 1][i],
-                                    o[nt][j + 2][i], o[nt][j + 3][i]);
-                    if (g == 0) {
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(mt[nt]), ws, (int)(mine + 4u * (uint32_t)(R * D + row)), 0, 16);
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(lt[nt]), ws, (int)(mine + 4u * (uint32_t)(R * D + R + row)), 0, 16);
-                    }
+            for (int w = 0; w < 4; ++w) {
+                const float f = exp2f(sm_m[w][row] - u);    // 0 without a key (NaN outputs stay NaN)
+                sum += sm_l[w][row] * f;
+                acc += *reinterpret_cast<const v4f*>(sm_o + (w * R + row) * kRow + 4 * c) * f;
+            }
+            if (whole) {
+                const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+                *reinterpret_cast<uint2*>(out_row(row) + 4 * c) =
+                    make_uint2(out_pair<PC == 3>(acc[0] * f, acc[1] * f), out_pair<PC == 3>(acc[2] * f, acc[3] * f));
+            } else {
+                sk_put4(ws, mine + 4u * (uint32_t)(row * D + 4 * c), acc[0], acc[1], acc[2], acc[3]);
+                if (c == 0) {
+                    ws_put(ws, mine + 4u * (uint32_t)(R * D + row), mx);
+                    ws_put(ws, mine + 4u * (uint32_t)(R * D + R + row), sum);
                 }
             }
         }
         if (!whole) {
-            const int g0 = r.start + head * r.tiles, w0 = g0 / r.run;
-            int pieces = (g0 + r.tiles - 1) / r.run - w0 + 1, mine_at = (int)blockIdx.x - w0, step = 1;
+            const int g0 = start + head * r_place, w0 = g0 / r.run;
+            int pieces = (g0 + tiles - 1) / r.run - w0 + 1, at = (int)blockIdx.x - w0, step = 1;
+            int fan = pieces;
+            if (pieces > kJoin)
+                for (fan = kJoin / 2; fan * fan < pieces;) ++fan;
             for (int level = 0; pieces > 1; ++level) {
-                const int lead = mine_at / kJoin * kJoin;           // in this level's pieces
-                const int count = min(kJoin, pieces - lead);
-                // the j-th piece's slot: its first run's
+                const int lead = at / fan * fan;            // among this round's
+                const int count = min(fan, pieces - lead);
+                // the j-th result's slot: its first run's
                 auto id = [&](int j) {
                     const int p = (lead + j) * step;
                     return 2u * (uint32_t)(w0 + p) + (p == 0 ? 1u : 0u);
                 };
                 if (!sk_arrive(counters + (int64_t)level * 2 * workgroups + id(0), count, &sm_flag)) break;
-                const bool final = pieces <= kJoin;
-                join_pieces<D, R, PC == 3>(ws, [&](int j) { return id(j) * kPart; }, count, rows, final, out_row, sm_j);
-                pieces = (pieces + kJoin - 1) / kJoin;
-                mine_at /= kJoin;
-                step *= kJoin;
+                const bool final = pieces <= fan;
+                join_pieces<D, R, PC == 3>(ws, [&](int j) { return id(j) * kPart; }, count, rows, final, out_row,
+                                           reinterpret_cast<float*>(smem));
+                pieces = (pieces + fan - 1) / fan;
+                at /= fan;
+                step *= fan;
             }
-            __syncthreads();
-        }
-        r.pos += cnt;
-        if (r.pos < r.end && t0 + cnt == r.tiles && head == hk - 1) {
-            r.start += r.tiles * hk;
-            for (r.tiles = 0; r.tiles == 0;) {
-                if (++r.seq >= a.seqs) return;
-                r.tiles = tiles_of(a, r.seq);
-            }
+            __syncthreads();                        // the flag is read
         }
     }
 }
@@ -880,27 +875,27 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
     v8i qf[S][PC];
     float mult;
     {
-        const bool vec = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_st) | (uintptr_t)(2 * a.q_sh)) & 15) == 0;
         const uint16_t* src = a.q + (int64_t)(s.q0 + tok) * a.q_st + (int64_t)(head * a.group + hh) * a.q_sh;
         uint32_t most = 0;
-        for (int c = 0; c < 2 * S; ++c) {
-            float x[16];
-            load_q16<PC == 3>(src + 32 * c + 16 * h, vec, x);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) most = max(most, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+        for (int c = 0; c < 2 * S; ++c) {
+            uint32_t x[8];
+            load_q16(src + 32 * c + 16 * h, x);
+            most = most_of<PC == 3>(x, most);
         }
         most = max(most, (uint32_t)__shfl_xor((int)most, 32));
         const float up = row_power(most, a.scale, &mult);
 #pragma unroll
         for (int c = 0; c < 2 * S; ++c) {
-            float x[16];
-            load_q16<PC == 3>(src + 32 * c + 16 * h, vec, x);
+            uint32_t x[8];
+            load_q16(src + 32 * c + 16 * h, x);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float y[4];
                 uint32_t w[PC];
+                widen4<PC == 3>(x + 2 * j, y);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = up != 0.0f ? x[4 * j + i] * up : 0.0f;
+                for (int i = 0; i < 4; ++i) y[i] = up != 0.0f ? y[i] * up : 0.0f;
                 pieces4<PC>(y, w);
 #pragma unroll
                 for (int p = 0; p < PC; ++p) qf[c >> 1][p][4 * (c & 1) + j] = (int)w[p];
@@ -1162,7 +1157,7 @@ struct Plan {
 // 4 NT D/16 registers
 constexpr int decode_rows(int D) { return D == 256 ? 32 : 64; }
 constexpr int decode_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-int decode_workgroups() { return 2 * device_cus(); }
+int decode_workgroups(int D, int nt) { return device_cus() * decode_waves(D, nt); }
 constexpr int prefill_waves(int D, bool fp16) { return D == 256 && fp16 ? 4 : 8; }
 
 Plan plan_attention(int64_t seqs, int64_t max_q, int hq, int hk, int D, bool fp16) {
@@ -1171,7 +1166,7 @@ Plan plan_attention(int64_t seqs, int64_t max_q, int hq, int hk, int D, bool fp1
     if (rows <= decode_rows(D)) {
         p.decode = true;
         p.nt = decode_tiles(rows);
-        p.workgroups = decode_workgroups();
+        p.workgroups = decode_workgroups(D, p.nt);
         return p;
     }
     p.nw = prefill_waves(D, fp16);
@@ -1212,10 +1207,10 @@ hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
 // The joins' counters, then enough for every call of at most these sizes: fewer
 // queries take the decode kernel (two partial results per run), fewer row tiles
 // are split over the keys (at most one partial result per CU).
-size_t attention_counter_bytes() { return (size_t)(4 * counter_words(decode_workgroups())); }
+size_t attention_counter_bytes() { return (size_t)(4 * counter_words(2 * device_cus())); }
 size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, int D) {
     const int64_t rows = max_q * (hq / hk), most = decode_rows(D);
-    int64_t floats = 2 * (int64_t)decode_workgroups() * part_floats(16 * decode_tiles(rows < most ? rows : most), D);
+    int64_t floats = 4 * (int64_t)device_cus() * part_floats(16 * decode_tiles(rows < most ? rows : most), D);
     if (rows > most) {
         const int64_t split = (int64_t)device_cus() * part_floats(32 * prefill_waves(D, false), D);
         if (split > floats) floats = split;
