@@ -140,10 +140,6 @@ __device__ __forceinline__ uint32_t bad_bytes(uint32_t x) {
     return (f << 1) - (f >> 7);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __bf16 x = (__bf16)a, y = (__bf16)b;
-    return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
-}
 // p as bf16 pieces: the rounded values, and (PC == 3) the rounded rest
 template <int PC>
 __device__ __forceinline__ void pack_p(const float* p, uint32_t* hi, uint32_t* lo) {
@@ -165,12 +161,7 @@ __device__ __forceinline__ float byte_scale(uint32_t x) {
 
 template <bool FP16>
 __device__ __forceinline__ uint32_t out_pair(float a, float b) {
-    if constexpr (FP16) {
-        const _Float16 x = (_Float16)a, y = (_Float16)b;
-        return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
-    } else {
-        return pack_bf16(a, b);
-    }
+    return FP16 ? pack_f16(a, b) : pack_bf16(a, b);
 }
 
 // ===========================================================================

@@ -28,82 +28,145 @@ namespace {
 
 constexpr int kThreads = 256;
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// eight 16-bit values at any 2-byte alignment (strided views of a fused
+// projection may start anywhere): one 16-byte load either way
+struct __attribute__((packed, aligned(2))) Half8 {
+    u32x4 d;
+};
+
 template <bool FP16>
-__device__ __forceinline__ float widen(uint32_t h) {
-    return FP16 ? f16_to_f32(h) : bf16_to_f32(h);
-}
-template <bool FP16>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
-    if constexpr (FP16) {
-        const _Float16 x = (_Float16)a, y = (_Float16)b;
-        return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
-    } else {
-        const __bf16 x = (__bf16)a, y = (__bf16)b;
-        return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+__device__ __forceinline__ void widen8(u32x4 d, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = FP16 ? f16_to_f32(d[j] & 0xFFFFu) : bf16_to_f32(d[j] & 0xFFFFu);
+        x[2 * j + 1] = FP16 ? f16_to_f32(d[j] >> 16) : __uint_as_float(d[j] & 0xFFFF0000u);
     }
 }
+template <bool FP16>
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = FP16 ? pack_f16(x[2 * j], x[2 * j + 1]) : pack_bf16(x[2 * j], x[2 * j + 1]);
+    *reinterpret_cast<u32x4*>(p) = v;
+}
 
-// sum over the GL lanes of a row
+// sum over the GL lanes of a row, in lanes' registers but for the last step
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+__device__ __forceinline__ float swap16(float v) {
+    return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), (0x10 << 10) | 0x1f));
+}
+__device__ __forceinline__ double swap16(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_swizzle((int)(uint32_t)b, (0x10 << 10) | 0x1f);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_swizzle((int)(uint32_t)(b >> 32), (0x10 << 10) | 0x1f);
+    return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
 template <int GL, typename T>
 __device__ __forceinline__ T row_sum(T v) {
-#pragma unroll
-    for (int off = GL / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
+    v += dpp<0xB1>(v);                       // lanes ^ 1
+    v += dpp<0x4E>(v);                       // lanes ^ 2
+    v += dpp<0x141>(v);                      // the mirrored half row: the other four of eight
+    if (GL >= 16) v += dpp<0x140>(v);        // the mirrored row: the other eight of sixteen
+    if (GL >= 32) v += swap16(v);
     return v;
 }
 
-// Lane L of a row's GL = D/8 lanes holds values 8L .. 8L+7.  rot is a multiple
-// of 16, so a lane is inside or outside the rotated part as a whole, and the
-// partner values of split pairs lie rot/16 lanes away.
-template <int D, typename T>
-__device__ __forceinline__ void norm_rotate(T (&x)[8], int L, const float* __restrict__ w, float eps,
-                                            const float* __restrict__ cs, int rot, bool interleaved, bool bad_pos) {
-    constexpr int GL = D / 8;
-    if (w) {
-        float wv[8];
+// What a lane multiplies its values by: the weight, the rotation and its partner's.
+//   y[j] = r (x[j] a[j] + x'[j] b[j]),   x' the pairs' other values, r the norm
+// For first values a = w c, b = -w' s; for second ones a = w c, b = w' s; outside
+// the rotation a = w, b = 0 and x' = 0.  Lane L of a row's GL = D/8 lanes holds
+// values 8L .. 8L+7; rot is a multiple of 16, so a lane is inside or outside the
+// rotation as a whole, and the partners of split pairs lie rot/16 lanes away.
+template <typename T>
+struct Factors {
+    T a[8], b[8];
+};
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+struct __attribute__((packed, aligned(4))) Float4 {   // a 16-byte load at any 4-byte alignment
+    f32x4 v;
+};
+__device__ __forceinline__ void load_floats(const float* p, float (&x)[8]) {
+    const f32x4 u = reinterpret_cast<const Float4*>(p)[0].v, v = reinterpret_cast<const Float4*>(p)[1].v;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) wv[j] = w[8 * L + j];
+    for (int j = 0; j < 4; ++j) x[j] = u[j], x[4 + j] = v[j];
+}
+template <typename T>
+__device__ __forceinline__ Factors<T> factors(int L, const float* __restrict__ w, const float* __restrict__ cs, int rot,
+                                              bool interleaved, bool bad_pos) {
+    Factors<T> f;
+    const int half = rot >> 1;
+    const bool in = 8 * L < rot, first = 8 * L < half;
+    const int other = interleaved || !in ? L : first ? L + (rot >> 4) : L - (rot >> 4);
+    float wa[8], wb[8], c[8], s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wa[j] = wb[j] = 1.0f;
+    if (w) {
+        load_floats(w + 8 * L, wa);
+        load_floats(w + 8 * other, wb);
+    }
+    if (in) {
+        if (interleaved) {
+            const f32x4 u = reinterpret_cast<const Float4*>(cs + 4 * L)->v, v = reinterpret_cast<const Float4*>(cs + half + 4 * L)->v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j] = u[j / 2], s[j] = j & 1 ? v[j / 2] : -v[j / 2];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float t = wb[j];
+                wb[j] = wb[j + 1], wb[j + 1] = t;
+            }
+        } else {
+            const int i = 8 * (first ? L : other);
+            load_floats(cs + i, c);
+            load_floats(cs + half + i, s);
+            if (first)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = -s[j];
+        }
+        if (bad_pos)   // rather than some other token's angles
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j] = __builtin_nanf("");
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        f.a[j] = (T)wa[j] * (T)c[j];
+        f.b[j] = (T)wb[j] * (T)s[j];
+    }
+    return f;
+}
+
+__device__ __forceinline__ float fma_t(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ double fma_t(double a, double b, double c) { return fma(a, b, c); }
+
+// A row: d the lane's eight values, p the pairs' other ones
+template <int D, typename T, bool FP16>
+__device__ __forceinline__ void turn_row(u32x4 d, u32x4 p, const Factors<T>& f, bool norm, float eps, float (&y)[8]) {
+    float x[8], o[8];
+    widen8<FP16>(d, x);
+    widen8<FP16>(p, o);
+    T r = 1;
+    if (norm) {
         T sq = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq += x[j] * x[j];
-        const T ms = row_sum<GL>(sq) * (T)(1.0 / D) + (T)eps;
-        const T r = sizeof(T) == 8 ? (T)rsqrt((double)ms) : (T)rsqrtf((float)ms);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * r * (T)wv[j];
+        for (int j = 0; j < 8; ++j) sq = fma_t((T)x[j], (T)x[j], sq);
+        const T ms = row_sum<D / 8>(sq) * (T)(1.0 / D) + (T)eps;
+        r = sizeof(T) == 8 ? (T)rsqrt((double)ms) : (T)rsqrtf((float)ms);
     }
-    if (rot == 0) return;
-    const int half = rot >> 1;
-    if (interleaved) {
-        if (8 * L < rot) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const T c = (T)cs[4 * L + j], s = (T)cs[half + 4 * L + j];
-                const T a = x[2 * j], b = x[2 * j + 1];
-                x[2 * j] = a * c - b * s;
-                x[2 * j + 1] = b * c + a * s;
-            }
-        }
-    } else {
-        const int hl = rot >> 4;   // lanes of one half
-        const bool first = L < hl;
-        const int self = (int)(threadIdx.x & 63);
-        const int from = first ? self + hl : (L < 2 * hl ? self - hl : self);
-        T y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __shfl(x[j], from);
-        if (8 * L < rot) {
-            const int i = 8 * (first ? L : L - hl);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const T c = (T)cs[i + j], s = (T)cs[half + i + j];
-                x[j] = first ? x[j] * c - y[j] * s : x[j] * c + y[j] * s;
-            }
-        }
-    }
-    // a position outside the table: NaN rather than some other token's angles
-    if (bad_pos && 8 * L < rot) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (T)__builtin_nanf("");
-    }
+    for (int j = 0; j < 8; ++j) y[j] = (float)(fma_t((T)x[j], f.a[j], (T)o[j] * f.b[j]) * r);
 }
 
 // Eight values of a 32-block (lanes 4i .. 4i+3 of the wave hold one block) ->
@@ -129,83 +192,102 @@ __device__ __forceinline__ uint32_t encode8(const float (&v)[8], int mode, uint3
     return fold_neg_zero(p);
 }
 
-template <bool FP16, bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-    uint32_t d[4];
-    if (VEC) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = (uint32_t)p[2 * j] | ((uint32_t)p[2 * j + 1] << 16);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = widen<FP16>(d[j] & 0xFFFFu);
-        x[2 * j + 1] = widen<FP16>(d[j] >> 16);
-    }
-}
-template <bool FP16>
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(narrow2<FP16>(x[0], x[1]), narrow2<FP16>(x[2], x[3]),
-                                              narrow2<FP16>(x[4], x[5]), narrow2<FP16>(x[6], x[7]));
-}
+// A wave takes up to HPU heads of one kind (one cached key head: its fp64 work is
+// the longest) of 64 / (D/8) neighbouring tokens, one token to a group of D/8
+// lanes: the wave takes one path, the factors are made once for its heads, their
+// loads are in flight together, and neighbouring tokens' exponent bytes are
+// written together.
+template <int HPU, bool CACHE>
+struct Units {
+    int q, k, v;
+    __host__ __device__ Units(const HeadRows& a)
+        : q((a.hq + HPU - 1) / HPU), k(CACHE ? a.hk : (a.hk + HPU - 1) / HPU), v((a.hv + HPU - 1) / HPU) {}
+    __host__ __device__ int all() const { return q + k + v; }
+};
 
-// One row per group of D/8 lanes, the rows of a token neighbours (queries, keys,
-// values in this order), so that its table row is read once from memory.
-template <int D, bool FP16, bool VEC>
+template <int D, bool FP16, int HPU, bool CACHE>
 __global__ __launch_bounds__(kThreads) void head_rows_kernel(const HeadRows a) {
-    constexpr int GL = D / 8;
-    const int L = threadIdx.x % GL;
-    const uint32_t f = blockIdx.x * (uint32_t)(kThreads / GL) + threadIdx.x / GL;
-    const uint32_t per = (uint32_t)(a.hq + a.hk + a.hv);
-    const uint32_t token = f / per;
-    int h = (int)(f - token * per);
-    if (token >= (uint32_t)a.tokens) return;   // whole groups
-    const int what = h < a.hq ? 0 : h < a.hq + a.hk ? 1 : 2;
-    h -= what == 0 ? 0 : what == 1 ? a.hq : a.hq + a.hk;
+    constexpr int GL = D / 8, TB = 64 / GL;
+    const int lane = threadIdx.x & 63, L = lane % GL;
+    const Units<HPU, CACHE> n(a);
+    const uint32_t wave = blockIdx.x * (kThreads / 64) + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t block = wave / (uint32_t)n.all();
+    const int u = (int)(wave - block * (uint32_t)n.all());
+    const int64_t token = (int64_t)block * TB + lane / GL;
+    if (token >= a.tokens) return;             // whole groups
+    const int what = u < n.q ? 0 : u < n.q + n.k ? 1 : 2;
+    const bool cached = CACHE && what > 0;
+    const int per = CACHE && what == 1 ? 1 : HPU;
+    const int h0 = per * (u - (what == 0 ? 0 : what == 1 ? n.q : n.q + n.k));
+    const int count = min(per, (what == 0 ? a.hq : what == 1 ? a.hk : a.hv) - h0);
     int64_t slot = 0;
-    if (a.slots && what > 0) {
+    if (cached) {
         slot = a.slots[token];
         if (slot < 0 || slot >= (a.cache.pages << a.page_shift)) return;   // padding
     }
-    float x[8];
-    const uint16_t* src = what == 0 ? a.q + token * a.q_st + h * a.q_sh
-                          : what == 1 ? a.k + token * a.k_st + h * a.k_sh
-                                      : a.v + token * a.v_st + h * a.v_sh;
-    load8<FP16, VEC>(src + 8 * L, x);
-    if (what < 2) {
-        const float* w = what == 0 ? a.q_weight : a.k_weight;
-        const float* cs = nullptr;
-        bool bad = false;
-        if (a.rot) {
-            int64_t pos = a.positions[token];
-            bad = pos < 0 || pos >= a.cs_rows;
-            cs = a.cos_sin + (bad ? 0 : pos) * a.rot;
-        }
-        if (what == 1 && a.slots) {
-            double y[8];
+    const int64_t sh = what == 0 ? a.q_sh : what == 1 ? a.k_sh : a.v_sh;
+    const uint16_t* src = (what == 0 ? a.q + token * a.q_st : what == 1 ? a.k + token * a.k_st : a.v + token * a.v_st) + h0 * sh + 8 * L;
+    u32x4 d[HPU];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = (double)x[j];
-            norm_rotate<D>(y, L, w, a.eps, cs, a.rot, a.interleaved, bad);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = (float)y[j];
-        } else {
-            norm_rotate<D>(x, L, w, a.eps, cs, a.rot, a.interleaved, bad);
-            uint16_t* out = what == 0 ? a.q_out + ((int64_t)token * a.hq + h) * D : a.k_out + ((int64_t)token * a.hk + h) * D;
-            store8<FP16>(out + 8 * L, x);
-            return;
-        }
+    for (int i = 0; i < HPU; ++i)
+        if (i < count) d[i] = reinterpret_cast<const Half8*>(src + i * sh)->d;
+
+    const float* w = what == 0 ? a.q_weight : a.k_weight;
+    const float* cs = nullptr;
+    bool bad = false;
+    if (a.rot && what < 2) {
+        const int64_t pos = a.positions[token];
+        bad = pos < 0 || pos >= a.cs_rows;
+        cs = a.cos_sin + (bad ? 0 : pos) * a.rot;
     }
-    uint32_t e;
-    const uint32_t codes = encode8(x, a.mode, &e);
+    // the pairs' other values: two to a dword, or those of the lane rot/16 away
+    const int far = a.rot >> 4;
+    const int from = 4 * (L < far ? lane + far : L < 2 * far ? lane - far : lane);
+    const uint32_t in = 8 * L < a.rot ? ~0u : 0u;
+    auto partner = [&](u32x4 v) {
+        u32x4 p;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            p[j] = in & (a.interleaved ? (v[j] >> 16) | (v[j] << 16) : (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[j]));
+        return p;
+    };
+    if (!CACHE || !cached) {
+        const Factors<float> fa = factors<float>(L, w, cs, a.rot, a.interleaved, bad);
+        uint16_t* out = (what == 0 ? a.q_out + ((int64_t)token * a.hq + h0) * D : a.k_out + ((int64_t)token * a.hk + h0) * D) + 8 * L;
+#pragma unroll
+        for (int i = 0; i < HPU; ++i)
+            if (i < count) {
+                float y[8];
+                turn_row<D, float, FP16>(d[i], partner(d[i]), fa, w != nullptr, a.eps, y);
+                store8<FP16>(out + i * D, y);
+            }
+        return;
+    }
     const int64_t page = slot >> a.page_shift;
     const int row = (int)(slot & ((1 << a.page_shift) - 1));
-    const int64_t head = page * a.cache.kv_heads + h;
     uint8_t* cd = what == 1 ? a.cache.k_codes : a.cache.v_codes;
     uint8_t* ex = what == 1 ? a.cache.k_e8m0 : a.cache.v_e8m0;
-    *reinterpret_cast<uint32_t*>(cd + ((head << a.page_shift) + row) * (D / 2) + 4 * L) = codes;
-    if ((L & 3) == 0) ex[((head * (D / 32) + L / 4) << a.page_shift) + row] = (uint8_t)e;
+    auto put = [&](int i, const float (&x)[8]) {
+        uint32_t e;
+        const uint32_t codes = encode8(x, a.mode, &e);
+        const int64_t head = page * a.cache.kv_heads + h0 + i;
+        *reinterpret_cast<uint32_t*>(cd + ((head << a.page_shift) + row) * (D / 2) + 4 * L) = codes;
+        if ((L & 3) == 0) ex[((head * (D / 32) + L / 4) << a.page_shift) + row] = (uint8_t)e;
+    };
+    if (what == 1) {
+        const Factors<double> fa = factors<double>(L, w, cs, a.rot, a.interleaved, bad);
+        float y[8];
+        turn_row<D, double, FP16>(d[0], partner(d[0]), fa, w != nullptr, a.eps, y);
+        put(0, y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < HPU; ++i)
+            if (i < count) {
+                float y[8];
+                widen8<FP16>(d[i], y);
+                put(i, y);
+            }
+    }
 }
 
 // Rows of the cache as bf16 (exact: an e2m1 value has two significant bits);
@@ -244,33 +326,37 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(const w4a8_kv_cache c
     store8<false>(out, x);
 }
 
-template <int D>
-hipError_t rows_dim(const HeadRows& a, bool fp16, bool vec, hipStream_t s) {
-    constexpr int G = kThreads / (D / 8);
-    const int64_t rows = a.tokens * (a.hq + a.hk + a.hv);
-    const dim3 grid((unsigned)((rows + G - 1) / G));
-    if (fp16) {
-        if (vec) head_rows_kernel<D, true, true><<<grid, kThreads, 0, s>>>(a);
-        else head_rows_kernel<D, true, false><<<grid, kThreads, 0, s>>>(a);
+template <int D, int HPU>
+hipError_t rows_go(const HeadRows& a, bool fp16, hipStream_t s) {
+    constexpr int TB = 64 / (D / 8);
+    const int64_t blocks = (a.tokens + TB - 1) / TB;
+    const auto grid = [&](int units) { return dim3((unsigned)((blocks * units + kThreads / 64 - 1) / (kThreads / 64))); };
+    if (a.slots) {
+        const dim3 g = grid(Units<HPU, true>(a).all());
+        if (fp16) head_rows_kernel<D, true, HPU, true><<<g, kThreads, 0, s>>>(a);
+        else head_rows_kernel<D, false, HPU, true><<<g, kThreads, 0, s>>>(a);
     } else {
-        if (vec) head_rows_kernel<D, false, true><<<grid, kThreads, 0, s>>>(a);
-        else head_rows_kernel<D, false, false><<<grid, kThreads, 0, s>>>(a);
+        const dim3 g = grid(Units<HPU, false>(a).all());
+        if (fp16) head_rows_kernel<D, true, HPU, false><<<g, kThreads, 0, s>>>(a);
+        else head_rows_kernel<D, false, HPU, false><<<g, kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
+}
+template <int D>
+hipError_t rows_dim(const HeadRows& a, bool fp16, hipStream_t s) {
+    // four heads to a wave where that still leaves every CU four workgroups
+    constexpr int TB = 64 / (D / 8);
+    const int64_t waves = (a.tokens + TB - 1) / TB * ((a.hq + 3) / 4 + (a.hk + 3) / 4 + (a.hv + 3) / 4);
+    return waves >= (int64_t)device_cus() * 4 * (kThreads / 64) ? rows_go<D, 4>(a, fp16, s) : rows_go<D, 1>(a, fp16, s);
 }
 
 }  // namespace
 
 hipError_t launch_head_rows(const HeadRows& a, bool fp16, hipStream_t stream) {
-    // 16-byte loads where every row of every input starts on 16 bytes
-    const auto vec16 = [](const uint16_t* p, int64_t st, int64_t sh) {
-        return !p || (((uintptr_t)p | (uintptr_t)(2 * st) | (uintptr_t)(2 * sh)) & 15) == 0;
-    };
-    const bool vec = vec16(a.q, a.q_st, a.q_sh) && vec16(a.k, a.k_st, a.k_sh) && vec16(a.v, a.v_st, a.v_sh);
     switch (a.cache.head_dim) {
-        case 64: return rows_dim<64>(a, fp16, vec, stream);
-        case 128: return rows_dim<128>(a, fp16, vec, stream);
-        default: return rows_dim<256>(a, fp16, vec, stream);
+        case 64: return rows_dim<64>(a, fp16, stream);
+        case 128: return rows_dim<128>(a, fp16, stream);
+        default: return rows_dim<256>(a, fp16, stream);
     }
 }
 
