@@ -122,16 +122,23 @@ __device__ __forceinline__ void widen4(const uint32_t* d, float* x) {
         x[2 * j + 1] = FP16 ? f16_to_f32(d[j] >> 16) : bf16_to_f32(d[j] >> 16);
     }
 }
-// the power of two that takes the row's largest magnitude (bits) to [128, 256),
-// and what undoes it in the score; a non-finite row's scores are NaN
+// What a row's values are multiplied by before they are split: the power of two
+// that takes its largest magnitude (fp32 bits) to [128, 256), with the softmax
+// scale's sign; `mult`, positive, makes scores in log2 of the products.  A
+// non-finite row's mult is NaN, and its pieces are zero.
 __device__ __forceinline__ float row_power(uint32_t most, float scale, float* mult) {
     if (most >= 0x7F800000u) {
         *mult = __builtin_nanf("");
-        return 0.0f;   // the pieces stay finite
+        return 0.0f;
+    }
+    if (scale == 0.0f) {
+        *mult = 1.0f;
+        return 0.0f;
     }
     const int e = max((int)(most >> 23) - 127, -119);
-    *mult = scale * kLog2e * ldexpf(1.0f, e - 7);
-    return __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+    *mult = fmaxf(fabsf(scale) * kLog2e * ldexpf(1.0f, e - 7), 0x1p-126f);
+    const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+    return scale < 0.0f ? -up : up;
 }
 
 // byte mask of a dword's bytes >= 253
@@ -806,19 +813,59 @@ __device__ __forceinline__ void join_row(int pieces, int rows, int row, uint16_t
 // Many query rows (prompts, chunks of prompts): the matrix pipe is the bound.
 //
 // A workgroup of NW waves holds 32 NW rows of one segment, a wave 32 of them as
-// the columns of 32x32 products; 64 keys per step, shared through LDS: the
+// the columns of 32x32 products; KT keys per step, shared through LDS: the
 // keys' codes as they are (fp4 operand), the values widened to bf16 and
-// transposed once for all waves.  The copies for the next step are in flight
-// while a step computes; two LDS buffers, one barrier per step.  Where there
-// are too few workgroups for the chip the keys are split in `ks` parts and
-// joined by a second kernel.
+// transposed once for all waves.
+//
+// A wave's step has two halves: products (outputs of the step before, scores of
+// this one) and the rest (probabilities, its share of widening the values).
+// Waves w and w + 4 share a SIMD, so with eight waves the second four run half a
+// step behind: while one wave of a SIMD multiplies, the other exponentiates.  Half
+// steps are kept apart by barriers.  In half step x (tile i):
+//   first four waves    x = 2i: products(i)           x = 2i+1: rest(i), widen(i)
+//   second four waves   x = 2i: rest(i-1), widen(i)   x = 2i+1: products(i)
+// products(i) reads keys i and values i-1; widen(i) makes values i (over i-2) and
+// the exponents of keys i+1 (over i-1), which the half step before read last.
+//
+// Codes and exponents come by direct copies to LDS, kAhead steps before their
+// use, into rings of eight tiles: keys i+1+kAhead and values i+kAhead are asked
+// for in widen(i), and what widen(i+1) and products(i+1) read is waited for
+// before the barrier that ends it.
+//
+// Where there are too few workgroups for the chip the keys are split in `ks`
+// parts and joined by a second kernel.
 // ===========================================================================
-template <int D, int NW>
+// keys per step: with 256 dims the outputs and queries leave registers for the
+// scores of 32
+constexpr int prefill_keys(int D) { return D == 256 ? 32 : 64; }
+constexpr int kRing = 8, kAhead = 3, kTable = 1024;
+template <int D>
 struct PrefillLds {
-    uint8_t k[kTile * D / 2];                // row key, 16-byte units XOR-swizzled
-    uint8_t e[2 * 2 * 32 * (D / 64)];        // [32-key tile][h][row][64-step]
-    uint16_t v[D * kTile];                   // [d][slot], 16-byte units XOR-swizzled
+    static constexpr int KT = prefill_keys(D);
+    uint8_t k[kRing][KT * D / 2];            // row key, 16-byte units XOR-swizzled
+    uint8_t vr[kRing][KT * D / 2];           // the values' codes, likewise
+    uint8_t er[kRing][2][KT * D / 32];       // exponents of keys and values, [32-block][key]
+    uint8_t e[2][KT * 2 * (D / 64)];         // the keys' as scale operands: [32-key tile][h][row][64-step]
+    uint16_t v[2][D * KT];                   // values: [d][slot], 16-byte units XOR-swizzled
+    int32_t table[kTable + 1];
 };
+
+// Copies of 16 or 4 bytes a lane from p to LDS at base + lane's place.  Inline, as
+// the compiler would drain them before every LDS read; awaited by wait_copies.
+// No register is written, so none can be reused under a copy in flight.
+__device__ __forceinline__ void copy16(const uint8_t* p, uint32_t base) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(const uint8_t* p, uint32_t base) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(base) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {   // at most N of this wave's still in flight
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(p));
+}
 
 template <int D, int PC, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs a, const int tiles_max, const int ks) {
@@ -826,20 +873,28 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
     constexpr int S = D / 64;                       // 64-deep products per score
     constexpr int DT = D / 32;                      // 32-wide output tiles
     constexpr int KU = D / 32;                      // 16-byte units of a key
-    constexpr int KI = kTile * KU, VI = kTile / 4 * (D / 8);
-    constexpr int KN = (KI + TH - 1) / TH, VN = (VI + TH - 1) / TH;
-    constexpr int EI = kTile / 4 * KU;              // dwords of exponents
-    __shared__ PrefillLds<D, NW> lds[2];
+    constexpr int KT = prefill_keys(D), NK = KT / 32;
+    constexpr int KQ = KT / 4;                      // groups of four keys
+    constexpr int KI = KT * KU / 64;                // copies of a wave for a tile's keys (or values)
+    constexpr int EI = KQ * KU;                     // dwords of exponents
+    constexpr int VI = KQ * (D / 4), VN = (VI + TH - 1) / TH;   // four keys by four dims each
+    constexpr int KR = 256 / (D / 2), VR = 256 / (2 * KT);      // rows per 256 bytes of LDS banks
+    static_assert(KI <= 4 && EI <= 64, "the copies' shares below");
+    __shared__ __attribute__((aligned(16))) PrefillLds<D> lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = NW == 8 ? wave >> 2 : 0;
     const int n = lane & 31, h = lane >> 5;
     const int hk = a.cache.kv_heads, ps = a.page_shift;
 
-    // the rows' last tiles first: with causal masks they are the longest
+    // The rows' last tiles first: with causal masks they are the longest.  The pair
+    // moves on from tile to tile, so that the XCDs (workgroup mod 8) share the
+    // sequences of different lengths alike.
     const int pairs = a.seqs * hk;
     int bid = blockIdx.x;
     const int part = bid % ks;
     bid /= ks;
-    const int pair = bid % pairs, tile = tiles_max - 1 - bid / pairs;
+    const int turn = bid / pairs;
+    const int pair = (bid + turn) % pairs, tile = tiles_max - 1 - turn;
     const int sq = pair / hk, head = pair - sq * hk;
     const Seq s = seq_of(a, sq);
     const int rows = s.qlen * a.group;
@@ -849,8 +904,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
 
     // keys of the workgroup, of its part, and of this wave
     const int tok_last = (min(row0 + 32 * NW, rows) - 1) / a.group;
-    const int k_lo = key_lo(a, s, row0 / a.group) / kTile;
-    const int k_hi = (max(key_hi(a, s, tok_last), 0) + kTile - 1) / kTile;
+    const int k_lo = key_lo(a, s, row0 / a.group) / KT;
+    const int k_hi = (max(key_hi(a, s, tok_last), 0) + KT - 1) / KT;
     const int k_n = max(k_hi - k_lo, 0);
     const int t_begin = k_lo + (int)((int64_t)k_n * part / ks), t_end = k_lo + (int)((int64_t)k_n * (part + 1) / ks);
     const int wrow0 = row0 + 32 * wave;
@@ -894,170 +949,176 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
         }
     }
 
-    v16f o[DT];
+    v16f o[DT], sc[NK];
+    uint32_t pf[NK][2][4], pl[NK][2][4];            // [32-key tile][16-key step]: probabilities, fp16: their rest
     float m = neg_inf(), mu = 0.0f, l = 0.0f;
 #pragma unroll
     for (int j = 0; j < DT; ++j)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
 
-    // ---- a step's copies: into registers, then (values widened) into LDS ----
-    uint4 kc[KN];
-    uint32_t vc[VN][4], vs[VN], ke = 0, kev = 0;
-    auto page_of = [&](int key, bool* ok) {
-        const int p = table[min(key, s.ctx - 1) >> ps];
-        *ok = (uint32_t)p < (uint64_t)a.cache.pages;
-        return (int64_t)(*ok ? p : 0) * hk + head;
+    // ---- copies of tile t (absolute) into ring slot r ----
+    const int mask = (1 << ps) - 1, last_key = s.ctx - 1;
+    int page0 = 0;                                  // the first of the table's entries in LDS
+    auto entry = [&](int key) { return lds.table[(min(key, last_key) >> ps) - page0]; };
+    auto head_of = [&](int p) { return (int64_t)((uint32_t)p < (uint64_t)a.cache.pages ? p : 0) * hk + head; };
+    auto copy_codes = [&](const uint8_t* codes, uint8_t* ring, int t, int c, bool value) {
+        const int slot = 64 * c + lane, kr = slot / KU, u = slot % KU;      // LDS: row, physical unit
+        const int key = t * KT + kr;
+        // keys: swizzled by the row, values by the group of four
+        const int from = u ^ ((value ? kr / 4 : kr / KR) & (KU - 1));
+        copy16(codes + ((head_of(entry(key)) << ps) + (key & mask)) * (D / 2) + 16 * from, lds_at(ring + 1024 * c));
     };
-    const int mask = (1 << ps) - 1;
-    auto fetch = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            const int it = TH - 1 - tid + i * TH;   // from the end: few values, other threads
-            if (it < KI) {
-                const int key = t * kTile + it / KU, u = it % KU;
-                bool ok;
-                const int64_t ph = page_of(key, &ok);
-                kc[i] = *reinterpret_cast<const uint4*>(a.cache.k_codes + ((ph << ps) + (key & mask)) * (D / 2) + 16 * u);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < VN; ++i) {
-            const int it = tid + i * TH;
-            if (it < VI) {
-                const int q = it & 15, oct = it >> 4;
-                const int key = t * kTile + 4 * q;
-                bool ok;
-                const int64_t ph = page_of(key, &ok);
-                const uint8_t* c = a.cache.v_codes + ((ph << ps) + (key & mask)) * (D / 2) + 4 * oct;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) vc[i][j] = *reinterpret_cast<const uint32_t*>(c + j * (D / 2));
-                vs[i] = *reinterpret_cast<const uint32_t*>(a.cache.v_e8m0 + ((ph * KU + oct / 4) << ps) + (key & mask));
-            }
-        }
-        if (tid < EI) {
-            const int q = tid & 15, b = tid >> 4;
-            const int key = t * kTile + 4 * q;
-            bool ok;
-            const int64_t ph = page_of(key, &ok);
-            const int64_t at = ((ph * KU + b) << ps) + (key & mask);
-            ke = *reinterpret_cast<const uint32_t*>(a.cache.k_e8m0 + at);
-            kev = *reinterpret_cast<const uint32_t*>(a.cache.v_e8m0 + at);
-            if (!ok) ke = 0xFFFFFFFFu;
+    auto copy_exps = [&](const uint8_t* exps, uint8_t* ring, int t) {
+        if (lane < EI) {
+            const int key = t * KT + 4 * (lane % KQ);
+            copy4(exps + ((head_of(entry(key)) * KU + lane / KQ) << ps) + (key & mask), lds_at(ring));
         }
     };
-    auto stage = [&](PrefillLds<D, NW>& b) {
-#pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            const int it = TH - 1 - tid + i * TH;
-            if (it < KI) {
-                const int key = it / KU, u = it % KU;
-                constexpr int RP = 256 / (D / 2);   // rows per 256 bytes of banks
-                *reinterpret_cast<uint4*>(b.k + key * (D / 2) + 16 * (u ^ ((key / RP) & (KU - 1)))) = kc[i];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < VN; ++i) {
-            const int it = tid + i * TH;
-            if (it < VI) {
-                const int q = it & 15, oct = it >> 4;
-                const uint32_t sb = vs[i] & ~bad_bytes(vs[i]);
-                const float sc[4] = {byte_scale<0>(sb), byte_scale<1>(sb), byte_scale<2>(sb), byte_scale<3>(sb)};
-                // the slots of keys 4q .. 4q+3: unit 2 (q / 4) + (q & 1), half (q / 2) & 1
-                const int unit = 2 * (q >> 2) + (q & 1), half = (q >> 1) & 1;
-                auto put = [&](auto B) {
-                    constexpr int bb = decltype(B)::value;
-                    uint32_t c[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) c[j] = fp4_pair<bb>(vc[i][j], sc[j]);
-#pragma unroll
-                    for (int odd = 0; odd < 2; ++odd) {
-                        const int d = 8 * oct + 2 * bb + odd;
-                        const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
-                        *reinterpret_cast<uint2*>(b.v + d * kTile + 8 * (unit ^ ((d >> 1) & 7)) + 4 * half) =
-                            make_uint2(__builtin_amdgcn_perm(c[1], c[0], sel), __builtin_amdgcn_perm(c[3], c[2], sel));
-                    }
-                };
-                put(std::integral_constant<int, 0>{});
-                put(std::integral_constant<int, 1>{});
-                put(std::integral_constant<int, 2>{});
-                put(std::integral_constant<int, 3>{});
-            }
-        }
+    // The waves' shares: with eight waves the first four copy keys, the second four
+    // values; each at most one of codes, and one wave of each also exponents.
+    const int cw = NW == 8 ? wave & 3 : wave;
+    const bool my_k = group == 0 && cw < KI, my_v = (NW == 4 || group == 1) && cw < KI;
+    const bool my_ke = NW == 8 ? wave == 0 : wave == 0, my_ve = NW == 8 ? wave == 4 : wave == 1;
+    constexpr int kEach = NW == 8 ? 1 : 2;          // copies of codes per wave and step
+    auto ask_k = [&](int t, int r) {
+        if (my_k) copy_codes(a.cache.k_codes, lds.k[r & (kRing - 1)], t, cw, false);
+        if (my_ke) copy_exps(a.cache.k_e8m0, lds.er[r & (kRing - 1)][0], t);
+    };
+    auto ask_v = [&](int t, int r) {
+        if (my_v) copy_codes(a.cache.v_codes, lds.vr[r & (kRing - 1)], t, cw, true);
+    };
+    auto ask_ve = [&](int t, int r) {
+        if (my_ve) copy_exps(a.cache.v_e8m0, lds.er[r & (kRing - 1)][1], t);
+    };
+
+    // ---- exponents of the keys of tile i as scale operands ----
+    auto scales = [&](int i, int t) {
         if (tid < EI) {
-            const int q = tid & 15, blk = tid >> 4;
-            const uint32_t e = ke | bad_bytes(kev);
-            uint8_t* dst = b.e + ((((q >> 3) * 2 + (blk & 1)) * 32 + 4 * (q & 7)) * S) + (blk >> 1);
+            const int q = tid % KQ, blk = tid / KQ;
+            const uint8_t(*r)[KT * D / 32] = lds.er[i & (kRing - 1)];
+            const bool ok = (uint32_t)entry(t * KT + 4 * q) < (uint64_t)a.cache.pages;
+            const uint32_t ke = *reinterpret_cast<const uint32_t*>(r[0] + 4 * tid);
+            const uint32_t kv = *reinterpret_cast<const uint32_t*>(r[1] + 4 * tid);
+            const uint32_t e = ok ? ke | bad_bytes(kv) : 0xFFFFFFFFu;
+            uint8_t* dst = lds.e[i & 1] + ((((q >> 3) * 2 + (blk & 1)) * 32 + 4 * (q & 7)) * S) + (blk >> 1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) dst[j * S] = (uint8_t)(e >> (8 * j));
         }
     };
+    // ---- values of tile i widened: a thread four keys by four dims ----
+    auto widen = [&](int i) {
+        uint16_t* const dst = lds.v[i & 1];
+        const uint8_t* const raw = lds.vr[i & (kRing - 1)];
+        const uint8_t* const exps = lds.er[i & (kRing - 1)][1];
+#pragma unroll
+        for (int w = 0; w < VN; ++w) {
+            const int it = tid + w * TH;
+            if (it < VI) {
+                const int q = it % KQ, c = it / KQ;             // dims 4c .. 4c+3
+                const uint32_t sv = *reinterpret_cast<const uint32_t*>(exps + (c >> 3) * KT + 4 * q);
+                const uint32_t sb = sv & ~bad_bytes(sv);
+                const float f[4] = {byte_scale<0>(sb), byte_scale<1>(sb), byte_scale<2>(sb), byte_scale<3>(sb)};
+                const uint8_t* src = raw + 4 * q * (D / 2) + 16 * ((c >> 3) ^ (q & (KU - 1))) + 2 * (c & 7);
+                uint32_t x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint16_t*>(src + j * (D / 2));
+                // the slots of keys 4q .. 4q+3: unit 2 (q / 4) + (q & 1), half (q / 2) & 1
+                const int unit = 2 * (q >> 2) + (q & 1), half = (q >> 1) & 1;
+                auto put = [&](auto B) {
+                    constexpr int bb = decltype(B)::value;
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = fp4_pair<bb>(x[j], f[j]);
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd) {
+                        const int d = 4 * c + 2 * bb + odd;
+                        const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
+                        *reinterpret_cast<uint2*>(dst + d * KT + 8 * (unit ^ ((d / VR) & (KT / 8 - 1))) + 4 * half) =
+                            make_uint2(__builtin_amdgcn_perm(y[1], y[0], sel), __builtin_amdgcn_perm(y[3], y[2], sel));
+                    }
+                };
+                put(std::integral_constant<int, 0>{});
+                put(std::integral_constant<int, 1>{});
+            }
+        }
+    };
 
-    if (t_begin < t_end) {
-        fetch(t_begin);
-        stage(lds[0]);
-    }
-    __syncthreads();
-    for (int t = t_begin; t < t_end; ++t) {
-        const PrefillLds<D, NW>& b = lds[(t - t_begin) & 1];
-        const bool more = t + 1 < t_end;
-        if (more) fetch(t + 1);
+    // ---- products ----
+    auto outputs = [&](int i, int kt) {             // of tile i
+        const uint16_t* bv = lds.v[i & 1];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            const int key0 = t * kTile + 32 * kt;
-            if (key0 >= w_hi || key0 + 32 <= w_lo) continue;   // nothing here for this wave
-            // ---- scores of 32 keys: register i of lane (n, h) is key 8 (i / 4) + 4 h + i % 4 ----
-            v16f sc;
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sc[i] = 0.0f;
-            const int key = 32 * kt + n;
-            constexpr int RP = 256 / (D / 2);
-            const uint8_t* krow = b.k + key * (D / 2);
-            const int sw = (key / RP) & (KU - 1);
-            const uint8_t* ep = b.e + ((kt * 2 + h) * 32 + n) * S;
-            const int es = S == 4 ? *reinterpret_cast<const int*>(ep) : S == 2 ? *reinterpret_cast<const uint16_t*>(ep) : *ep;
-            auto dot = [&](auto ST) {
-                constexpr int st = decltype(ST)::value;
-                const uint4 kq = *reinterpret_cast<const uint4*>(krow + 16 * ((2 * st + h) ^ sw));
-                const v8i kf = {(int)kq.x, (int)kq.y, (int)kq.z, (int)kq.w, 0, 0, 0, 0};
-#pragma unroll
-                for (int p = 0; p < PC; ++p)
-                    sc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qf[st][p], sc, kFmtFp4, kFmtFp8, st, es, 0,
-                                                                        127 - 4 * p);
-            };
-            dot(std::integral_constant<int, 0>{});
-            if constexpr (S > 1) dot(std::integral_constant<int, 1>{});
-            if constexpr (S > 2) {
-                dot(std::integral_constant<int, 2>{});
-                dot(std::integral_constant<int, 3>{});
+            for (int j = 0; j < DT; ++j) {
+                const int d = 32 * j + n;
+                const v8h av = *reinterpret_cast<const v8h*>(bv + d * KT + 8 * ((4 * kt + 2 * st + h) ^ ((d / VR) & (KT / 8 - 1))));
+                o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pf[kt][st])), o[j], 0, 0, 0);
+                if (PC == 3)
+                    o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pl[kt][st])), o[j], 0, 0, 0);
             }
+    };
+    // scores of 32 keys: register x of lane (n, h) is key 8 (x / 4) + 4 h + x % 4
+    auto scores = [&](int i, int kt) {
+        const int key = 32 * kt + n;
+        const uint8_t* krow = lds.k[i & (kRing - 1)] + key * (D / 2);
+        const int sw = (key / KR) & (KU - 1);
+        const uint8_t* ep = lds.e[i & 1] + ((kt * 2 + h) * 32 + n) * S;
+        const int es = S == 4 ? *reinterpret_cast<const int*>(ep) : S == 2 ? *reinterpret_cast<const uint16_t*>(ep) : *ep;
+        v16f acc;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sc[i] *= mult;
-            if (key0 + 32 > all_hi || key0 < all_lo) {
+        for (int x = 0; x < 16; ++x) acc[x] = 0.0f;
+        auto dot = [&](auto ST) {
+            constexpr int st = decltype(ST)::value;
+            const uint4 kq = *reinterpret_cast<const uint4*>(krow + 16 * ((2 * st + h) ^ sw));
+            const v8i kf = {(int)kq.x, (int)kq.y, (int)kq.z, (int)kq.w, 0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int k = key0 + 8 * (i / 4) + 4 * h + i % 4;
-                    if (k >= r_hi || k < r_lo) sc[i] = neg_inf();
+            for (int p = 0; p < PC; ++p)
+                acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qf[st][p], acc, kFmtFp4, kFmtFp8, st, es, 0,
+                                                                     127 - 4 * p);
+        };
+        dot(std::integral_constant<int, 0>{});
+        if constexpr (S > 1) dot(std::integral_constant<int, 1>{});
+        if constexpr (S > 2) {
+            dot(std::integral_constant<int, 2>{});
+            dot(std::integral_constant<int, 3>{});
+        }
+        sc[kt] = acc;
+    };
+    // ---- running maximum, probabilities of the tile at key0 ----
+    auto rest = [&](int key0) {
+        if (key0 + KT > all_hi || key0 < all_lo) {
+#pragma unroll
+            for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int k = key0 + 32 * kt + 8 * (x / 4) + 4 * h + x % 4;
+                    if (k >= r_hi || k < r_lo) sc[kt][x] = neg_inf();
                 }
-            }
-            // ---- running maximum, probabilities ----
-            float mx = neg_inf();
+        }
+        float mx = neg_inf();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[i]);
-            if (__any(mx > m + kLazy)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float mn = fmaxf(m, mx);
-                const float un = mn == neg_inf() ? 0.0f : mn;
-                const float f = exp2f(m - un);
-                m = mn;
-                mu = un;
-                l *= f;
+        for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-                for (int j = 0; j < DT; ++j)
+            for (int x = 0; x < 16; ++x) mx = fmaxf(mx, sc[kt][x]);
+        mx *= mult;                                 // positive, or NaN with the row
+        if (__any(mx > m + kLazy)) {
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float mn = fmaxf(m, mx);
+            const float un = mn == neg_inf() ? 0.0f : mn;
+            const float f = exp2f(m - un);
+            m = mn;
+            mu = un;
+            l *= f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[j][i] *= f;
-            }
-            uint32_t pf[2][4], pl[2][4];
+            for (int j = 0; j < DT; ++j)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[j][x] *= f;
+        }
+#pragma unroll
+        for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
             for (int st = 0; st < 2; ++st)
 #pragma unroll
@@ -1065,27 +1126,89 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
                     float p[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        p[x] = __builtin_amdgcn_exp2f(sc[8 * st + 2 * e + x] - mu);
+                        p[x] = __builtin_amdgcn_exp2f(fmaf(sc[kt][8 * st + 2 * e + x], mult, -mu));
                         l += p[x];
                     }
-                    pack_p<PC>(p, &pf[st][e], &pl[st][e]);
+                    pack_p<PC>(p, &pf[kt][st][e], &pl[kt][st][e]);
                 }
-            // ---- values ----
-#pragma unroll
-            for (int st = 0; st < 2; ++st)
-#pragma unroll
-                for (int j = 0; j < DT; ++j) {
-                    const int d = 32 * j + n;
-                    const v8h av = *reinterpret_cast<const v8h*>(b.v + d * kTile + 8 * ((4 * kt + 2 * st + h) ^ ((d >> 1) & 7)));
-                    o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pf[st])), o[j], 0, 0, 0);
-                    if (PC == 3)
-                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pl[st])), o[j], 0, 0, 0);
-                }
-        }
-        if (more) stage(lds[(t + 1 - t_begin) & 1]);
+    };
+
+    // runs of tiles whose block-table entries fit in LDS
+    const int chunk = (kTable << ps) / KT;
+    for (int c0 = t_begin; c0 < t_end; c0 += chunk) {
+        const int tiles = min(chunk, t_end - c0);
+        page0 = (c0 * KT) >> ps;
+        const int count = (min((c0 + tiles) * KT - 1, last_key) >> ps) - page0 + 1;
+        for (int i = tid; i < count; i += TH) lds.table[i] = table[page0 + i];
         __syncthreads();
+        for (int i = 0; i <= kAhead; ++i)
+            if (i < tiles) {
+                ask_k(c0 + i, i);
+                ask_ve(c0 + i, i);
+                if (i < kAhead) ask_v(c0 + i, i);
+            }
+        wait_copies<0>();
+        __syncthreads();
+        scales(0, c0);
+        __syncthreads();
+        auto ahead = [&](int i) {                   // the copies and widening of step i
+            const bool more = i + 1 + kAhead < tiles;
+            if (more) {
+                ask_k(c0 + i + 1 + kAhead, i + 1 + kAhead);
+                ask_ve(c0 + i + 1 + kAhead, i + 1 + kAhead);
+            }
+            if (i + kAhead < tiles) ask_v(c0 + i + kAhead, i + kAhead);
+            return more;
+        };
+        auto finish = [&](int i, bool more) {
+            if (i + 1 < tiles) scales(i + 1, c0 + i + 1);
+            if (i < tiles) widen(i);
+            if (!more) wait_copies<0>();
+            else if (my_ke || my_ve) wait_copies<(kEach + 1) * (kAhead - 1)>();
+            else wait_copies<kEach * (kAhead - 1)>();
+        };
+        if (group) {
+            const bool more = ahead(0);
+            finish(0, more);
+            __syncthreads();
+        }
+        auto idle = [&](int i) {
+            __syncthreads();
+            const bool more = ahead(i + group);
+            finish(i + group, more);
+            __syncthreads();
+        };
+        // the tiles in which this wave sees a key
+        const int see_lo = min(max(w_lo / KT - c0, 0), tiles);
+        const int see_hi = w_hi > w_lo ? min(max((w_hi + KT - 1) / KT - c0, see_lo), tiles) : see_lo;
+        int i = 0;
+        for (; i < see_lo; ++i) idle(i);
+        for (; i < see_hi; ++i) {
+#pragma unroll
+            for (int kt = 0; kt < NK; ++kt) scores(i, kt);
+            // here, or the compiler sinks the products past the barrier to their first use
+#pragma unroll
+            for (int kt = 0; kt < NK; ++kt) asm volatile("" : "+v"(sc[kt]));
+            __syncthreads();
+            const bool more = ahead(i + group);
+            rest((c0 + i) * KT);
+#pragma unroll
+            for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+                for (int st = 0; st < 2; ++st)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        asm volatile("" : "+v"(pf[kt][st][e]));
+                        if (PC == 3) asm volatile("" : "+v"(pl[kt][st][e]));
+                    }
+            finish(i + group, more);
+            __syncthreads();
+#pragma unroll
+            for (int kt = 0; kt < NK; ++kt) outputs(i, kt);
+        }
+        for (; i < tiles; ++i) idle(i);
+        __syncthreads();                            // the rings and the table are free
+        if (NW == 8 && !group) __syncthreads();
     }
 
     l += __shfl_xor(l, 32);
