@@ -832,21 +832,27 @@ __device__ __forceinline__ void join_row(int pieces, int rows, int row, uint16_t
 // for in widen(i), and what widen(i+1) and products(i+1) read is waited for
 // before the barrier that ends it.
 //
-// Where there are too few workgroups for the chip the keys are split in `ks`
-// parts and joined by a second kernel.
+// Where there are too few workgroups for the chip the keys are cut into up to
+// `ks` parts, joined by a second kernel.
 // ===========================================================================
 // keys per step: with 256 dims the outputs and queries leave registers for the
 // scores of 32
 constexpr int prefill_keys(int D) { return D == 256 ? 32 : 64; }
-constexpr int kRing = 8, kAhead = 3, kTable = 1024;
-template <int D>
+constexpr int kTable = 1024;
+// the queries' last piece lies in LDS where two waves of a SIMD share its
+// registers with the outputs of 256 dims
+constexpr bool prefill_q_lds(int D, int NW) { return D == 256 && NW == 8; }
+template <int D, int NW>
 struct PrefillLds {
     static constexpr int KT = prefill_keys(D);
+    static constexpr bool kQ = prefill_q_lds(D, NW);
+    static constexpr int kAhead = kQ ? 2 : 3, kRing = kQ ? 4 : 8;
     uint8_t k[kRing][KT * D / 2];            // row key, 16-byte units XOR-swizzled
     uint8_t vr[kRing][KT * D / 2];           // the values' codes, likewise
     uint8_t er[kRing][2][KT * D / 32];       // exponents of keys and values, [32-block][key]
     uint8_t e[2][KT * 2 * (D / 64)];         // the keys' as scale operands: [32-key tile][h][row][64-step]
     uint16_t v[2][D * KT];                   // values: [d][slot], 16-byte units XOR-swizzled
+    uint4 q[kQ ? NW : 1][kQ ? D / 64 : 1][2][64];   // [wave][64-step][half][lane]
     int32_t table[kTable + 1];
 };
 
@@ -867,6 +873,34 @@ __device__ __forceinline__ uint32_t lds_at(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(p));
 }
 
+// N times: a matrix product, then an LDS read
+template <int N>
+__device__ __forceinline__ void sched_pairs() {
+    if constexpr (N > 0) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        sched_pairs<N - 1>();
+    }
+}
+
+// The key tiles [lo, lo + n) that a workgroup's rows [row0, row0 + count) see, and
+// the parts that they are cut into: of `ks`, as many as have kPartSteps of them
+// (a part costs the time of about as many beside its own).
+constexpr int kPartSteps = 16;
+struct Span {
+    int lo, n, parts;
+};
+template <int D>
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int row0, int count, int ks) {
+    constexpr int KT = prefill_keys(D);
+    const int last = (min(row0 + count, s.qlen * a.group) - 1) / a.group;
+    Span r;
+    r.lo = key_lo(a, s, row0 / a.group) / KT;
+    r.n = max((max(key_hi(a, s, last), 0) + KT - 1) / KT - r.lo, 0);
+    r.parts = min(ks, max(r.n / kPartSteps, 1));
+    return r;
+}
+
 template <int D, int PC, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs a, const int tiles_max, const int ks) {
     constexpr int TH = 64 * NW;
@@ -880,7 +914,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
     constexpr int VI = KQ * (D / 4), VN = (VI + TH - 1) / TH;   // four keys by four dims each
     constexpr int KR = 256 / (D / 2), VR = 256 / (2 * KT);      // rows per 256 bytes of LDS banks
     static_assert(KI <= 4 && EI <= 64, "the copies' shares below");
-    __shared__ __attribute__((aligned(16))) PrefillLds<D> lds;
+    typedef PrefillLds<D, NW> Lds;
+    constexpr int kRing = Lds::kRing, kAhead = Lds::kAhead;
+    constexpr int PR = Lds::kQ ? PC - 1 : PC;       // pieces of the queries in registers
+    __shared__ __attribute__((aligned(16))) Lds lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = NW == 8 ? wave >> 2 : 0;
     const int n = lane & 31, h = lane >> 5;
@@ -903,11 +940,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
     const int32_t* table = a.table + (int64_t)sq * a.table_stride;
 
     // keys of the workgroup, of its part, and of this wave
-    const int tok_last = (min(row0 + 32 * NW, rows) - 1) / a.group;
-    const int k_lo = key_lo(a, s, row0 / a.group) / KT;
-    const int k_hi = (max(key_hi(a, s, tok_last), 0) + KT - 1) / KT;
-    const int k_n = max(k_hi - k_lo, 0);
-    const int t_begin = k_lo + (int)((int64_t)k_n * part / ks), t_end = k_lo + (int)((int64_t)k_n * (part + 1) / ks);
+    const Span span = span_of<D>(a, s, row0, 32 * NW, ks);
+    if (part >= span.parts) return;
+    const int t_begin = span.lo + (int)((int64_t)span.n * part / span.parts);
+    const int t_end = span.lo + (int)((int64_t)span.n * (part + 1) / span.parts);
     const int wrow0 = row0 + 32 * wave;
     const bool live = wrow0 < rows;
     const int wtok0 = min(wrow0, rows - 1) / a.group, wtok1 = min(wrow0 + 31, rows - 1) / a.group;
@@ -918,7 +954,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
     const int row = min(wrow0 + n, rows - 1);
     const int tok = row / a.group, hh = row - tok * a.group;
     const int r_hi = key_hi(a, s, tok), r_lo = key_lo(a, s, tok);
-    v8i qf[S][PC];
+    v8i qf[S][PR];
     float mult;
     {
         const uint16_t* src = a.q + (int64_t)(s.q0 + tok) * a.q_st + (int64_t)(head * a.group + hh) * a.q_sh;
@@ -935,6 +971,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
         for (int c = 0; c < 2 * S; ++c) {
             uint32_t x[8];
             load_q16(src + 32 * c + 16 * h, x);
+            uint32_t last[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float y[4];
@@ -944,8 +981,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
                 for (int i = 0; i < 4; ++i) y[i] = up != 0.0f ? y[i] * up : 0.0f;
                 pieces4<PC>(y, w);
 #pragma unroll
-                for (int p = 0; p < PC; ++p) qf[c >> 1][p][4 * (c & 1) + j] = (int)w[p];
+                for (int p = 0; p < PR; ++p) qf[c >> 1][p][4 * (c & 1) + j] = (int)w[p];
+                last[j] = w[PC - 1];
             }
+            if constexpr (Lds::kQ) lds.q[wave][c >> 1][c & 1][lane] = make_uint4(last[0], last[1], last[2], last[3]);
         }
     }
 
@@ -1075,9 +1114,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
             const uint4 kq = *reinterpret_cast<const uint4*>(krow + 16 * ((2 * st + h) ^ sw));
             const v8i kf = {(int)kq.x, (int)kq.y, (int)kq.z, (int)kq.w, 0, 0, 0, 0};
 #pragma unroll
-            for (int p = 0; p < PC; ++p)
-                acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qf[st][p], acc, kFmtFp4, kFmtFp8, st, es, 0,
-                                                                     127 - 4 * p);
+            for (int p = 0; p < PC; ++p) {
+                v8i qp;
+                if (Lds::kQ && p == PC - 1) {
+                    const uint4 q0 = lds.q[wave][st][0][lane], q1 = lds.q[wave][st][1][lane];
+                    qp = v8i{(int)q0.x, (int)q0.y, (int)q0.z, (int)q0.w, (int)q1.x, (int)q1.y, (int)q1.z, (int)q1.w};
+                } else
+                    qp = qf[st][p];
+                acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qp, acc, kFmtFp4, kFmtFp8, st, es, 0, 127 - 4 * p);
+            }
         };
         dot(std::integral_constant<int, 0>{});
         if constexpr (S > 1) dot(std::integral_constant<int, 1>{});
@@ -1183,9 +1228,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
         const int see_hi = w_hi > w_lo ? min(max((w_hi + KT - 1) / KT - c0, see_lo), tiles) : see_lo;
         int i = 0;
         for (; i < see_lo; ++i) idle(i);
-        for (; i < see_hi; ++i) {
+        if (Lds::kQ && i < see_hi)
 #pragma unroll
             for (int kt = 0; kt < NK; ++kt) scores(i, kt);
+        for (; i < see_hi; ++i) {
+            if (!Lds::kQ)
+#pragma unroll
+                for (int kt = 0; kt < NK; ++kt) scores(i, kt);
             // here, or the compiler sinks the products past the barrier to their first use
 #pragma unroll
             for (int kt = 0; kt < NK; ++kt) asm volatile("" : "+v"(sc[kt]));
@@ -1203,8 +1252,23 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
                     }
             finish(i + group, more);
             __syncthreads();
+            if constexpr (Lds::kQ) {
+                // With the scores of the next tile (past the last one they are of whatever the
+                // rings hold, and not used) in one block, whose LDS reads run kDeep ahead of
+                // its products: left to itself the compiler waits for each read.
+                constexpr int kReads = NK * (2 * DT + S + 2 * S + 1), kProducts = NK * (2 * DT + S * PC), kDeep = 4;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kt = 0; kt < NK; ++kt) outputs(i, kt);
+                for (int kt = 0; kt < NK; ++kt) outputs(i, kt);
+#pragma unroll
+                for (int kt = 0; kt < NK; ++kt) scores(i + 1, kt);
+                __builtin_amdgcn_sched_group_barrier(0x100, kDeep, 0);
+                sched_pairs<(kReads - kDeep < kProducts ? kReads - kDeep : kProducts)>();
+                __builtin_amdgcn_sched_barrier(0);
+            } else {
+#pragma unroll
+                for (int kt = 0; kt < NK; ++kt) outputs(i, kt);
+            }
         }
         for (; i < tiles; ++i) idle(i);
         __syncthreads();                            // the rings and the table are free
@@ -1213,7 +1277,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
 
     l += __shfl_xor(l, 32);
     if (wrow0 + n >= rows) return;
-    if (ks == 1) {
+    if (span.parts == 1) {
         uint16_t* dst = a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + hh) * D;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -1248,11 +1312,13 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(const AttnArgs a, con
     const Seq s = seq_of(a, sq);
     if (row >= s.qlen * a.group) return;
     const int tile = row / tile_rows;
+    const int parts = span_of<D>(a, s, tile * tile_rows, tile_rows, ks).parts;
+    if (parts == 1) return;
     const int tok = row / a.group, h = row - tok * a.group;
     uint16_t* dst = a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
     const float* ws = reinterpret_cast<const float*>(a.ws) + a.ws_skip;
     const int64_t size = part_floats(tile_rows, D);
-    join_row<D, FP16>(ks, tile_rows, row - tile * tile_rows, dst,
+    join_row<D, FP16>(parts, tile_rows, row - tile * tile_rows, dst,
                       [&](int i) { return ws + (((int64_t)pair * tiles_max + tile) * ks + i) * size; });
 }
 
@@ -1274,6 +1340,21 @@ constexpr int decode_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 
 int decode_workgroups(int D, int nt) { return device_cus() * decode_waves(D, nt); }
 constexpr int prefill_waves(int D, bool fp16) { return D == 256 && fp16 ? 4 : 8; }
 
+// Parts of the keys: what fills whole rounds of the CUs best, fewest first; a
+// step up has to fill a tenth more.  Two rounds and more of row tiles are not cut.
+constexpr int kSplitRounds = 3;
+int split_of(int64_t grid, int64_t cus) {
+    if (grid >= 2 * cus) return 1;
+    int best = 1;
+    double fill = 0;
+    for (int64_t ks = 1; grid * ks <= kSplitRounds * cus; ++ks) {
+        const int64_t rounds = (grid * ks + cus - 1) / cus;
+        const double f = (double)(grid * ks) / (double)(rounds * cus);
+        if (f > 1.1 * fill) best = (int)ks, fill = f;
+    }
+    return best;
+}
+
 Plan plan_attention(int64_t seqs, int64_t max_q, int hq, int hk, int D, bool fp16) {
     Plan p{};
     const int64_t rows = max_q * (hq / hk);
@@ -1285,8 +1366,7 @@ Plan plan_attention(int64_t seqs, int64_t max_q, int hq, int hk, int D, bool fp1
     }
     p.nw = prefill_waves(D, fp16);
     p.tiles = (int)((rows + 32 * p.nw - 1) / (32 * p.nw));
-    const int64_t grid = seqs * hk * p.tiles, cus = device_cus();
-    p.ks = (int)(grid >= cus ? 1 : cus / grid);
+    p.ks = split_of(seqs * hk * p.tiles, device_cus());
     return p;
 }
 
@@ -1320,13 +1400,13 @@ hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
 
 // The joins' counters, then enough for every call of at most these sizes: fewer
 // queries take the decode kernel (two partial results per run), fewer row tiles
-// are split over the keys (at most one partial result per CU).
+// are split over the keys (at most kSplitRounds partial results per CU).
 size_t attention_counter_bytes() { return (size_t)(4 * counter_words(2 * device_cus())); }
 size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, int D) {
     const int64_t rows = max_q * (hq / hk), most = decode_rows(D);
     int64_t floats = 4 * (int64_t)device_cus() * part_floats(16 * decode_tiles(rows < most ? rows : most), D);
     if (rows > most) {
-        const int64_t split = (int64_t)device_cus() * part_floats(32 * prefill_waves(D, false), D);
+        const int64_t split = (int64_t)kSplitRounds * device_cus() * part_floats(32 * prefill_waves(D, false), D);
         if (split > floats) floats = split;
     }
     return attention_counter_bytes() + (size_t)floats * 4;
