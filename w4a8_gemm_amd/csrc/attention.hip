@@ -126,19 +126,19 @@ __device__ __forceinline__ void widen4(const uint32_t* d, float* x) {
 // that takes its largest magnitude (fp32 bits) to [128, 256), with the softmax
 // scale's sign; `mult`, positive, makes scores in log2 of the products.  A
 // non-finite row's mult is NaN, and its pieces are zero.
-__device__ __forceinline__ float row_power(uint32_t most, float scale, float* mult) {
+__device__ __forceinline__ float row_power(uint32_t most, const AttnArgs& a, float* mult) {
     if (most >= 0x7F800000u) {
         *mult = __builtin_nanf("");
         return 0.0f;
     }
-    if (scale == 0.0f) {
+    if (a.scale == 0.0f) {
         *mult = 1.0f;
         return 0.0f;
     }
     const int e = max((int)(most >> 23) - 127, -119);
-    *mult = fmaxf(fabsf(scale) * kLog2e * ldexpf(1.0f, e - 7), 0x1p-126f);
+    *mult = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 0x1p-126f);
     const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-    return scale < 0.0f ? -up : up;
+    return a.scale < 0.0f ? -up : up;
 }
 
 // byte mask of a dword's bytes >= 253
@@ -180,7 +180,7 @@ __device__ __forceinline__ uint32_t out_pair(float a, float b) {
 // them to arrive (below).  The cut follows the lengths in device memory, so the
 // grid depends on none of them.
 //
-// A wave takes every fourth tile of its workgroup's run.  Rows of 16 queries are
+// A wave takes every NW-th tile of its workgroup's run.  Rows of 16 queries are
 // the columns of the 16x16 products:
 //   S^T = K Q^T: tile u of four holds keys 4r + u (r = row), so that a lane reads
 //     the exponents of its four keys as one dword and picks by opsel;
@@ -212,9 +212,10 @@ __device__ __forceinline__ int first_tile(const AttnArgs& a, const Seq& s) { ret
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, const Seq& q) {
     return max(1, (q.ctx + kTile - 1) / kTile - first_tile(a, q));
 }
+template <int NW>
 __device__ __forceinline__ int place_of(const AttnArgs& a, int s) {
     const Seq q = seq_of(a, s);
-    return q.qlen ? (tiles_of(a, q) + kSegment + 3) & ~3 : 0;
+    return q.qlen ? (tiles_of(a, q) + kSegment + NW - 1) & ~(NW - 1) : 0;
 }
 __device__ __forceinline__ int wave_scan(int v) {   // inclusive
     const int lane = threadIdx.x & 63;
@@ -229,31 +230,46 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive
 // A workgroup's run [pos, end) of the line, and the sequence that holds its
 // start: first position and length per head.
 struct Run {
-    int total, run;          // of the line; per workgroup
+    int run;                 // per workgroup
     int pos, end;
     int seq, start, place;
 };
+// tiles of a wave up to which segments are not cut: a join takes as long
+constexpr int kWhole = 2;
+template <int NW>
 __device__ __forceinline__ Run run_of(const AttnArgs& a, int workgroups) {
     const int lane = threadIdx.x & 63, hk = a.cache.kv_heads;
-    Run r;
-    int n = lane < a.seqs ? place_of(a, lane) : 0;
-    int incl = wave_scan(n);
-    const int64_t head = (int64_t)__shfl(incl, 63);
-    int64_t t = head;
-    for (int s0 = 64; s0 < a.seqs; s0 += 64) t += __shfl(wave_scan(s0 + lane < a.seqs ? place_of(a, s0 + lane) : 0), 63);
     const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-    r.total = uniform((int)t * hk);
-    r.run = uniform(max((r.total + workgroups - 1) / workgroups, 4));   // a tile for every wave
-    const int64_t pos = (int64_t)blockIdx.x * r.run;
-    r.pos = (int)min(pos, (int64_t)r.total);
-    r.end = min(r.pos + r.run, r.total);
-    r.seq = a.seqs;
+    Run r;
+    int n = lane < a.seqs ? place_of<NW>(a, lane) : 0, longest = n;
+    int incl = wave_scan(n);
+    int64_t t = __shfl(incl, 63);
+    for (int s0 = 64; s0 < a.seqs; s0 += 64) {
+        const int v = s0 + lane < a.seqs ? place_of<NW>(a, s0 + lane) : 0;
+        longest = max(longest, v);
+        t += __shfl(wave_scan(v), 63);
+    }
     r.start = r.place = 0;
-    if (r.pos >= r.total) return r;
+    if ((int64_t)a.seqs * hk <= workgroups && !__any(longest > NW * kWhole + kSegment)) {   // a workgroup each
+        r.seq = (int)blockIdx.x / hk;
+        r.place = r.seq < a.seqs ? uniform(place_of<NW>(a, r.seq)) : 0;
+        if (r.place == 0) r.seq = a.seqs;
+        r.pos = ((int)blockIdx.x - r.seq * hk) * r.place;
+        r.run = r.place;
+        r.end = r.pos + r.place;
+        return r;
+    }
+    const int total = uniform((int)t * hk);
+    r.run = uniform(max((total + workgroups - 1) / workgroups, NW));   // a tile for every wave
+    const int64_t pos = (int64_t)blockIdx.x * r.run;
+    r.pos = (int)min(pos, (int64_t)total);
+    r.end = min(r.pos + r.run, total);
+    r.seq = a.seqs;
+    if (r.pos >= total) return r;
     int base = 0;
     for (int s0 = 0; s0 < a.seqs; s0 += 64) {
         if (s0) {
-            n = s0 + lane < a.seqs ? place_of(a, s0 + lane) : 0;
+            n = s0 + lane < a.seqs ? place_of<NW>(a, s0 + lane) : 0;
             incl = wave_scan(n);
         }
         const int first = base + (incl - n) * hk;
@@ -293,11 +309,11 @@ __device__ __forceinline__ void ws_put(__amdgpu_buffer_rsrc_t ws, uint32_t at, f
 
 // Joins `count` results (the j-th at slot(j)) of `rows` live rows: into slot(0),
 // or normalized into the output.  R = rows of a slot; ml: 2 R kJoinMost floats.
-template <int D, int R, bool FP16, typename SLOT, typename OUT>
+template <int D, int R, int TH, bool FP16, typename SLOT, typename OUT>
 __device__ __forceinline__ void join_pieces(__amdgpu_buffer_rsrc_t ws, SLOT slot, int count, int rows, bool final, OUT out,
                                             float* ml) {
     constexpr int C = D / 4;                // threads per row
-    constexpr int RG = 256 / C;
+    constexpr int RG = TH / C;
     constexpr int B = 8;                    // results in flight
     const int tid = threadIdx.x, c = tid % C;
     auto fetch = [&](sk_i32x4* v, int row, int j0) {
@@ -308,7 +324,7 @@ __device__ __forceinline__ void join_pieces(__amdgpu_buffer_rsrc_t ws, SLOT slot
     int row = tid / C;
     sk_i32x4 v[B];
     if (row < rows) fetch(v, row, 0);
-    for (int i = tid; i < rows * count; i += 256) {
+    for (int i = tid; i < rows * count; i += TH) {
         const int j = i / rows, r = i - j * rows;
         ml[j * R + r] = ws_get(ws, slot(j) + 4u * (uint32_t)(R * D + r));
         ml[(kJoinMost + j) * R + r] = ws_get(ws, slot(j) + 4u * (uint32_t)(R * D + R + r));
@@ -347,16 +363,27 @@ __device__ __forceinline__ void join_pieces(__amdgpu_buffer_rsrc_t ws, SLOT slot
     }
 }
 
-// waves per SIMD: the outputs of many rows need the registers of two
-constexpr int decode_waves(int D, int NT) { return NT * (D / 16) > 16 ? 1 : 2; }
+// waves per SIMD of four-wave workgroups: the outputs of many rows need the registers
+// of two; with 64 dims there are registers for three, and the third hides changes of
+// segments (3200 segments of 1620 keys on average 98 -> 90 us; with 128 dims it spills,
+// and 512 segments took 71 us for 68)
+constexpr int decode_waves(int D, int NT) { return NT * (D / 16) > 16 || NT == 4 ? 1 : NT == 1 && D == 64 ? 3 : 2; }
+constexpr int kWavesMost = 3;
 
-template <int D, int NT, int PC>
-__global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const AttnArgs a, const int workgroups) {
+// NW waves to a workgroup.  Eight, one workgroup to a CU, where few segments have
+// tiles for all of them: the runs are half as many pieces to join, and all waves keep
+// step (of two workgroups the older is served first: equal runs ended after 40 and 55
+// us).  Three contexts to 131072 keys 75 -> 70 us, eight of 4000 14.7 -> 13.6 us.  Four,
+// two or three workgroups to a CU, where runs cross segments, so that one streams while
+// another changes segments (64 sequences of drafts, 25.7 us with eight, 24.1 with four),
+// and for short contexts (one of 1021 keys: 15.1 and 13.7 us).
+template <int D, int NT, int PC, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : decode_waves(D, NT)) void decode_kernel(const AttnArgs a, const int workgroups) {
     constexpr int KS = D >= 128 ? D / 128 : 1;      // 128-deep products per score
     constexpr int QP = D >= 128 ? PC : PC - 1;      // q operands per 128 (D = 64: pieces side by side)
     constexpr int DT = D / 16;                      // output tiles
     constexpr int C = D / 64;                       // runs of 16 query values per lane
-    constexpr int R = NT * 16;
+    constexpr int R = NT * 16, TH = 64 * NW;
     typedef typename VWord<D>::T VT;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -364,10 +391,10 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
     // queries while the keys stream; then the waves' results, rows padded by 16
     // bytes; then the joined pieces' maxima and sums
     constexpr int kRow = D + 4;
-    constexpr int kQBytes = NT * KS * QP * 2048, kOBytes = 4 * R * kRow * 4, kMBytes = 2 * R * kJoinMost * 4;
+    constexpr int kQBytes = NT * KS * QP * 2048, kOBytes = NW * R * kRow * 4, kMBytes = 2 * R * kJoinMost * 4;
     constexpr int kBytes = kQBytes > kOBytes ? (kQBytes > kMBytes ? kQBytes : kMBytes) : (kOBytes > kMBytes ? kOBytes : kMBytes);
     __shared__ __attribute__((aligned(16))) uint8_t smem[kBytes];
-    __shared__ float sm_m[4][R], sm_l[4][R];
+    __shared__ float sm_m[NW][R], sm_l[NW][R];
     __shared__ uint32_t sm_flag;
     __shared__ int32_t sm_table[16 * kTile + 1];
     uint4* const sm_q = reinterpret_cast<uint4*>(smem);                 // [nt][k][p][half][lane]
@@ -375,7 +402,7 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
     uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws);
     float* const parts = reinterpret_cast<float*>(a.ws) + a.ws_skip;
 
-    Run r = run_of(a, workgroups);
+    Run r = run_of<NW>(a, workgroups);
     if (r.seq >= a.seqs) return;
 
     while (r.pos < r.end) {
@@ -387,9 +414,9 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
         const int cnt = min(span, tiles - t0);                  // tiles among it
         r.pos += span;
         const int seq = r.seq, start = r.start, r_place = r.place;
-        if (t0 + span == r.place && head == hk - 1) {           // the next sequence with queries
+        if (r.pos < r.end && t0 + span == r.place && head == hk - 1) {   // the next sequence with queries
             r.start += r.place * hk;
-            for (r.place = 0; r.place == 0 && ++r.seq < a.seqs;) r.place = place_of(a, r.seq);
+            for (r.place = 0; r.place == 0 && ++r.seq < a.seqs;) r.place = place_of<NW>(a, r.seq);
             if (r.seq >= a.seqs) r.end = r.pos;
         }
         if (cnt <= 0) continue;
@@ -408,7 +435,7 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
         auto fill_table = [&](int from, int to) {   // those of tiles [from, to)
             page0 = (from * kTile) >> ps;
             const int count = (min(to * kTile - 1, last_key) >> ps) - page0 + 1;
-            for (int i = threadIdx.x; i < count; i += 256) sm_table[i] = table[page0 + i];
+            for (int i = threadIdx.x; i < count; i += TH) sm_table[i] = table[page0 + i];
         };
         // the page of a lane's four keys, and of its sixteen values; keys past the
         // context take the last one's (they are masked).  An entry outside the cache
@@ -445,11 +472,11 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
         // tiles whose entries are in LDS together
         const int chunk = 16 << ps;
         int c_end = min(t_end, first + t0 + chunk);
-        if (first + t0 < t_end) fill_table(first + t0, c_end);
 
         // ---- queries: every wave finds its rows' powers, and converts its share ----
         float mult[NT];
         int hi[NT], lo[NT];
+        uint32_t x[NT][C][8], most[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = min(nt * 16 + n, rows - 1);
@@ -457,30 +484,38 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
             hi[nt] = key_hi(a, s, tok);
             lo[nt] = key_lo(a, s, tok);
             const uint16_t* src = a.q + (int64_t)(s.q0 + tok) * a.q_st + (int64_t)(head * a.group + h) * a.q_sh + 16 * g;
-            uint32_t x[C][8], most = 0;
 #pragma unroll
-            for (int c = 0; c < C; ++c) load_q16(src + 64 * c, x[c]);
-            if (nt == 0) {
-                __syncthreads();                    // the table; the last segment's results are out
-                if (t < c_end) {                    // the first tile's loads run meanwhile
-                    load_k(t);
-                    load_v(t);
-                }
-            }
+            for (int c = 0; c < C; ++c) load_q16(src + 64 * c, x[nt][c]);
+        }
+        if (first + t0 < t_end) fill_table(first + t0, c_end);
+        __syncthreads();                            // the table; the last segment's results are out
+        // all of the queries are waited for here: past the branch their wait would be one
+        // for the keys
 #pragma unroll
-            for (int c = 0; c < C; ++c) most = most_of<PC == 3>(x[c], most);
-            most = max(most, (uint32_t)__shfl_xor((int)most, 16));
-            most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-            const float up = row_power(most, a.scale, &mult[nt]);
+        for (int nt = 0; nt < NT; ++nt) {
+            most[nt] = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) most[nt] = most_of<PC == 3>(x[nt][c], most[nt]);
+            asm volatile("" : "+v"(most[nt]));
+        }
+        if (t < c_end) {                            // the first tile's loads run meanwhile
+            load_k(t);
+            load_v(t);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            most[nt] = max(most[nt], (uint32_t)__shfl_xor((int)most[nt], 16));
+            most[nt] = max(most[nt], (uint32_t)__shfl_xor((int)most[nt], 32));
+            const float up = row_power(most[nt], a, &mult[nt]);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                if (((nt * C + c) & 3) != wave) continue;
+                if (((nt * C + c) & (NW - 1)) != wave) continue;
                 uint32_t w[PC][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float y[4];
                     uint32_t v[PC];
-                    widen4<PC == 3>(x[c] + 2 * j, y);
+                    widen4<PC == 3>(x[nt][c] + 2 * j, y);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) y[i] = up != 0.0f ? y[i] * up : 0.0f;
                     pieces4<PC>(y, v);
@@ -569,7 +604,7 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
                         dot(std::integral_constant<int, 3>{});
                     }
                 __builtin_amdgcn_sched_barrier(0);
-                if (nt == NT - 1 && more) load_k(t + 4);
+                if (nt == NT - 1 && more) load_k(t + NW);
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -667,13 +702,17 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
                     }
                 }
             }
-            if (more) load_v(t + 4);
+            if (more) load_v(t + NW);
         };
         while (true) {
             if (t < c_end) {
-                for (; t + 4 < c_end; t += 4) step(std::true_type{});
+                for (; t + NW < c_end; t += NW) {
+                    step(std::true_type{});
+                    // all waves have a next tile: in step (loads in flight are not awaited)
+                    if (NW == 8 && t - wave + 2 * NW <= c_end) __builtin_amdgcn_s_barrier();
+                }
                 step(std::false_type{});
-                t += 4;
+                t += NW;
             }
             if (c_end >= t_end) break;
             __syncthreads();                        // the next tiles' entries
@@ -687,7 +726,7 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
             }
         }
 
-        // ---- the four waves' results ----
+        // ---- the waves' results ----
         __syncthreads();                            // the queries are read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -716,15 +755,15 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
         constexpr uint32_t kPart = (uint32_t)(4 * part_floats(R, D));
         const __amdgpu_buffer_rsrc_t ws = sk_rsrc(parts);
         const uint32_t mine = (2u * blockIdx.x + (t0 == 0 ? 1u : 0u)) * kPart;
-        for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+        for (int i = threadIdx.x; i < rows * (D / 4); i += TH) {
             const int row = i / (D / 4), c = i - row * (D / 4);
             float mx = neg_inf(), sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) mx = fmaxf(mx, sm_m[w][row]);
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm_m[w][row]);
             const float u = mx == neg_inf() ? 0.0f : mx;
             v4f acc = {0, 0, 0, 0};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const float f = exp2f(sm_m[w][row] - u);    // 0 without a key (NaN outputs stay NaN)
                 sum += sm_l[w][row] * f;
                 acc += *reinterpret_cast<const v4f*>(sm_o + (w * R + row) * kRow + 4 * c) * f;
@@ -757,7 +796,7 @@ __global__ __launch_bounds__(256, decode_waves(D, NT)) void decode_kernel(const 
                 };
                 if (!sk_arrive(counters + (int64_t)level * 2 * workgroups + id(0), count, &sm_flag)) break;
                 const bool final = pieces <= fan;
-                join_pieces<D, R, PC == 3>(ws, [&](int j) { return id(j) * kPart; }, count, rows, final, out_row,
+                join_pieces<D, R, TH, PC == 3>(ws, [&](int j) { return id(j) * kPart; }, count, rows, final, out_row,
                                            reinterpret_cast<float*>(smem));
                 pieces = (pieces + fan - 1) / fan;
                 at /= fan;
@@ -966,7 +1005,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
             most = most_of<PC == 3>(x, most);
         }
         most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-        const float up = row_power(most, a.scale, &mult);
+        const float up = row_power(most, a, &mult);
 #pragma unroll
         for (int c = 0; c < 2 * S; ++c) {
             uint32_t x[8];
@@ -1329,7 +1368,7 @@ struct Plan {
     bool decode;
     int nt;              // decode: 16-row tiles
     int workgroups;      // decode: runs of the line
-    int nw;              // prompts: waves
+    int nw;              // waves of a workgroup
     int tiles;           // prompts: row tiles per segment
     int ks;              // prompts: parts of the keys
 };
@@ -1337,7 +1376,6 @@ struct Plan {
 // 4 NT D/16 registers
 constexpr int decode_rows(int D) { return D == 256 ? 32 : 64; }
 constexpr int decode_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-int decode_workgroups(int D, int nt) { return device_cus() * decode_waves(D, nt); }
 constexpr int prefill_waves(int D, bool fp16) { return D == 256 && fp16 ? 4 : 8; }
 
 // Parts of the keys: what fills whole rounds of the CUs best, fewest first; a
@@ -1355,13 +1393,15 @@ int split_of(int64_t grid, int64_t cus) {
     return best;
 }
 
-Plan plan_attention(int64_t seqs, int64_t max_q, int hq, int hk, int D, bool fp16) {
+Plan plan_attention(int64_t seqs, int64_t max_q, int64_t keys, int hq, int hk, int D, bool fp16) {
     Plan p{};
     const int64_t rows = max_q * (hq / hk);
     if (rows <= decode_rows(D)) {
         p.decode = true;
         p.nt = decode_tiles(rows);
-        p.workgroups = decode_workgroups(D, p.nt);
+        const int64_t tiles = seqs * hk * ((keys + kTile - 1) / kTile), cus = device_cus();
+        p.nw = decode_waves(D, p.nt) >= 2 && 4 * seqs * hk <= cus && tiles >= 8 * cus ? 8 : 4;
+        p.workgroups = (int)cus * (p.nw == 4 ? decode_waves(D, p.nt) : 1);
         return p;
     }
     p.nw = prefill_waves(D, fp16);
@@ -1370,11 +1410,17 @@ Plan plan_attention(int64_t seqs, int64_t max_q, int hq, int hk, int D, bool fp1
     return p;
 }
 
+template <int D, int NT, int NW>
+hipError_t go_waves(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
+    if (fp16) decode_kernel<D, NT, 3, NW><<<p.workgroups, 64 * NW, 0, st>>>(a, p.workgroups);
+    else decode_kernel<D, NT, 2, NW><<<p.workgroups, 64 * NW, 0, st>>>(a, p.workgroups);
+    return hipGetLastError();
+}
 template <int D, int NT>
 hipError_t go_decode(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
-    if (fp16) decode_kernel<D, NT, 3><<<p.workgroups, 256, 0, st>>>(a, p.workgroups);
-    else decode_kernel<D, NT, 2><<<p.workgroups, 256, 0, st>>>(a, p.workgroups);
-    return hipGetLastError();
+    if constexpr (decode_waves(D, NT) >= 2)
+        if (p.nw == 8) return go_waves<D, NT, 8>(a, p, fp16, st);
+    return go_waves<D, NT, 4>(a, p, fp16, st);
 }
 template <int D>
 hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
@@ -1401,10 +1447,10 @@ hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
 // The joins' counters, then enough for every call of at most these sizes: fewer
 // queries take the decode kernel (two partial results per run), fewer row tiles
 // are split over the keys (at most kSplitRounds partial results per CU).
-size_t attention_counter_bytes() { return (size_t)(4 * counter_words(2 * device_cus())); }
+size_t attention_counter_bytes() { return (size_t)(4 * counter_words(kWavesMost * device_cus())); }
 size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, int D) {
     const int64_t rows = max_q * (hq / hk), most = decode_rows(D);
-    int64_t floats = 4 * (int64_t)device_cus() * part_floats(16 * decode_tiles(rows < most ? rows : most), D);
+    int64_t floats = 2 * kWavesMost * (int64_t)device_cus() * part_floats(16 * decode_tiles(rows < most ? rows : most), D);
     if (rows > most) {
         const int64_t split = (int64_t)kSplitRounds * device_cus() * part_floats(32 * prefill_waves(D, false), D);
         if (split > floats) floats = split;
@@ -1415,7 +1461,10 @@ size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, in
 hipError_t launch_attention(const AttnArgs& args, bool fp16, hipStream_t stream) {
     AttnArgs a = args;
     a.ws_skip = (int64_t)attention_counter_bytes() / 4;
-    const Plan p = plan_attention(a.seqs, a.max_q, a.hq, a.cache.kv_heads, a.cache.head_dim, fp16);
+    a.scale_log2 = fabsf(a.scale) * kLog2e;
+    // the most keys that a sequence's queries see
+    const int64_t room = (int64_t)a.table_width << a.page_shift, reach = (int64_t)a.window + a.max_q;
+    const Plan p = plan_attention(a.seqs, a.max_q, a.window && reach < room ? reach : room, a.hq, a.cache.kv_heads, a.cache.head_dim, fp16);
     switch (a.cache.head_dim) {
         case 64: return go_dim<64>(a, p, fp16, stream);
         case 128: return go_dim<128>(a, p, fp16, stream);

@@ -235,7 +235,7 @@ struct AttnArgs {
     int64_t table_stride;
     int table_width;
     const int32_t* context;
-    float scale;
+    float scale, scale_log2;            // |scale| log2(e) (set by the launcher)
     int causal, window;                 // window 0: none
     uint8_t* ws;
     int64_t ws_skip;                    // floats of the counters at its start (set by the launcher)
