@@ -1343,22 +1343,27 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
     }
 }
 
+// A workgroup joins `per` rows of a pair, one after another.
 template <int D, bool FP16>
-__global__ __launch_bounds__(256) void prefill_join_kernel(const AttnArgs a, const int tiles_max, const int ks, const int tile_rows) {
-    const uint32_t pair = blockIdx.x / (uint32_t)(a.max_q * a.group);
-    const int row = (int)(blockIdx.x - pair * (uint32_t)(a.max_q * a.group));
+__global__ __launch_bounds__(256) void prefill_join_kernel(const AttnArgs a, const int tiles_max, const int ks, const int tile_rows,
+                                                           const int per) {
+    const uint32_t blocks = (uint32_t)((a.max_q * a.group + per - 1) / per);
+    const uint32_t pair = blockIdx.x / blocks;
+    const int row0 = (int)(blockIdx.x - pair * blocks) * per;
     const int sq = pair / a.cache.kv_heads, head = pair - sq * a.cache.kv_heads;
     const Seq s = seq_of(a, sq);
-    if (row >= s.qlen * a.group) return;
-    const int tile = row / tile_rows;
-    const int parts = span_of<D>(a, s, tile * tile_rows, tile_rows, ks).parts;
-    if (parts == 1) return;
-    const int tok = row / a.group, h = row - tok * a.group;
-    uint16_t* dst = a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
     const float* ws = reinterpret_cast<const float*>(a.ws) + a.ws_skip;
     const int64_t size = part_floats(tile_rows, D);
-    join_row<D, FP16>(parts, tile_rows, row - tile * tile_rows, dst,
-                      [&](int i) { return ws + (((int64_t)pair * tiles_max + tile) * ks + i) * size; });
+    for (int row = row0; row < min(row0 + per, s.qlen * a.group); ++row) {
+        const int tile = row / tile_rows;
+        const int parts = span_of<D>(a, s, tile * tile_rows, tile_rows, ks).parts;
+        if (parts == 1) continue;
+        const int tok = row / a.group, h = row - tok * a.group;
+        uint16_t* dst = a.out + ((int64_t)(s.q0 + tok) * a.hq + head * a.group + h) * D;
+        join_row<D, FP16>(parts, tile_rows, row - tile * tile_rows, dst,
+                          [&](int i) { return ws + (((int64_t)pair * tiles_max + tile) * ks + i) * size; });
+        __syncthreads();                            // join_row's LDS is read
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1379,13 +1384,13 @@ constexpr int decode_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 
 constexpr int prefill_waves(int D, bool fp16) { return D == 256 && fp16 ? 4 : 8; }
 
 // Parts of the keys: what fills whole rounds of the CUs best, fewest first; a
-// step up has to fill a tenth more.  Two rounds and more of row tiles are not cut.
+// step up has to fill a tenth more; `most` for the longest context.  Two rounds and more of row tiles are not cut.
 constexpr int kSplitRounds = 3;
-int split_of(int64_t grid, int64_t cus) {
+int split_of(int64_t grid, int64_t cus, int64_t most) {
     if (grid >= 2 * cus) return 1;
     int best = 1;
     double fill = 0;
-    for (int64_t ks = 1; grid * ks <= kSplitRounds * cus; ++ks) {
+    for (int64_t ks = 1; ks <= most && grid * ks <= kSplitRounds * cus; ++ks) {
         const int64_t rounds = (grid * ks + cus - 1) / cus;
         const double f = (double)(grid * ks) / (double)(rounds * cus);
         if (f > 1.1 * fill) best = (int)ks, fill = f;
@@ -1406,7 +1411,7 @@ Plan plan_attention(int64_t seqs, int64_t max_q, int64_t keys, int hq, int hk, i
     }
     p.nw = prefill_waves(D, fp16);
     p.tiles = (int)((rows + 32 * p.nw - 1) / (32 * p.nw));
-    p.ks = split_of(seqs * hk * p.tiles, device_cus());
+    p.ks = split_of(seqs * hk * p.tiles, device_cus(), keys / (prefill_keys(D) * kPartSteps));
     return p;
 }
 
@@ -1425,7 +1430,6 @@ hipError_t go_decode(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st
 template <int D>
 hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
     hipError_t e;
-    const dim3 join((unsigned)((int64_t)a.seqs * a.cache.kv_heads * a.max_q * a.group));
     if (p.decode) {
         if (p.nt == 1) return go_decode<D, 1>(a, p, fp16, st);
         if (p.nt == 2) return go_decode<D, 2>(a, p, fp16, st);
@@ -1437,8 +1441,13 @@ hipError_t go_dim(const AttnArgs& a, const Plan& p, bool fp16, hipStream_t st) {
     else prefill_kernel<D, 2, 8><<<grid, 64 * p.nw, 0, st>>>(a, p.tiles, p.ks);
     e = hipGetLastError();
     if (e != hipSuccess || p.ks == 1) return e;
-    if (fp16) prefill_join_kernel<D, true><<<join, 256, 0, st>>>(a, p.tiles, p.ks, 32 * p.nw);
-    else prefill_join_kernel<D, false><<<join, 256, 0, st>>>(a, p.tiles, p.ks, 32 * p.nw);
+    // rows per workgroup: about eight of them on a CU, most with nothing to join where contexts are short
+    const int64_t pairs = (int64_t)a.seqs * a.cache.kv_heads, rows = (int64_t)a.max_q * a.group;
+    const int64_t share = pairs * rows / (8 * (int64_t)device_cus());
+    const int per = (int)(share < 1 ? 1 : share > 8 ? 8 : share);
+    const dim3 join((unsigned)(pairs * ((rows + per - 1) / per)));
+    if (fp16) prefill_join_kernel<D, true><<<join, 256, 0, st>>>(a, p.tiles, p.ks, 32 * p.nw, per);
+    else prefill_join_kernel<D, false><<<join, 256, 0, st>>>(a, p.tiles, p.ks, 32 * p.nw, per);
     return hipGetLastError();
 }
 
