@@ -196,7 +196,9 @@ __device__ __forceinline__ uint32_t encode8(const float (&v)[8], int mode, uint3
 // the longest) of 64 / (D/8) neighbouring tokens, one token to a group of D/8
 // lanes: the wave takes one path, the factors are made once for its heads, their
 // loads are in flight together, and neighbouring tokens' exponent bytes are
-// written together.
+// written together.  Bound by HBM from some thousand tokens on: 16384 tokens x 28 heads
+// of 256 dims 87 us, 5.4 TB/s; the append of 16381 (24 / 4 heads) 102 us, where the
+// cached keys' fp64 weighs too; a single token is the launch.
 template <int HPU, bool CACHE>
 struct Units {
     int q, k, v;
@@ -344,10 +346,12 @@ hipError_t rows_go(const HeadRows& a, bool fp16, hipStream_t s) {
 }
 template <int D>
 hipError_t rows_dim(const HeadRows& a, bool fp16, hipStream_t s) {
-    // four heads to a wave where that still leaves every CU four workgroups
+    // four heads to a wave where that still leaves every CU two workgroups (28 heads of 256
+    // dims, one and four: 512 tokens 6.1 and 6.2 us, 1024 tokens 9.7 and 9.2, 16384 tokens
+    // 129 and 87; appended with the read back 16381 tokens 247 and 121)
     constexpr int TB = 64 / (D / 8);
     const int64_t waves = (a.tokens + TB - 1) / TB * ((a.hq + 3) / 4 + (a.hk + 3) / 4 + (a.hv + 3) / 4);
-    return waves >= (int64_t)device_cus() * 4 * (kThreads / 64) ? rows_go<D, 4>(a, fp16, s) : rows_go<D, 1>(a, fp16, s);
+    return waves >= (int64_t)device_cus() * 2 * (kThreads / 64) ? rows_go<D, 4>(a, fp16, s) : rows_go<D, 1>(a, fp16, s);
 }
 
 }  // namespace
