@@ -615,7 +615,8 @@ w4a8_status w4a8_kv_read_mxfp4(const w4a8_kv_cache *cache, int64_t tokens, const
  * d_ws: w4a8_attention_workspace_bytes(seqs, max_q, ...) bytes, 256-byte aligned;
  * one sized for more sequences and query tokens of the same heads serves smaller
  * calls too.  Its first w4a8_attention_counter_bytes() bytes must be zero before
- * the first call (w4a8_workspace_init); every call leaves them zero.  UNSUPPORTED_SHAPE: seqs * kv_heads * the table's keys / 64, or
+ * the first call (w4a8_workspace_init); every call leaves them zero.
+ * UNSUPPORTED_SHAPE: seqs * kv_heads * (the table's keys / 64 + 16), or
  * seqs * q_heads * max_q, of 2^30 and more. */
 size_t      w4a8_attention_counter_bytes(void);
 size_t      w4a8_attention_workspace_bytes(int64_t seqs, int64_t max_q, int q_heads, int kv_heads, int head_dim);

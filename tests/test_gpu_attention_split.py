@@ -73,6 +73,18 @@ def test_block_table_past_its_copy():
     Case([(70, 20000)] + [(70, 70)] * 64, 8, 8, 64, 16, BF, seed=3).check()
 
 
+@pytest.mark.parametrize("hq,hk,d,dtype", [(2, 2, 64, BF), (4, 2, 128, HF), (6, 1, 256, BF), (6, 1, 256, HF)])
+@pytest.mark.parametrize("q_len,ctx", [(90, 60), (5, 2), (4, 0)])
+def test_queries_without_keys_may_hold_anything(hq, hk, d, dtype, q_len, ctx):
+    say("attention queries without keys", (hq, hk, d, dtype, q_len, ctx))
+    c = Case([(q_len, ctx), (2, 40)], hq, hk, d, 16, dtype, seed=11)
+    clean = c.run()
+    none = q_len - ctx
+    c.q[:none:2], c.q[1:none:2, :, 3] = float("nan"), float("inf")
+    got = c.run()
+    assert (got[:none] == 0).all() and torch.equal(got, clean)
+
+
 def test_the_layer_example():
     path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
     spec = importlib.util.spec_from_file_location("attention_layer", path)

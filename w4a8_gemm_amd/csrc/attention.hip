@@ -1012,6 +1012,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
         }
         most = max(most, (uint32_t)__shfl_xor((int)most, 32));
         const float up = row_power(most, a, &mult);
+        if (r_hi <= r_lo) mult = 1.0f;              // no keys: zeros, whatever the query holds
 #pragma unroll
         for (int c = 0; c < 2 * S; ++c) {
             uint32_t x[8];

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxCount = (int64_t)1 << 30;
 constexpr int kMaxHeads = 1024;
+constexpr int kSegmentTiles = 16;   // at most what a segment counts for beside its tiles (attention.hip)
 
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -163,7 +164,7 @@ w4a8_status w4a8_attention_mxfp4(const w4a8_kv_cache* cache, w4a8_float type, co
     if (!d_cu_q && (tokens != seqs || max_q != 1)) return W4A8_ERR_INVALID_ARG;
     if (tokens >= kMaxCount / q_heads || seqs >= kMaxCount || max_q >= kMaxCount / (seqs * q_heads) ||
         table_width >= kMaxCount / cache->page ||
-        (table_width * cache->page + 63) / 64 >= kMaxCount / (seqs * cache->kv_heads))
+        (table_width * cache->page + 63) / 64 + kSegmentTiles >= kMaxCount / (seqs * cache->kv_heads))
         return W4A8_ERR_UNSUPPORTED_SHAPE;
     const size_t need = attention_workspace_bytes(seqs, max_q, q_heads, cache->kv_heads, cache->head_dim);
     if (need && (!d_ws || ws_bytes < need || !aligned(d_ws, 256))) return W4A8_ERR_WORKSPACE;
