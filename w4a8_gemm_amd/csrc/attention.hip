@@ -902,12 +902,13 @@ struct PrefillLds {
 
 // Copies of 16 or 4 bytes a lane from p to LDS at base + lane's place.  Inline, as
 // the compiler would drain them before every LDS read; awaited by wait_copies.
-// No register is written, so none can be reused under a copy in flight.
+// No register is written, so none can be reused under a copy in flight.  m0 takes a
+// wait state to reach the copy that reads it; the compiler adds none in asm.
 __device__ __forceinline__ void copy16(const uint8_t* p, uint32_t base) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(base) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(const uint8_t* p, uint32_t base) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(base) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(base) : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {   // at most N of this wave's still in flight

@@ -2049,12 +2049,13 @@ __device__ __forceinline__ i32x4 make_rsrc(const void* base, uint64_t bytes) {
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(p));
 }
+// (m0 takes a wait state to reach the copy that reads it; the compiler adds none in asm)
 __device__ __forceinline__ void lds_dma16(const i32x4& rs, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  ::"v"(voff), "s"(rs), "s"(soff), "s"(lds) : "memory", "m0");
 }
 __device__ __forceinline__ void lds_dma4(const i32x4& rs, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
                  ::"v"(voff), "s"(rs), "s"(soff), "s"(lds) : "memory", "m0");
 }
 
