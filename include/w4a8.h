@@ -609,8 +609,10 @@ w4a8_status w4a8_kv_read_mxfp4(const w4a8_kv_cache *cache, int64_t tokens, const
  * queries to `tokens` and max_q: rows past max_q are not written).  A table entry
  * outside the cache, a NaN block, or a value block whose exponent byte is 253 or
  * 254 makes the scores of its keys NaN; keys that a query does not see never
- * reach its output, whatever the cache holds there.  Scores and sums are fp32, the
- * probabilities are rounded to bf16 (fp16 queries: to two bf16 pieces).
+ * reach its output, whatever the cache holds there.  Scores and sums are fp32; the
+ * probabilities are held in two bf16 pieces (2^-16 of each), but with bf16 queries and
+ * more than 64 rows (query tokens x heads of a key head; 32 with 256 dims) rounded to
+ * bf16.
  *
  * d_ws: w4a8_attention_workspace_bytes(seqs, max_q, ...) bytes, 256-byte aligned;
  * one sized for more sequences and query tokens of the same heads serves smaller

@@ -17,10 +17,14 @@
 // 1/256 are the operand's scale; 2^(e-7) and the softmax scale multiply the
 // fp32 score.
 //
-// p.v runs in bf16: an e2m1 value times a power of two is exact in it, p is
-// rounded to bf16 (relative 2^-8 at most, as the output's own rounding; fp16
-// queries take p as two bf16 pieces, relative 2^-16).  Scores, sums and outputs
-// accumulate in fp32.
+// p.v runs in bf16, where an e2m1 value times a power of two is exact, with p as
+// the sum of two bf16 pieces (relative 2^-16): few query rows take them in the time
+// of one, as the keys' bytes bound them (the cases below 68 and 70 us either way; 30
+// rows with 256 dims 59 us for 54, 56 with 128 dims 86 for 74).  Prompts of bf16
+// queries, which the matrix pipe bounds, round p to one piece, relative 2^-8 at most
+// as the output's own rounding: two took 1482 us for 880 in prompts of 8191 and 3533
+// tokens (24 / 4 heads of 256 dims, whose registers spill) and 2654 for 2030 in two of
+// 8192 unmasked (32 / 8 of 128).  Scores, sums and outputs accumulate in fp32.
 //
 // Values whose exponent byte is 253 or more (NaN blocks; magnitudes at the end
 // of bf16's range) count as NaN: their key's score becomes NaN, and the value
@@ -147,11 +151,11 @@ __device__ __forceinline__ uint32_t bad_bytes(uint32_t x) {
     return (f << 1) - (f >> 7);
 }
 
-// p as bf16 pieces: the rounded values, and (PC == 3) the rounded rest
-template <int PC>
+// p as bf16 pieces: the rounded values, and (TWO) the rounded rest
+template <bool TWO>
 __device__ __forceinline__ void pack_p(const float* p, uint32_t* hi, uint32_t* lo) {
     *hi = pack_bf16(p[0], p[1]);
-    if (PC == 3) *lo = pack_bf16(p[0] - __uint_as_float(*hi << 16), p[1] - __uint_as_float(*hi & 0xFFFF0000u));
+    if (TWO) *lo = pack_bf16(p[0] - __uint_as_float(*hi << 16), p[1] - __uint_as_float(*hi & 0xFFFF0000u));
 }
 
 // bf16 pairs of the e2m1 codes of byte B of x, times the power of two s
@@ -656,7 +660,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : decode_waves(D, NT)) void de
                         l[nt] += p[e];
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) pack_p<PC>(p + 2 * e, &pf[nt][st][e], &pl[nt][st][e]);
+                    for (int e = 0; e < 4; ++e) pack_p<true>(p + 2 * e, &pf[nt][st][e], &pl[nt][st][e]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -687,9 +691,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : decode_waves(D, NT)) void de
                         for (int nt = 0; nt < NT; ++nt) {
                             o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                                 av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pf[nt][st])), o[nt][j], 0, 0, 0);
-                            if (PC == 3)
-                                o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pl[nt][st])), o[nt][j], 0, 0, 0);
+                            o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                av, __builtin_bit_cast(v8h, *reinterpret_cast<const uint4*>(pl[nt][st])), o[nt][j], 0, 0, 0);
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);   // one pair's words at a time, or they fill the registers
@@ -1221,7 +1224,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void prefill_kernel(const AttnArgs
                         p[x] = __builtin_amdgcn_exp2f(fmaf(sc[kt][8 * st + 2 * e + x], mult, -mu));
                         l += p[x];
                     }
-                    pack_p<PC>(p, &pf[kt][st][e], &pl[kt][st][e]);
+                    pack_p<PC == 3>(p, &pf[kt][st][e], &pl[kt][st][e]);
                 }
     };
 
