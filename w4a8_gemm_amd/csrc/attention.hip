@@ -1484,8 +1484,10 @@ hipError_t launch_attention(const AttnArgs& args, bool fp16, hipStream_t stream)
     AttnArgs a = args;
     a.ws_skip = (int64_t)attention_counter_bytes() / 4;
     a.scale_log2 = fabsf(a.scale) * kLog2e;
+    const int64_t room = (int64_t)a.table_width << a.page_shift;
+    if (a.window >= room) a.window = 0;             // none; key_lo's differences stay above -2^31
     // the most keys that a sequence's queries see
-    const int64_t room = (int64_t)a.table_width << a.page_shift, reach = (int64_t)a.window + a.max_q;
+    const int64_t reach = (int64_t)a.window + a.max_q;
     const Plan p = plan_attention(a.seqs, a.max_q, a.window && reach < room ? reach : room, a.hq, a.cache.kv_heads, a.cache.head_dim, fp16);
     switch (a.cache.head_dim) {
         case 64: return go_dim<64>(a, p, fp16, stream);
