@@ -138,6 +138,15 @@ class AttentionWorkspace:
         self.buf[:binding.lib().w4a8_attention_counter_bytes()].zero_()
 
 
+def _buf(workspace):
+    if workspace is None:
+        return None
+    # the linears' Workspace keeps partial results where the joins' counters must be zero
+    if not isinstance(workspace, AttentionWorkspace):
+        raise TypeError("workspace must be an AttentionWorkspace")
+    return workspace.buf
+
+
 def attention_mxfp4(q: torch.Tensor, cache: KVCacheMXFP4, block_table: torch.Tensor, context_lens: torch.Tensor,
                     cu_q: torch.Tensor | None = None, max_q: int = 1, scale: float | None = None, causal: bool = True,
                     window: int = 0, workspace: AttentionWorkspace | None = None,
@@ -149,4 +158,4 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCacheMXFP4, block_table: torch.Ten
     query sees the last `window` keys up to its own.  Without a workspace one is
     allocated for the call."""
     return _native().attention(q, _cache(cache), block_table, context_lens, cu_q, max_q, scale, causal, window,
-                               None if workspace is None else workspace.buf, out)
+                               _buf(workspace), out)
