@@ -534,7 +534,9 @@ size_t      w4a8_mxfp4_gemm_prepared_noalloc_max_scratch(void);
  *
  * 16-bit activations are bf16 or fp16 (w4a8_float); strides are in elements,
  * the head_dim values of a head are contiguous.  head_dim is 64, 128 or 256
- * (else UNSUPPORTED_SHAPE), heads at most 1024, tokens x heads < 2^30.
+ * (else UNSUPPORTED_SHAPE), heads at most 1024, tokens x heads < 2^30 and no
+ * launch of 2^32 threads (else UNSUPPORTED_SHAPE: head rows x head_dim / 8 of
+ * 2^32, or prompts of 2^23 sequences x key heads, are refused).
  * Inputs may be non-finite here: see each call. */
 typedef enum { W4A8_BF16 = 0, W4A8_FP16 = 1 } w4a8_float;
 

@@ -1480,15 +1480,26 @@ size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, in
     return attention_counter_bytes() + (size_t)floats * 4;
 }
 
+namespace {
+Plan plan_of(const AttnArgs& a, bool fp16) {
+    // the most keys that a sequence's queries see
+    const int64_t room = (int64_t)a.table_width << a.page_shift, reach = (int64_t)a.window + a.max_q;
+    return plan_attention(a.seqs, a.max_q, a.window && reach < room ? reach : room, a.hq, a.cache.kv_heads, a.cache.head_dim, fp16);
+}
+}  // namespace
+
+int64_t attention_threads(const AttnArgs& a, bool fp16) {
+    const Plan p = plan_of(a, fp16);
+    return p.decode ? (int64_t)64 * p.nw * p.workgroups : (int64_t)a.seqs * a.cache.kv_heads * p.tiles * p.ks * 64 * p.nw;
+}
+
 hipError_t launch_attention(const AttnArgs& args, bool fp16, hipStream_t stream) {
     AttnArgs a = args;
     a.ws_skip = (int64_t)attention_counter_bytes() / 4;
     a.scale_log2 = fabsf(a.scale) * kLog2e;
     const int64_t room = (int64_t)a.table_width << a.page_shift;
     if (a.window >= room) a.window = 0;             // none; key_lo's differences stay above -2^31
-    // the most keys that a sequence's queries see
-    const int64_t reach = (int64_t)a.window + a.max_q;
-    const Plan p = plan_attention(a.seqs, a.max_q, a.window && reach < room ? reach : room, a.hq, a.cache.kv_heads, a.cache.head_dim, fp16);
+    const Plan p = plan_of(a, fp16);
     switch (a.cache.head_dim) {
         case 64: return go_dim<64>(a, p, fp16, stream);
         case 128: return go_dim<128>(a, p, fp16, stream);

@@ -81,6 +81,7 @@ w4a8_status w4a8_qk_norm_rope(w4a8_float type, const uint16_t* d_q, int64_t q_st
     a.interleaved = interleaved != 0;
     a.q_out = d_q_out, a.k_out = d_k_out;
     a.cache.head_dim = head_dim;
+    if (head_rows_threads(a) >= kGridThreads) return W4A8_ERR_UNSUPPORTED_SHAPE;
     return hip_status(launch_head_rows(a, type == W4A8_FP16, as_stream(stream)));
 }
 
@@ -120,6 +121,7 @@ w4a8_status w4a8_kv_append_mxfp4(const w4a8_kv_cache* cache, w4a8_float type, co
     a.page_shift = page_shift_of(cache->page);
     a.slots = d_slots;
     a.mode = (int)mode;
+    if (head_rows_threads(a) >= kGridThreads) return W4A8_ERR_UNSUPPORTED_SHAPE;
     return hip_status(launch_head_rows(a, type == W4A8_FP16, as_stream(stream)));
 }
 
@@ -130,7 +132,8 @@ w4a8_status w4a8_kv_read_mxfp4(const w4a8_kv_cache* cache, int64_t tokens, const
     if (tokens < 1 || !d_slots || !d_k_out || !d_v_out || !aligned(d_slots, 8) || !aligned(d_k_out, 16) ||
         !aligned(d_v_out, 16))
         return W4A8_ERR_INVALID_ARG;
-    if (tokens >= kMaxCount / (2 * cache->kv_heads)) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    if (tokens >= kMaxCount / (2 * cache->kv_heads) || kv_read_threads(*cache, tokens) >= kGridThreads)
+        return W4A8_ERR_UNSUPPORTED_SHAPE;
     return hip_status(launch_kv_read(*cache, page_shift_of(cache->page), tokens, d_slots, d_k_out, d_v_out,
                                      as_stream(stream)));
 }
@@ -182,6 +185,7 @@ w4a8_status w4a8_attention_mxfp4(const w4a8_kv_cache* cache, w4a8_float type, co
     a.scale = scale;
     a.causal = causal != 0, a.window = window;
     a.ws = static_cast<uint8_t*>(d_ws);
+    if (attention_threads(a, type == W4A8_FP16) >= kGridThreads) return W4A8_ERR_UNSUPPORTED_SHAPE;
     return hip_status(launch_attention(a, type == W4A8_FP16, as_stream(stream)));
 }
 

@@ -206,6 +206,7 @@ struct Units {
         : q((a.hq + HPU - 1) / HPU), k(CACHE ? a.hk : (a.hk + HPU - 1) / HPU), v((a.hv + HPU - 1) / HPU) {}
     __host__ __device__ int all() const { return q + k + v; }
 };
+constexpr int64_t token_blocks(int64_t tokens, int D) { return (tokens + 512 / D - 1) / (512 / D); }
 
 template <int D, bool FP16, int HPU, bool CACHE>
 __global__ __launch_bounds__(kThreads) void head_rows_kernel(const HeadRows a) {
@@ -330,9 +331,9 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(const w4a8_kv_cache c
 
 template <int D, int HPU>
 hipError_t rows_go(const HeadRows& a, bool fp16, hipStream_t s) {
-    constexpr int TB = 64 / (D / 8);
-    const int64_t blocks = (a.tokens + TB - 1) / TB;
-    const auto grid = [&](int units) { return dim3((unsigned)((blocks * units + kThreads / 64 - 1) / (kThreads / 64))); };
+    const auto grid = [&](int units) {
+        return dim3((unsigned)((token_blocks(a.tokens, D) * units + kThreads / 64 - 1) / (kThreads / 64)));
+    };
     if (a.slots) {
         const dim3 g = grid(Units<HPU, true>(a).all());
         if (fp16) head_rows_kernel<D, true, HPU, true><<<g, kThreads, 0, s>>>(a);
@@ -344,17 +345,28 @@ hipError_t rows_go(const HeadRows& a, bool fp16, hipStream_t s) {
     }
     return hipGetLastError();
 }
+// four heads to a wave where that still leaves every CU two workgroups (28 heads of 256
+// dims, one and four: 512 tokens 6.1 and 6.2 us, 1024 tokens 9.7 and 9.2, 16384 tokens
+// 129 and 87; appended with the read back 16381 tokens 247 and 121)
+bool four_heads(const HeadRows& a) {
+    const int64_t waves = token_blocks(a.tokens, a.cache.head_dim) * ((a.hq + 3) / 4 + (a.hk + 3) / 4 + (a.hv + 3) / 4);
+    return waves >= (int64_t)device_cus() * 2 * (kThreads / 64);
+}
 template <int D>
 hipError_t rows_dim(const HeadRows& a, bool fp16, hipStream_t s) {
-    // four heads to a wave where that still leaves every CU two workgroups (28 heads of 256
-    // dims, one and four: 512 tokens 6.1 and 6.2 us, 1024 tokens 9.7 and 9.2, 16384 tokens
-    // 129 and 87; appended with the read back 16381 tokens 247 and 121)
-    constexpr int TB = 64 / (D / 8);
-    const int64_t waves = (a.tokens + TB - 1) / TB * ((a.hq + 3) / 4 + (a.hk + 3) / 4 + (a.hv + 3) / 4);
-    return waves >= (int64_t)device_cus() * 2 * (kThreads / 64) ? rows_go<D, 4>(a, fp16, s) : rows_go<D, 1>(a, fp16, s);
+    return four_heads(a) ? rows_go<D, 4>(a, fp16, s) : rows_go<D, 1>(a, fp16, s);
 }
 
 }  // namespace
+
+int64_t head_rows_threads(const HeadRows& a) {
+    const int units = four_heads(a) ? (a.slots ? Units<4, true>(a).all() : Units<4, false>(a).all())
+                                    : (a.slots ? Units<1, true>(a).all() : Units<1, false>(a).all());
+    return 64 * token_blocks(a.tokens, a.cache.head_dim) * units + kThreads;
+}
+int64_t kv_read_threads(const w4a8_kv_cache& c, int64_t tokens) {
+    return tokens * 2 * c.kv_heads * (c.head_dim / 8) + kThreads;
+}
 
 hipError_t launch_head_rows(const HeadRows& a, bool fp16, hipStream_t stream) {
     switch (a.cache.head_dim) {

@@ -216,6 +216,10 @@ struct HeadRows {
     const int64_t* slots;
     int mode;
 };
+// Threads of the launches, rounded up; a grid holds fewer than kGridThreads of them.
+constexpr int64_t kGridThreads = (int64_t)1 << 32;
+int64_t head_rows_threads(const HeadRows& a);
+int64_t kv_read_threads(const w4a8_kv_cache& c, int64_t tokens);
 hipError_t launch_head_rows(const HeadRows& a, bool fp16, hipStream_t stream);
 hipError_t launch_kv_read(const w4a8_kv_cache& c, int page_shift, int64_t tokens, const int64_t* slots, uint16_t* k_out,
                           uint16_t* v_out, hipStream_t stream);
@@ -242,6 +246,7 @@ struct AttnArgs {
 };
 size_t attention_counter_bytes();
 size_t attention_workspace_bytes(int64_t seqs, int64_t max_q, int hq, int hk, int head_dim);
+int64_t attention_threads(const AttnArgs& a, bool fp16);
 hipError_t launch_attention(const AttnArgs& a, bool fp16, hipStream_t stream);
 int device_cus();   // CUs of the current device (cached per device)
 
