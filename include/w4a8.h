@@ -548,7 +548,11 @@ typedef enum { W4A8_BF16 = 0, W4A8_FP16 = 1 } w4a8_float;
  * page: rows per page, a power of two from 16 to 1024; pages >= 1 and
  * pages * page < 2^40.  Token i of a sequence lies in row i % page of the page
  * that entry i / page of its block table names.  An exponent byte 255 marks a
- * block that held a non-finite value: it reads as NaN. */
+ * block that held a non-finite value: it reads as NaN.  Byte 0 (2^-127) reads as
+ * any other.  At the other end e2m1 times 2^126 passes fp32: W4A8_EXP_NOCLIP gives
+ * magnitudes over 1.5 x 2^127 byte 253, which in values counts as NaN in the
+ * attention (below), and those of 1.75 x 2^127 and more read back as infinity;
+ * W4A8_EXP_OCP stays at byte 252, whose codes saturate at 1.5 x 2^127. */
 typedef struct {
     uint8_t *k_codes, *k_e8m0, *v_codes, *v_e8m0;
     int64_t pages;

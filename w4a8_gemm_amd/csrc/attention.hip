@@ -163,7 +163,8 @@ template <int B>
 __device__ __forceinline__ uint32_t fp4_pair(uint32_t x, float s) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, B));
 }
-// an exponent byte in place of an fp32's exponent: 2^(byte - 127)
+// an exponent byte in place of an fp32's exponent: 2^(byte - 127) to the conversions,
+// which read that field alone, 0 too
 template <int B>
 __device__ __forceinline__ float byte_scale(uint32_t x) {
     const uint32_t s = B == 3 ? x >> 1 : B == 2 ? x << 7 : B == 1 ? x << 15 : x << 23;
