@@ -211,9 +211,10 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-extra", action="store_true", help="skip the prefill/requant/variant loops")
     ap.add_argument("--cpu-rows", type=int, default=34816, help="weight rows in the all-threads oracle sample")
-    ap.add_argument("--pmc-probe", choices=["decode", "prefill", "requant", "tiles"],
+    ap.add_argument("--pmc-probe", choices=["decode", "prefill", "requant", "tiles", "attention"],
                     help="only the launches a counter record is read on (run under rocprofv3 --pmc): a 1 GiB "
-                         "device copy (calibration), then the kernel of interest")
+                         "device copy (calibration), then the kernel of interest (attention: --warmup and then "
+                         "--steps passes of each recorded case of perf/operators.py)")
     ap.add_argument("--probe-m", type=int, default=64, help="decode probe: the step's M whose GEMM is probed")
     ap.add_argument("--trace-summarize", metavar="DIR",
                     help="turn a rocprofv3 --kernel-trace --stats output directory of the default run into "
@@ -221,7 +222,8 @@ def main():
     ap.add_argument("--pmc-summarize", nargs="+", metavar="ARG",
                     help="KIND DIR [DIR ...]: turn rocprofv3 --pmc output directories into a record under "
                          "profiles/ (decode: FETCH_SIZE dir, WRITE_SIZE dir; prefill: the SQ/GRBM dir; "
-                         "requant and tiles: FETCH_SIZE dir, WRITE_SIZE dir, SQ/GRBM dir)")
+                         "requant and tiles: FETCH_SIZE dir, WRITE_SIZE dir, SQ/GRBM dir; attention: the same "
+                         "three after the kernel trace's)")
     args = ap.parse_args()
     if args.trace_summarize:
         trace_summarize(args.trace_summarize)
@@ -244,6 +246,9 @@ def main():
     timer = Timer(torch)
     log = lambda *m: print("[bench]", *m, file=sys.stderr, flush=True)
 
+    if args.pmc_probe == "attention":
+        pmc_probe_attention(torch, dev, args.warmup, args.steps, log)
+        return
     if args.pmc_probe in ("prefill", "requant", "tiles"):
         pmc_probe_other(args.pmc_probe, torch, w4, synth, dev, log)
         return
@@ -448,6 +453,34 @@ def pmc_probe_other(kind, torch, w4, synth, dev, log):
     log("pmc probe done")
 
 
+# (case of perf/operators.py, kernel, what the record calls it)
+ATTENTION_KERNELS = [
+    ("norm_rope prompts", "head_rows_kernel<256, false, 4, false>", "head norms, 4 heads to a wave"),
+    ("append prompts", "head_rows_kernel<256, false, 4, true>", "append with the queries' norms, 4 heads to a wave"),
+    ("append prompts", "kv_read_kernel<256>", "read back"),
+    ("attention decode batch", "decode_kernel<128, 1, 2, 4>", "four waves"),
+    ("attention long context", "decode_kernel<256, 1, 2, 8>", "eight waves"),
+    ("attention prompts", "prefill_kernel<256, 2, 8>", "eight waves"),
+    ("attention one token", "decode_kernel<256, 1, 2, 4>", "four waves"),
+]
+
+
+def pmc_probe_attention(torch, dev, warmup, steps, log):
+    """Passes of the recorded cases, on two states of each in turn."""
+    import perf.operators as ops
+    ops.own = True
+    _calibration_copy(torch, dev)
+    recorded = {c for c, _, _ in ATTENTION_KERNELS}
+    for case in ops.listed():
+        if case["name"] in recorded:
+            states = [ops.prepare(case, seed) for seed in range(2)]
+            for r in range(warmup + steps):
+                ops.run(states[r % 2])
+            torch.cuda.synchronize()
+            log(case["name"], "done")
+    log("pmc probe done")
+
+
 def _per_dispatch(d, counters):
     """{counter: [(kernel name, grid, value summed over the dispatch)]} from
     the counter_collection.csv files under rocprofv3 output directory d."""
@@ -611,6 +644,8 @@ def pmc_summarize(kind, dirs, probe_m):
         ]
     elif kind == "tiles":
         lines, path = _tiles_record(dirs)
+    elif kind == "attention":
+        lines, path = _attention_record(dirs)
     else:
         f = _per_dispatch(dirs[0], ["FETCH_SIZE"])["FETCH_SIZE"]
         w = _per_dispatch(dirs[1], ["WRITE_SIZE"])["WRITE_SIZE"]
@@ -656,6 +691,68 @@ def pmc_summarize(kind, dirs, probe_m):
     with open(path, "w") as fh:
         fh.write("\n".join(lines) + "\n")
     print("\n".join(lines))
+
+
+ATTENTION_SQ = ["SQ_INSTS_VALU", "SQ_INSTS_MFMA", "SQ_VALU_MFMA_BUSY_CYCLES", "SQ_LDS_BANK_CONFLICT",
+                "SQ_LDS_IDX_ACTIVE", "GRBM_GUI_ACTIVE"]
+ATTENTION_PASSES = 20           # of the trace, after the warm-up passes: those that count
+
+
+def _attention_record(dirs):
+    """Record of the attention block's kernels: times of the trace's last passes, matrix-pipe busy,
+    LDS conflicts and HBM bytes per launch."""
+    import csv
+    import glob
+    trace = glob.glob(os.path.join(dirs[0], "**", "*kernel_trace.csv"), recursive=True)
+    if not trace:
+        raise SystemExit(f"no kernel_trace.csv under {dirs[0]}")
+    times = {}
+    for r in csv.DictReader(open(trace[0])):
+        times.setdefault(_short(r["Kernel_Name"]), []).append(
+            (int(r["Start_Timestamp"]), int(r["End_Timestamp"]) - int(r["Start_Timestamp"])))
+    f = _per_dispatch(dirs[1], ["FETCH_SIZE"])["FETCH_SIZE"]
+    w = _per_dispatch(dirs[2], ["WRITE_SIZE"])["WRITE_SIZE"]
+    c = _per_dispatch(dirs[3], ATTENTION_SQ)
+    fs, ws = _calib_scale(f), _calib_scale(w)
+
+    def mean(recs, name):
+        v = [x for n, g, x in recs if _short(n) == name]
+        if not v:
+            raise SystemExit(f"no dispatch of {name}")
+        return sum(v) / len(v)
+
+    probe = "-f csv -o run -- python3 -u bench.py --pmc-probe attention"
+    lines = [
+        "# Counter record of the attention block's kernels",
+        "",
+        "Commands (repository root, one MI355X; $OUT is an output directory):",
+        "",
+        f"    rocprofv3 --kernel-trace --stats -d $OUT/at_trace {probe} --warmup 200 --steps {ATTENTION_PASSES}",
+        f"    rocprofv3 --pmc FETCH_SIZE -d $OUT/at_fetch {probe} --warmup 0 --steps 4",
+        f"    rocprofv3 --pmc WRITE_SIZE -d $OUT/at_write {probe} --warmup 0 --steps 4",
+        f"    rocprofv3 --pmc {' '.join(ATTENTION_SQ)} -d $OUT/at_sq {probe} --warmup 0 --steps 4",
+        "    python3 bench.py --pmc-summarize attention $OUT/at_trace $OUT/at_fetch $OUT/at_write $OUT/at_sq",
+        "",
+        f"The cases are those of `perf/operators.py`. us: mean of the last {ATTENTION_PASSES} passes of the trace, at "
+        "the sustained clock. MFMA busy = SQ_VALU_MFMA_BUSY_CYCLES / SIMDs / (GRBM_GUI_ACTIVE / XCDs). HBM bytes: "
+        f"FETCH_SIZE / {fs:.4f} and WRITE_SIZE / {ws:.4f} (counter bytes per byte of a plain copy).",
+        "",
+        "| case | kernel | us | MFMA busy | VALU instr. | LDS conflicts / active | HBM read MB | HBM written MB |",
+        "|---|---|---|---|---|---|---|---|",
+    ]
+    for case, name, what in ATTENTION_KERNELS:
+        if name not in times:
+            raise SystemExit(f"no dispatch of {name} in the trace")
+        last = [t for _, t in sorted(times[name])[-ATTENTION_PASSES:]]
+        busy = mean(c["SQ_VALU_MFMA_BUSY_CYCLES"], name) / SIMDS / (mean(c["GRBM_GUI_ACTIVE"], name) / XCDS)
+        active = mean(c["SQ_LDS_IDX_ACTIVE"], name)
+        conflicts = f"{mean(c['SQ_LDS_BANK_CONFLICT'], name) / active:.2f}" if active else "-"
+        lines.append(f"| {case} | {name} ({what}) | {sum(last) / len(last) / 1e3:.1f} | {busy:.2f} | "
+                     f"{mean(c['SQ_INSTS_VALU'], name):.3g} | {conflicts} | {mean(f, name) * 1024 / fs / 1e6:.1f} | "
+                     f"{mean(w, name) * 1024 / ws / 1e6:.1f} |")
+    csrc = os.path.join(HERE, "w4a8_gemm_amd", "csrc")
+    lines += ["", *(f"{s}_source_sha256: {_source_hash(os.path.join(csrc, s + '.hip'))}" for s in ("attention", "kv_cache"))]
+    return lines, os.path.join(PROFILES, "attention_block_counters.md")
 
 
 TILE_SQ = ["SQ_VALU_MFMA_BUSY_CYCLES", "SQ_ACTIVE_INST_VALU", "SQ_INSTS_VALU", "SQ_ACTIVE_INST_LDS",
