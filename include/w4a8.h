@@ -612,7 +612,9 @@ w4a8_status w4a8_kv_read_mxfp4(const w4a8_kv_cache *cache, int64_t tokens, const
  *                   the last `window` of these; not causal: all (window must be 0)
  * A query that sees no key (context 0, or more query tokens than context) gives
  * zeros.  Lengths are clamped to the tensors they index (context to the table,
- * queries to `tokens` and max_q: rows past max_q are not written).  A table entry
+ * queries to `tokens` and max_q: rows past max_q, and those of no sequence, are not
+ * written).  Query values less than 2^-13 of their row's largest are taken to 2^-21 of
+ * it, the others exactly.  A table entry
  * outside the cache, a NaN block, or a value block whose exponent byte is 253 or
  * 254 makes the scores of its keys NaN; keys that a query does not see never
  * reach its output, whatever the cache holds there.  Scores and sums are fp32; the

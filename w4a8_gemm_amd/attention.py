@@ -155,7 +155,8 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCacheMXFP4, block_table: torch.Ten
     values of their sequences.  block_table int32 [seqs, width] (rows may be strided); context_lens
     int32 [seqs], the new tokens among them; cu_q int32 [seqs + 1] with at most max_q query
     tokens per sequence, or None for one each.  scale: head_dim ** -0.5 by default.  window > 0: each
-    query sees the last `window` keys up to its own.  Without a workspace one is
+    query sees the last `window` keys up to its own.  Output rows of no sequence, and those past
+    max_q, are not written.  Without a workspace one is
     allocated for the call."""
     return _native().attention(q, _cache(cache), block_table, context_lens, cu_q, max_q, scale, causal, window,
                                _buf(workspace), out)

@@ -18,10 +18,10 @@
 // fp32 score.
 //
 // p.v runs in bf16, where an e2m1 value times a power of two is exact, with p as
-// the sum of two bf16 pieces (relative 2^-16): few query rows take them in the time
-// of one, as the keys' bytes bound them (the cases below 68 and 70 us either way; 30
-// rows with 256 dims 59 us for 54, 56 with 128 dims 86 for 74).  Prompts of bf16
-// queries, which the matrix pipe bounds, round p to one piece, relative 2^-8 at most
+// the sum of two bf16 pieces (relative 2^-16): few query rows take them in about the
+// time of one, as the keys' bytes bound them (the two cases below 67 and 71 us, 67 and
+// 70 with one; 30 rows with 256 dims 59 for 54, 56 with 128 dims 85 for 74).  Prompts
+// of bf16 queries, which the matrix pipe bounds, round p to one piece, relative 2^-8 at most
 // as the output's own rounding: two took 1482 us for 880 in prompts of 8191 and 3533
 // tokens (24 / 4 heads of 256 dims, whose registers spill) and 2654 for 2030 in two of
 // 8192 unmasked (32 / 8 of 128).  Scores, sums and outputs accumulate in fp32.
@@ -197,7 +197,7 @@ __device__ __forceinline__ uint32_t out_pair(float a, float b) {
 // exponents and keys after the scores, values after the products.  Loads return
 // in order, so nothing that is needed early is asked for late: the block-table
 // entries of a run lie in LDS.  Bound by HBM: 64 sequences to 8192 keys (32 / 8 heads
-// of 128 dims, 308 MB) take 68 us, three to 131072 keys (24 / 4 of 256, 316 MB) 70 us;
+// of 128 dims, 308 MB) take 67 us, three to 131072 keys (24 / 4 of 256, 316 MB) 71 us;
 // the stream itself runs at 6 TB/s.
 // ===========================================================================
 template <int D>
@@ -372,18 +372,18 @@ __device__ __forceinline__ void join_pieces(__amdgpu_buffer_rsrc_t ws, SLOT slot
 
 // waves per SIMD of four-wave workgroups: the outputs of many rows need the registers
 // of two; with 64 dims there are registers for three, and the third hides changes of
-// segments (3200 segments of 1620 keys on average 98 -> 90 us; with 128 dims it spills,
-// and 512 segments took 71 us for 68)
+// segments (3200 segments of 1620 keys on average 104 -> 96 us; with 128 dims it spills,
+// and 512 segments took 72 us for 67)
 constexpr int decode_waves(int D, int NT) { return NT * (D / 16) > 16 || NT == 4 ? 1 : NT == 1 && D == 64 ? 3 : 2; }
 constexpr int kWavesMost = 3;
 
 // NW waves to a workgroup.  Eight, one workgroup to a CU, where few segments have
 // tiles for all of them: the runs are half as many pieces to join, and all waves keep
 // step (of two workgroups the older is served first: equal runs ended after 40 and 55
-// us).  Three contexts to 131072 keys 75 -> 70 us, eight of 4000 14.7 -> 13.6 us.  Four,
+// us).  Three contexts to 131072 keys 75 -> 71 us, eight of 4000 14.9 -> 13.7 us.  Four,
 // two or three workgroups to a CU, where runs cross segments, so that one streams while
-// another changes segments (64 sequences of drafts, 25.7 us with eight, 24.1 with four),
-// and for short contexts (one of 1021 keys: 15.1 and 13.7 us).
+// another changes segments (16 sequences of four drafts on 8192 keys, 26.6 us with eight,
+// 24.7 with four), and for short contexts (one of 1021 keys: 15.8 and 13.9 us).
 template <int D, int NT, int PC, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : decode_waves(D, NT)) void decode_kernel(const AttnArgs a, const int workgroups) {
     constexpr int KS = D >= 128 ? D / 128 : 1;      // 128-deep products per score
@@ -866,9 +866,9 @@ __device__ __forceinline__ void join_row(int pieces, int rows, int row, uint16_t
 // this one) and the rest (probabilities, its share of widening the values).
 // Waves w and w + 4 share a SIMD, so with eight waves the second four run half a
 // step behind: while one wave of a SIMD multiplies, the other exponentiates.  Half
-// steps are kept apart by barriers.  Prompts of 8191 and 3523 tokens (24 / 4 heads of
-// 256 dims) take 886 us, 1104 TFLOP/s, the matrix pipe busy in 44 % of the cycles; two
-// of 8192 unmasked with 32 / 8 heads of 128 dims 2.0 ms, 1090 TFLOP/s.
+// steps are kept apart by barriers.  Prompts of 8191 and 3533 tokens (24 / 4 heads of
+// 256 dims) take 885 us, 1105 TFLOP/s, the matrix pipe busy in 45 % of the cycles; two
+// of 8192 unmasked with 32 / 8 heads of 128 dims 2.05 ms, 1075 TFLOP/s.
 // In half step x (tile i):
 //   first four waves    x = 2i: products(i)           x = 2i+1: rest(i), widen(i)
 //   second four waves   x = 2i: rest(i-1), widen(i)   x = 2i+1: products(i)
@@ -876,9 +876,9 @@ __device__ __forceinline__ void join_row(int pieces, int rows, int row, uint16_t
 // the exponents of keys i+1 (over i-1), which the half step before read last.
 //
 // Codes and exponents come by direct copies to LDS, kAhead steps before their
-// use, into rings of eight tiles: keys i+1+kAhead and values i+kAhead are asked
-// for in widen(i), and what widen(i+1) and products(i+1) read is waited for
-// before the barrier that ends it.
+// use, into rings of eight tiles (two steps and four tiles with 256 dims): keys
+// i+1+kAhead and values i+kAhead are asked for in widen(i), and what widen(i+1)
+// and products(i+1) read is waited for before the barrier that ends it.
 //
 // Where there are too few workgroups for the chip the keys are cut into up to
 // `ks` parts, joined by a second kernel.
