@@ -619,7 +619,7 @@ w4a8_status w4a8_kv_read_mxfp4(const w4a8_kv_cache *cache, int64_t tokens, const
  * 254 makes the scores of its keys NaN; keys that a query does not see never
  * reach its output, whatever the cache holds there.  Scores and sums are fp32; the
  * probabilities are held in two bf16 pieces (2^-16 of each), but with bf16 queries and
- * more than 64 rows (query tokens x heads of a key head; 32 with 256 dims) rounded to
+ * more than 64 rows (max_q x query heads of a key head; 32 with 256 dims) rounded to
  * bf16.
  *
  * d_ws: w4a8_attention_workspace_bytes(seqs, max_q, ...) bytes, 256-byte aligned;
