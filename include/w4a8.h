@@ -532,13 +532,13 @@ size_t      w4a8_mxfp4_gemm_prepared_noalloc_max_scratch(void);
  * attention over it.  Not on the pages: these calls are what a serving program
  * needs between this library's linears, on the library's own MXFP4 format.
  *
- * 16-bit activations are bf16 or fp16 (w4a8_float); strides are in elements,
+ * 16-bit activations are bf16 or fp16 (w4a8_float; FP32 is INVALID_ARG here); strides are in elements,
  * the head_dim values of a head are contiguous.  head_dim is 64, 128 or 256
  * (else UNSUPPORTED_SHAPE), heads at most 1024, tokens x heads < 2^30 and no
  * launch of 2^32 threads (else UNSUPPORTED_SHAPE: head rows x head_dim / 8 of
  * 2^32, or prompts of 2^23 sequences x key heads, are refused).
  * Inputs may be non-finite here: see each call. */
-typedef enum { W4A8_BF16 = 0, W4A8_FP16 = 1 } w4a8_float;
+typedef enum { W4A8_BF16 = 0, W4A8_FP16 = 1, W4A8_FP32 = 2 } w4a8_float;
 
 /* The cache, in caller-owned device memory (16-byte aligned):
  *   k_codes, v_codes  uint8 [pages][kv_heads][page][head_dim / 2]: e2m1 codes,
@@ -636,6 +636,93 @@ w4a8_status w4a8_attention_mxfp4(const w4a8_kv_cache *cache, w4a8_float type, co
                                  const int32_t *d_block_table, int64_t table_stride, int64_t table_width,
                                  const int32_t *d_context_lens, float scale, int causal, int window,
                                  uint16_t *d_out, void *d_ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The expert half of a decoder layer: the norms around a block, with its gate and
+ * residual sum, whose result leaves as the linears' fp8 activations; the choice of
+ * each token's experts; and the experts' gated products on MXFP4 weights.  Not on
+ * the pages, but for the fp8 stream that the norm feeds ("radiance_nvfp4.py",
+ * module docstring; "vllm-radiance (MXFP4)", NVFP4 checkpoints: online
+ * requantization to MXFP4: norm and quant epilogues feeding the next linear). */
+
+/* For each of `tokens` rows of `hidden` values, in fp32, each output rounded once:
+ *   u = y                                      (type bf16 or fp16, rows ld_y apart)
+ *   u <- u (mean(u^2) + eps)^-1/2 post_weight  where d_post_weight (fp32 [hidden]) is given
+ *   u <- u gate                                where d_gate (of y's type) is given: element
+ *        (t, i) at t * gate_stride_token + i * gate_stride_col; a column stride of 1,
+ *        or 0 for one gate per token; a token stride of 0 for one per channel
+ *   r = residual + scale u                     residual (where given) bf16 / fp16 as y, or
+ *        fp32 (residual_fp32 != 0), rows ld_residual apart; without it r = scale u
+ *   h = r (mean(r^2) + eps)^-1/2 weight        (fp32 [hidden]; NULL: ones), r not yet rounded
+ * Outputs, each where its pointer is given (one at least): d_residual_out = r, in the
+ * residual's type (y's without one), rows ld_residual_out apart; d_out = h in y's type,
+ * contiguous; d_x_fp8 [tokens][hidden] and d_x_scale [tokens] (both or neither) = the e4m3
+ * codes of h / s and s = max |h| / 448 (1 for a row of zeros; rows below 2^-110 are scaled as
+ * if at 2^-110): what the linears and w4a8_moe_mxfp4 take.  A row with a NaN or
+ * infinite h has such a scale.  d_residual_out may be d_residual and d_out may be d_y with the
+ * same strides; other overlaps are not allowed.
+ * hidden from 1 to 32768 (else UNSUPPORTED_SHAPE), tokens * hidden < 2^40; 16-bit pointers
+ * 2-byte, fp32 ones 4-byte aligned.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, HIP. */
+w4a8_status w4a8_residual_norm(w4a8_float type, const uint16_t *d_y, int64_t ld_y, int64_t tokens, int64_t hidden,
+                               const float *d_post_weight, const uint16_t *d_gate, int64_t gate_stride_token,
+                               int64_t gate_stride_col, float scale, const void *d_residual, int residual_fp32,
+                               int64_t ld_residual, void *d_residual_out, int64_t ld_residual_out,
+                               const float *d_weight, float eps, uint16_t *d_out, uint8_t *d_x_fp8,
+                               float *d_x_scale, void *stream);
+
+/* The top_k experts of each token from the router's logits [tokens][experts] (bf16,
+ * fp16 or fp32, rows ld apart) and their weights:
+ *   p = softmax of the row, or 1 / (1 + exp(-logit)) (w4a8_score)
+ *   the choice goes by the logits; with a bias (fp32 [experts]) or groups > 1, by p + bias
+ *       in fp64
+ *   groups > 1: the experts form `groups` equal runs; a run counts the sum of its
+ *       group_top (1 or 2) largest choice scores, and only the groups_kept best runs take part
+ *   the top_k largest, ties to the lower index, in descending order: d_ids [tokens][top_k]
+ *   d_weights [tokens][top_k] = scale p, or scale p / (sum of the chosen p) with
+ *       renormalize != 0 (0 where that sum is 0)
+ * A logit of -inf or NaN (with a bias also a score of -inf or NaN) is an expert that is off:
+ * it is never chosen and counts as 0 in the softmax; where fewer than top_k are left the
+ * row ends in ids of -1 with weights of 0.  Logits of +inf share the softmax evenly.
+ * experts from 1 to 1024, top_k from 1 to 32 and to experts, groups a divisor of experts
+ * up to 64, groups_kept from 1 to groups (else UNSUPPORTED_SHAPE).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, HIP. */
+typedef enum { W4A8_SCORE_SOFTMAX = 0, W4A8_SCORE_SIGMOID = 1 } w4a8_score;
+w4a8_status w4a8_moe_route(w4a8_float type, const void *d_logits, int64_t ld, int64_t tokens, int experts, int top_k,
+                           w4a8_score score, const float *d_bias, int groups, int groups_kept, int group_top,
+                           int renormalize, float scale, int32_t *d_ids, float *d_weights, void *stream);
+
+/* Experts' weights, prepared (w4a8_mxfp4_prepare) as two tall matrices, 16-byte aligned:
+ *   up    [experts * 2 inter][hidden]  of each expert the gate's rows, then the up rows
+ *   down  [experts * hidden][inter]
+ * hidden and inter multiples of 128 up to 65536, experts from 1 to 1024 (else
+ * UNSUPPORTED_SHAPE). */
+typedef struct {
+    const uint8_t *up_w, *up_s, *down_w, *down_s;
+    int experts;
+    int64_t hidden, inter;
+} w4a8_experts_mxfp4;
+typedef enum { W4A8_ACT_SILU = 0, W4A8_ACT_GELU_TANH = 1 } w4a8_act;
+
+/* out[t] = bf16( sum over j < top_k of weights[t, j] v[t, j] W_down[e]^T ),  e = ids[t, j],
+ *   g, u = the two halves of s_t x8[t] W_up[e]^T        (fp32)
+ *   v    = act(g) u, act(g) = g / (1 + exp(-g)) or g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2,
+ *          held between the products as e4m3 codes with one power of two per 32 values of
+ *          inter, the least that keeps the 32 within 448 (at least 2^-127); a block with a NaN
+ *          or infinite value is NaN
+ * for activations as the linears take them (d_x_fp8 e4m3 [tokens][hidden], 16-byte aligned,
+ * d_x_scale fp32 [tokens]).  Products accumulate in fp32; the sum over j is fp32 in the order
+ * of j, so that results do not depend on timing.  A slot whose id lies outside
+ * [0, experts) is left out, its weight not looked at; a token without experts gives
+ * zeros; the same expert twice counts twice.  Two kernels, nothing allocated, no atomics on
+ * device memory.  Made for few tokens: every expert met is read once per 2048 / top_k tokens.
+ * d_ws: w4a8_moe_workspace_bytes(...) bytes, 256-byte aligned, contents of no meaning between
+ * calls; one sized for more tokens (or slots) of the same inter serves fewer.  top_k from 1
+ * to 32 and to experts, tokens * top_k < 2^30, at most 2^15 * (2048 / top_k) tokens (else
+ * UNSUPPORTED_SHAPE).  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, WORKSPACE, HIP. */
+size_t      w4a8_moe_workspace_bytes(int64_t tokens, int top_k, int64_t inter);
+w4a8_status w4a8_moe_mxfp4(const w4a8_experts_mxfp4 *experts, const uint8_t *d_x_fp8, const float *d_x_scale,
+                           int64_t tokens, const int32_t *d_ids, const float *d_weights, int top_k, w4a8_act act,
+                           uint16_t *d_out, void *d_ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Decode band with an explicit plan, for tile-size sweeps (the two GEMM entry

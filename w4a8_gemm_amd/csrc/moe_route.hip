@@ -1,0 +1,200 @@
+// moe_route.hip -- each token's experts from the router's logits.
+//
+// A wave takes a token: lane L holds the experts L, L + 64, ...  Each round of the
+// choice takes the largest key of the wave (unsigned keys in the scores' order, so
+// a maximum is one instruction a step) and, of those that hold it, the lowest
+// expert: the lanes' equal keys as a 64-bit mask per held expert.
+//
+// Without bias and groups the choice goes by the logits themselves.  With them it
+// goes by scores in fp64: which expert a token meets should follow from the inputs,
+// not from how an exponential or a sum was rounded.  Weights are sums and
+// exponentials in the same precision, rounded once to fp32.
+#include <type_traits>
+
+#include "w4a8_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace w4a8 {
+namespace {
+
+constexpr int kRouteWaves = 4;   // tokens to a workgroup
+
+// keys in the order of the values, 0 for one that may not be chosen
+__device__ __forceinline__ uint32_t key_of(float v) {
+    if (!(v > -__builtin_inff())) return 0u;
+    const uint32_t b = __float_as_uint(v + 0.0f);   // -0 counts as 0
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t key_of(double v) {
+    if (!(v > -__builtin_inf())) return 0u;
+    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
+    return b >> 63 ? ~b : b | (1ull << 63);
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ T wave_reduce(T v, F f) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v = f(v, __shfl_xor(v, off));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_max(T v) {
+    return wave_reduce(v, [](T a, T b) { return a > b ? a : b; });
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+    return wave_reduce(v, [](T a, T b) { return a + b; });
+}
+
+__device__ __forceinline__ float exponential(float v) { return expf(v); }
+__device__ __forceinline__ double exponential(double v) { return exp(v); }
+
+template <w4a8_float TYPE>
+__device__ __forceinline__ float load_logit(const void* row, int i) {
+    if (TYPE == W4A8_FP32) return static_cast<const float*>(row)[i];
+    const uint16_t h = static_cast<const uint16_t*>(row)[i];
+    return TYPE == W4A8_FP16 ? f16_to_f32(h) : bf16_to_f32(h);
+}
+
+// NL: experts per lane.  S: type of the scores (double: the choice goes by them)
+template <w4a8_float TYPE, int NL, typename S>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
+    constexpr bool kByScore = sizeof(S) == 8;
+    using Key = std::conditional_t<kByScore, uint64_t, uint32_t>;
+    __shared__ double line[kByScore ? kRouteWaves : 1][kByScore ? 64 * NL : 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t token = (int64_t)blockIdx.x * kRouteWaves + wave;
+    if (token >= a.tokens) return;   // whole waves; no barrier of the workgroup follows
+    const void* row = static_cast<const uint8_t*>(a.logits) + token * a.ld * (TYPE == W4A8_FP32 ? 4 : 2);
+    const float inf = __builtin_inff();
+    float logit[NL];
+    S p[NL];
+    Key key[NL];
+    float top = -inf;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int e = lane + 64 * i;
+        const float v = e < a.experts ? load_logit<TYPE>(row, e) : -inf;
+        logit[i] = v == v ? v : -inf;
+        top = fmaxf(top, logit[i]);
+    }
+    S total = 1;
+    if (a.score == W4A8_SCORE_SOFTMAX) {
+        top = wave_max(top);
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            // equal to the top, infinity included: 1; off: 0
+            const S d = logit[i] == top ? S(0) : S(logit[i]) - S(top);
+            p[i] = logit[i] > -inf ? exponential(d) : S(0);
+            total += p[i];
+        }
+        total = wave_sum(total);
+        if (!(total > 0)) total = 1;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) p[i] = S(1) / (S(1) + exponential(-S(logit[i])));
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        if constexpr (kByScore) {
+            p[i] = p[i] / total;
+            const int e = lane + 64 * i;
+            const double by = a.bias && e < a.experts ? p[i] + (double)a.bias[e] : p[i];
+            key[i] = logit[i] > -inf ? key_of(by) : 0;
+            if (a.groups > 1) line[wave][e] = key[i] ? by : -__builtin_inf();
+        } else {
+            key[i] = key_of(logit[i]);
+        }
+    }
+    if constexpr (kByScore) {
+        if (a.groups > 1) {
+            // lane g: the group's largest scores.  The wave's own lines: its LDS accesses are in order.
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            const int size = a.experts / a.groups;
+            uint64_t group = 0;
+            if (lane < a.groups) {
+                double first = -__builtin_inf(), second = first;
+                for (int i = 0; i < size; ++i) {
+                    const double v = line[wave][lane * size + i];
+                    second = fmax(second, fmin(first, v));
+                    first = fmax(first, v);
+                }
+                const double sum = a.group_top == 2 && size > 1 ? first + second : first;
+                // a group with too few experts is behind all others, but not behind nothing
+                group = sum > -__builtin_inf() ? key_of(sum) : 1;
+            }
+            uint64_t kept = 0;
+            for (int j = 0; j < a.groups_kept; ++j) {
+                const uint64_t best = wave_max(group);
+                const int at = __builtin_ctzll(__ballot(group == best));
+                kept |= 1ull << at;
+                if (lane == at) group = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int e = lane + 64 * i;
+                if (e < a.experts && !((kept >> (e / size)) & 1)) key[i] = 0;
+            }
+        }
+    }
+    int id = -1;
+    S mine = 0, sum = 0;
+    for (int j = 0; j < a.top_k; ++j) {
+        Key best = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) best = key[i] > best ? key[i] : best;
+        best = wave_max(best);
+        if (best == 0) break;   // the same in all lanes: nothing is left
+        int at = -1;
+        S w = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            if (at >= 0) continue;
+            const uint64_t have = __ballot(key[i] == best);
+            if (!have) continue;
+            const int from = __builtin_ctzll(have);
+            at = 64 * i + from;
+            w = __shfl(p[i], from);
+            if (lane == from) key[i] = 0;
+        }
+        sum += w;
+        if (lane == j) id = at, mine = w;
+    }
+    if constexpr (!kByScore) mine = mine / total, sum = sum / total;
+    if (a.renormalize) mine = sum > 0 ? mine / sum : S(0);
+    if (lane < a.top_k) {
+        a.ids[token * a.top_k + lane] = id;
+        a.weights[token * a.top_k + lane] = (float)(mine * S(a.scale));
+    }
+}
+
+template <w4a8_float TYPE, typename S>
+hipError_t launch_type(const RouteArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)((a.tokens + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
+#define W4A8_ROUTE(NL) hipLaunchKernelGGL((route_kernel<TYPE, NL, S>), grid, block, 0, stream, a)
+    if (a.experts <= 64) W4A8_ROUTE(1);
+    else if (a.experts <= 128) W4A8_ROUTE(2);
+    else if (a.experts <= 256) W4A8_ROUTE(4);
+    else if (a.experts <= 512) W4A8_ROUTE(8);
+    else W4A8_ROUTE(16);
+#undef W4A8_ROUTE
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t moe_route_threads(const RouteArgs& a) { return (a.tokens + kRouteWaves - 1) / kRouteWaves * 64 * kRouteWaves; }
+
+hipError_t launch_moe_route(const RouteArgs& a, w4a8_float type, hipStream_t stream) {
+    const bool by_score = a.bias || a.groups > 1;
+    switch (type) {
+        case W4A8_FP32: return by_score ? launch_type<W4A8_FP32, double>(a, stream) : launch_type<W4A8_FP32, float>(a, stream);
+        case W4A8_FP16: return by_score ? launch_type<W4A8_FP16, double>(a, stream) : launch_type<W4A8_FP16, float>(a, stream);
+        default: return by_score ? launch_type<W4A8_BF16, double>(a, stream) : launch_type<W4A8_BF16, float>(a, stream);
+    }
+}
+
+}  // namespace w4a8

@@ -250,6 +250,66 @@ int64_t attention_threads(const AttnArgs& a, bool fp16);
 hipError_t launch_attention(const AttnArgs& a, bool fp16, hipStream_t stream);
 int device_cus();   // CUs of the current device (cached per device)
 
+// Norms around a block with its gate and residual sum (residual_norm.hip).
+struct NormArgs {
+    const uint16_t* y;
+    int64_t ldy;
+    int64_t tokens;
+    int hidden;
+    const float* post_weight;           // NULL: no norm after the block
+    const uint16_t* gate;               // NULL: none
+    int64_t gate_st, gate_sc;           // elements; gate_sc 0 or 1
+    float scale;
+    const void* residual;               // NULL: none
+    bool residual_fp32;
+    int64_t ldr;
+    void* residual_out;                 // NULL: not written
+    int64_t ldro;
+    const float* weight;                // NULL: ones
+    float eps;
+    uint16_t* out;                      // NULL: not written
+    uint8_t* x8;                        // NULL: not written
+    float* xs;
+};
+int64_t residual_norm_threads(const NormArgs& a);
+hipError_t launch_residual_norm(const NormArgs& a, bool fp16, hipStream_t stream);
+
+// The experts of each token from the router's logits (moe_route.hip).
+struct RouteArgs {
+    const void* logits;
+    int64_t ld, tokens;
+    int experts, top_k;
+    int score;
+    const float* bias;
+    int groups, groups_kept, group_top;
+    bool renormalize;
+    float scale;
+    int32_t* ids;
+    float* weights;
+};
+int64_t moe_route_threads(const RouteArgs& a);
+hipError_t launch_moe_route(const RouteArgs& a, w4a8_float type, hipStream_t stream);
+
+// Experts' products on MXFP4 weights (moe.hip).
+struct MoeArgs {
+    w4a8_experts_mxfp4 e;
+    const uint8_t* x8;
+    const float* xs;
+    int64_t tokens;
+    const int32_t* ids;
+    const float* weights;
+    int top_k;
+    int act;
+    uint16_t* out;
+    uint8_t* ws;
+};
+// slots (token, j) that a workgroup lists at once, and the tokens of such a chunk
+constexpr int kMoeSlots = 2048;
+inline int64_t moe_chunk_tokens(int top_k) { return kMoeSlots / top_k; }
+size_t moe_workspace_bytes(int64_t slots, int64_t inter);
+int64_t moe_threads(const MoeArgs& a);
+hipError_t launch_moe(const MoeArgs& a, hipStream_t stream);
+
 // GEMM plans: the host picks the band, the tile and the K split.
 struct GemmPlan {
     int band;       // 0 decode (weights streamed, split K), 1 prefill (LDS tiles)
