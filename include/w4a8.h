@@ -716,10 +716,10 @@ typedef enum { W4A8_ACT_SILU = 0, W4A8_ACT_GELU_TANH = 1 } w4a8_act;
  * zeros; the same expert twice counts twice.  Two kernels, nothing allocated, no atomics on
  * device memory.  Made for few tokens: every expert met is read once per 2048 / top_k tokens.
  * d_ws: w4a8_moe_workspace_bytes(...) bytes, 256-byte aligned, contents of no meaning between
- * calls; one sized for more tokens (or slots) of the same inter serves fewer.  top_k from 1
+ * calls; one sized for more tokens * top_k of the same hidden and inter serves fewer.  top_k from 1
  * to 32 and to experts, tokens * top_k < 2^30, at most 2^15 * (2048 / top_k) tokens (else
  * UNSUPPORTED_SHAPE).  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, WORKSPACE, HIP. */
-size_t      w4a8_moe_workspace_bytes(int64_t tokens, int top_k, int64_t inter);
+size_t      w4a8_moe_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inter);
 w4a8_status w4a8_moe_mxfp4(const w4a8_experts_mxfp4 *experts, const uint8_t *d_x_fp8, const float *d_x_scale,
                            int64_t tokens, const int32_t *d_ids, const float *d_weights, int top_k, w4a8_act act,
                            uint16_t *d_out, void *d_ws, size_t ws_bytes, void *stream);

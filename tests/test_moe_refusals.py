@@ -27,7 +27,7 @@ def L():
                                        _vp, _f32, _vp, _vp, _vp, _vp]
     lib.w4a8_moe_route.argtypes = [_int, _vp, _i64, _i64, _int, _int, _int, _vp, _int, _int, _int, _int, _f32, _vp, _vp, _vp]
     lib.w4a8_moe_mxfp4.argtypes = [ctypes.POINTER(_Experts), _vp, _vp, _i64, _vp, _vp, _int, _int, _vp, _vp, _size, _vp]
-    lib.w4a8_moe_workspace_bytes.argtypes = [_i64, _int, _i64]
+    lib.w4a8_moe_workspace_bytes.argtypes = [_i64, _int, _i64, _i64]
     lib.w4a8_moe_workspace_bytes.restype = _size
     return lib
 
@@ -101,12 +101,16 @@ def test_moe_refusals(L, kw, status):
 
 def test_workspace_bytes(L):
     b = L.w4a8_moe_workspace_bytes
-    # one byte a value and an exponent byte for each of 32, in dwords of four steps
-    assert b(1, 8, 768) == 8 * (768 + 32)
-    assert b(5, 2, 512) == 10 * (512 + 16)
-    assert b(0, 2, 512) == b(5, 0, 512) == b(5, 33, 512) == b(5, 2, 64) == b(5, 2, 130) == b(1 << 29, 2, 128) == 0
-    for t in (1, 7, 300):
-        assert b(t + 1, 2, 384) > b(t, 2, 384)
+    # one byte a value and an exponent byte for each of 32, in dwords of four steps; fp32 sums of the slots,
+    # up to four parts of each while there are no more than 2048 rows
+    assert b(1, 8, 2048, 768) == 8 * (768 + 32) + 32 * 2048 * 4
+    assert b(5, 2, 256, 512) == 10 * (512 + 16) + 40 * 256 * 4
+    assert b(500, 2, 256, 512) == 1000 * (512 + 16) + 2048 * 256 * 4
+    assert b(3000, 2, 256, 512) == 6000 * (512 + 16) + 6000 * 256 * 4
+    assert b(0, 2, 256, 512) == b(5, 0, 256, 512) == b(5, 33, 256, 512) == b(5, 2, 256, 64) == b(5, 2, 256, 130) == 0
+    assert b(5, 2, 100, 512) == b(5, 2, 0, 512) == b(5, 2, 1 << 17, 512) == b(1 << 29, 2, 256, 128) == 0
+    for t in (1, 7, 255, 300, 1023, 1024, 2000):
+        assert b(t + 1, 2, 256, 384) > b(t, 2, 256, 384)
 
 
 def _t(*shape, dtype=torch.bfloat16):
@@ -196,4 +200,4 @@ def test_moe_python_refusals():
                dict(tokens=1 << 40)):
         with pytest.raises(ValueError):
             w4.MoEWorkspace(**{**dict(tokens=3, top_k=2, experts=4, hidden=256, inter=128, device="cpu"), **kw})
-    assert w4.MoEWorkspace(3, 2, 4, 256, 128, device="cpu").nbytes == w4.moe_workspace_bytes(3, 2, 128)
+    assert w4.MoEWorkspace(3, 2, 4, 256, 128, device="cpu").nbytes == w4.moe_workspace_bytes(3, 2, 256, 128)

@@ -123,7 +123,7 @@ def lib() -> ctypes.CDLL:
         L.w4a8_attention_counter_bytes.restype = _size
         L.w4a8_attention_workspace_bytes.argtypes = [_i64, _i64, _int, _int, _int]
         L.w4a8_attention_workspace_bytes.restype = _size
-        L.w4a8_moe_workspace_bytes.argtypes = [_i64, _int, _i64]
+        L.w4a8_moe_workspace_bytes.argtypes = [_i64, _int, _i64, _i64]
         L.w4a8_moe_workspace_bytes.restype = _size
         L.w4a8_status_string.argtypes = [_int]
         L.w4a8_status_string.restype = ctypes.c_char_p

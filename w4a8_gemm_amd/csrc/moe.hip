@@ -23,12 +23,15 @@
 //   down  a workgroup per 16 columns of the output, its waves over the units (and parts
 //         of K where units are few); every slot's 16 partial sums meet in LDS, and are
 //         added in the order of j: no atomics, no third kernel
+#include <type_traits>
+
 #include "w4a8_internal.h"
 
 namespace w4a8 {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -52,15 +55,15 @@ __device__ __forceinline__ v4f product(v8i w, v8i x, v4f c, uint32_t sw, uint32_
 struct alignas(16) MoePlan {
     uint32_t count[kMaxExperts + 1];    // slots of each expert, then its first place in `list` (and the end of the last)
     uint16_t list[kMoeSlots];           // slots (of the chunk) by expert
-    uint32_t unit[kMoeSlots];           // first place | (slots - 1) << 11 | expert << 17
+    uint32_t unit[kMoeSlots];           // first place | (slots - 1) << 11 | expert << 18
     uint32_t part[16];
     int units, several;                 // several: some expert has more than one unit
 };
 __device__ __forceinline__ int unit_first(uint32_t u) { return u & 2047; }
-__device__ __forceinline__ int unit_slots(uint32_t u) { return ((u >> 11) & 63) + 1; }
-__device__ __forceinline__ int unit_expert(uint32_t u) { return u >> 17; }
+__device__ __forceinline__ int unit_slots(uint32_t u) { return ((u >> 11) & 127) + 1; }
+__device__ __forceinline__ int unit_expert(uint32_t u) { return u >> 18; }
 
-// All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 64).  The atomics
+// All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 128).  The atomics
 // list an expert's slots in any order.  Where workgroups share an expert of several units
 // (ORDER) they have to agree on which slots are whose: such an expert's are sorted, each
 // slot counting the smaller ones.
@@ -107,7 +110,7 @@ __device__ void make_plan(MoePlan& p, const int32_t* ids, int slots, int experts
         if (e < experts) p.count[e] = first;
         if (ORDER && c > US) p.several = 1;
         for (int k = 0; k < c; k += US, ++u)
-            p.unit[u] = (uint32_t)(first + k) | (uint32_t)(min(c - k, US) - 1) << 11 | (uint32_t)e << 17;
+            p.unit[u] = (uint32_t)(first + k) | (uint32_t)(min(c - k, US) - 1) << 11 | (uint32_t)e << 18;
         before += mine[i];
     }
     __syncthreads();
@@ -136,6 +139,60 @@ __device__ void make_plan(MoePlan& p, const int32_t* ids, int slots, int experts
     }
 }
 
+// Up to 64 slots: every wave lists them in its registers, lane s holding slot s.  No LDS, no
+// barrier, and the units come in the same order in every wave.
+constexpr int kWaveSlots = 64;
+struct WaveList {
+    int id;              // the slot's expert, -1 if it has none
+    uint64_t same;       // slots of the same expert
+    int rank;            // how many of these come before it
+    uint64_t starts;     // slots that begin a unit of 16
+    __device__ __forceinline__ int units() const { return __popcll(starts); }
+};
+__device__ __forceinline__ WaveList wave_list(const int32_t* ids, int slots, int experts) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t before = (1ull << lane) - 1;
+    WaveList r;
+    r.id = lane < slots ? ids[lane] : -1;
+    if ((uint32_t)r.id >= (uint32_t)experts) r.id = -1;
+    r.same = 0;
+    for (int s = 0; s < slots; ++s) {
+        const int e = __builtin_amdgcn_readlane(r.id, s);
+        const uint64_t m = __ballot(r.id == e);
+        if (lane == s) r.same = m;
+    }
+    r.rank = __popcll(r.same & before);
+    r.starts = __ballot(r.id >= 0 && (r.rank & 15) == 0);
+    return r;
+}
+// A unit as a wave has it: lane n (of 16) of column tile j has slot[j] in column 16 j + n, the
+// columns past cols the last one's
+template <int MT>
+struct Unit {
+    int expert, cols;
+    int slot[MT];
+};
+__device__ __forceinline__ void wave_unit(const WaveList& l, int u, Unit<1>& r) {
+    const int lane = threadIdx.x & 63;
+    const bool here = ((l.starts >> lane) & 1) && __popcll(l.starts & ((1ull << lane) - 1)) == u;
+    const int at = __builtin_ctzll(__ballot(here));
+    const int first = __builtin_amdgcn_readlane(l.rank, at);
+    r.expert = __builtin_amdgcn_readlane(l.id, at);
+    const bool in = l.id == r.expert && l.rank >= first && l.rank < first + 16;
+    r.cols = __popcll(__ballot(in));
+    // each slot to the lane of its column (the others to lanes that are not read)
+    const int got = __builtin_amdgcn_ds_permute(4 * (in ? l.rank - first : 16 + (lane & 15)), lane);
+    r.slot[0] = __builtin_amdgcn_ds_bpermute(4 * min(lane & 15, r.cols - 1), got);
+}
+template <int MT>
+__device__ __forceinline__ void plan_unit(const MoePlan& p, int u, Unit<MT>& r) {
+    const uint32_t v = uniform(p.unit[u]);
+    r.expert = unit_expert(v);
+    r.cols = unit_slots(v);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) r.slot[j] = p.list[unit_first(v) + min(16 * j + (int)(threadIdx.x & 15), r.cols - 1)];
+}
+
 struct MoeShape {
     int64_t tokens, hidden, inter;
     int experts, top_k, chunk;          // tokens of a chunk
@@ -156,7 +213,16 @@ struct DownArgs {
     const int32_t* ids;
     const float* weights;
     uint16_t* out;
-    int rows;                           // of partial sums that LDS holds
+    int rows, slots;                    // of partial sums that LDS holds; of a chunk at most
+};
+struct DownTileArgs {
+    MoeShape m;
+    const uint8_t *w, *s;
+    const int32_t* ids;
+    const float* weights;
+    uint16_t* out;
+    float* sums;
+    int ks;                             // K parts
 };
 
 // ---------------------------------------------------------------------------
@@ -168,6 +234,57 @@ __device__ __forceinline__ float activated(float g, int act) {
     return g / (1.0f + expf(-2.0f * t));   // (1 + tanh t) / 2
 }
 
+// One step's products of a 16-row tile with 16 columns, for the first product.
+//
+// The e2m1 x e4m3 instruction aligns its 128 products to the largest and cuts what lies 2^-14
+// below it.  That is far under what bf16 outputs show, but v is rounded to four bits next, and a
+// value that the cut takes over the border of two codes moves by a whole step: for one token
+// such a step of a large value is the output's error (0.0036 of it for 0.0016, one token
+// through 8 of 128 experts).  Where tokens are few (BF16) the operands are widened instead, exact
+// as both are, and the products added in fp32; it takes 4 instructions for one, which a kernel
+// that waits for its weights has time for.  With more tokens the rare steps average out.
+template <bool BF16>
+struct Columns;
+template <>
+struct Columns<false> {
+    v8i x;
+    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) { x = frag_fp8(lo, hi); }
+    __device__ __forceinline__ v4f times(uint4 w, uint32_t scale, v4f c) const {
+        return product(frag_fp4(w), x, c, scale, kUnitScale);
+    }
+};
+template <>
+struct Columns<true> {
+    v8bf x[4];
+    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = i < 2 ? lo[2 * i] : hi[2 * i - 4], b = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+            const u32x4 r = {pair<false>(a), pair<true>(a), pair<false>(b), pair<true>(b)};
+            x[i] = __builtin_bit_cast(v8bf, r);
+        }
+    }
+    __device__ __forceinline__ v4f times(uint4 w, uint32_t scale, v4f c) const {
+        // the conversion reads the scale's exponent field alone: 2^(byte - 127), for 0 too
+        const float s = __uint_as_float((scale & 0xFFu) << 23);
+        const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const u32x4 r = {fp4<0>(d[i], s), fp4<1>(d[i], s), fp4<2>(d[i], s), fp4<3>(d[i], s)};
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, r), x[i], c, 0, 0, 0);
+        }
+        return c;
+    }
+    template <bool HIGH>
+    static __device__ __forceinline__ uint32_t pair(uint32_t codes) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HIGH));
+    }
+    template <int B>
+    static __device__ __forceinline__ uint32_t fp4(uint32_t codes, float s) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, B));
+    }
+};
+
 template <int MT>
 struct UpStep {
     uint4 w[4];            // gate rows i0 .. +15 and +16 .. +31, then the up rows
@@ -175,40 +292,80 @@ struct UpStep {
     u32x4 x[MT][2];
 };
 
-template <int MT>
+// v of 32 of inter (block blk) for 16 columns, from the sums of the tiles: a lane has 4 values of each half
+__device__ __forceinline__ void store_v(const MoeShape& m, const v4f (&r)[4], float sx, int act, int64_t row, int blk, int g,
+                                        bool mine) {
+    float v[2][4];
+    uint32_t top = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[h][i] = activated(sx * r[h][i], act) * (sx * r[2 + h][i]);
+            top = max(top, __float_as_uint(v[h][i]) & 0x7FFFFFFFu);
+        }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    // the least e with top <= 448 2^e = 1.75 2^(e + 8)
+    const int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -127);
+    const bool finite = top < 0x7F800000u;
+    const float to_code = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e, -e <= 127
+    if (!mine) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[h][0] * to_code, v[h][1] * to_code, 0, false);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(v[h][2] * to_code, v[h][3] * to_code, c, true);
+        *reinterpret_cast<int*>(m.v + row * m.inter + 32 * blk + 16 * h + 4 * g) = finite ? c : 0x7F7F7F7F;
+    }
+    if (g == 0)   // block blk: k / 32 % 4 = blk % 4 of step blk / 4
+        m.ve[row * m.e_stride + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] = finite ? (uint8_t)(e + 127) : 255;
+}
+
+// WAVE: up to 64 slots, listed by every wave.  D: steps in flight.
+template <int MT, int D, bool WAVE>
 __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
+    constexpr bool kBf16 = MT == 1;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds);
-    float4* join = reinterpret_cast<float4*>(lds + sizeof(MoePlan));   // [wave][tile][MT][lane]
+    float4* join = reinterpret_cast<float4*>(lds + (WAVE ? 0 : sizeof(MoePlan)));   // [wave][tile][MT][lane]
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
-    make_plan<kUpThreads, 16 * MT, true>(p, a.ids + t0 * m.top_k, slots, m.experts);
+    WaveList list;
+    if constexpr (WAVE)
+        list = wave_list(a.ids + t0 * m.top_k, slots, m.experts);
+    else
+        make_plan<kUpThreads, 16 * MT, true>(p, a.ids + t0 * m.top_k, slots, m.experts);
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int kw = a.kw, part = wave % kw, per_wg = 8 / kw;
-    const int blocks = (int)(m.inter / 32), items = p.units * blocks;
+    const int blocks = (int)(m.inter / 32), items = (WAVE ? list.units() : p.units) * blocks;
     const int c_pad = (m.h_steps + 3) / 4;
     const int64_t tiles_i = m.inter / 16;
     const int s0 = m.h_steps * part / kw, s1 = m.h_steps * (part + 1) / kw;
+    const uint8_t* x = a.x8 + t0 * m.hidden;
     for (int base = blockIdx.x * per_wg; base < items; base += gridDim.x * per_wg) {   // the same in all waves
         const int item = base + wave / kw;
         const bool live = item < items;
-        const uint32_t u = uniform(p.unit[live ? item / blocks : 0]);
-        const int blk = live ? item % blocks : 0, cols = unit_slots(u);
-        int slot[MT];
-        const uint8_t* x = a.x8 + t0 * m.hidden;
+        const int blk = live ? item % blocks : 0;
+        Unit<MT> u;
+        if constexpr (WAVE)
+            wave_unit(list, live ? item / blocks : 0, u);
+        else
+            plan_unit(p, live ? item / blocks : 0, u);
         uint32_t xo[MT];
+        float sx[MT];
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            slot[j] = p.list[unit_first(u) + min(16 * j + n, cols - 1)];
-            xo[j] = (uint32_t)(slot[j] / m.top_k) * (uint32_t)m.hidden + 16 * g;
+            const int t = u.slot[j] / m.top_k;
+            xo[j] = (uint32_t)t * (uint32_t)m.hidden + (kBf16 ? 32 : 16) * g;
+            sx[j] = a.xs[t0 + t];
         }
         const uint8_t *wp[4];
         const uint32_t* sp[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int64_t tile = (2 * unit_expert(u) + (q >> 1)) * tiles_i + 2 * blk + (q & 1);
+            const int64_t tile = (2 * u.expert + (q >> 1)) * tiles_i + 2 * blk + (q & 1);
             wp[q] = a.w + tile * c_pad * 4096;
             sp[q] = reinterpret_cast<const uint32_t*>(a.s) + tile * c_pad * 64;
         }
@@ -226,26 +383,29 @@ __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 r.x[j][0] = *reinterpret_cast<const u32x4*>(x + 128 * s + xo[j]);
-                r.x[j][1] = *reinterpret_cast<const u32x4*>(x + 128 * s + 64 + xo[j]);
+                r.x[j][1] = *reinterpret_cast<const u32x4*>(x + 128 * s + (kBf16 ? 16 : 64) + xo[j]);
             }
         };
         const auto compute = [&](int s, const UpStep<MT>& r) {
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-                const v8i x = frag_fp8(r.x[j][0], r.x[j][1]);
+                Columns<kBf16> c;
+                c.set(r.x[j][0], r.x[j][1]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[q][j] = product(frag_fp4(r.w[q]), x, acc[q][j], r.s[q] >> (8 * (s & 3)), kUnitScale);
+                for (int q = 0; q < 4; ++q) acc[q][j] = c.times(r.w[q], r.s[q] >> (8 * (s & 3)), acc[q][j]);
             }
         };
-        if (live && s0 < s1) {
-            UpStep<MT> ring[2];
-            load(s0, ring[0]);
-            for (int s = s0; s < s1; s += 2) {
-                if (s + 1 < s1) load(s + 1, ring[1]);
-                compute(s, ring[0]);
-                if (s + 2 < s1) load(s + 2, ring[0]);
-                if (s + 1 < s1) compute(s + 1, ring[1]);
+        if (live) {
+            UpStep<MT> ring[D];
+#pragma unroll
+            for (int d = 0; d < D - 1; ++d)
+                if (s0 + d < s1) load(s0 + d, ring[d]);
+            for (int s = s0; s < s1; s += D) {
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    if (s + d + D - 1 < s1) load(s + d + D - 1, ring[(d + D - 1) % D]);
+                    if (s + d < s1) compute(s + d, ring[d]);
+                }
             }
         }
         if (kw > 1) {
@@ -273,32 +433,7 @@ __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
                     r[q] += v4f{f.x, f.y, f.z, f.w};
                 }
             }
-            const float sx = a.xs[t0 + slot[j] / m.top_k];
-            float v[2][4];
-            uint32_t top = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[h][i] = activated(sx * r[h][i], a.act) * (sx * r[2 + h][i]);
-                    top = max(top, __float_as_uint(v[h][i]) & 0x7FFFFFFFu);
-                }
-            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-            // the least e with top <= 448 2^e = 1.75 2^(e + 8)
-            const int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -127);
-            const bool finite = top < 0x7F800000u;
-            const float to_code = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e, -e <= 127
-            if (16 * j + n >= cols) continue;
-            const int64_t row = t0 * m.top_k + slot[j];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[h][0] * to_code, v[h][1] * to_code, 0, false);
-                c = __builtin_amdgcn_cvt_pk_fp8_f32(v[h][2] * to_code, v[h][3] * to_code, c, true);
-                *reinterpret_cast<int*>(m.v + row * m.inter + 32 * blk + 16 * h + 4 * g) = finite ? c : 0x7F7F7F7F;
-            }
-            if (g == 0)   // block blk: k / 32 % 4 = blk % 4 of step blk / 4
-                m.ve[row * m.e_stride + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] = finite ? (uint8_t)(e + 127) : 255;
+            store_v(m, r, sx[j], a.act, t0 * m.top_k + u.slot[j], blk, g, 16 * j + n < u.cols);
         }
         if (kw > 1) __syncthreads();
     }
@@ -315,36 +450,51 @@ struct DownStep {
     uint32_t e[MT];
 };
 
-template <int MT>
+template <int MT, int D, bool WAVE>
 __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    MoePlan& p = *reinterpret_cast<MoePlan*>(lds);
-    float4* part = reinterpret_cast<float4*>(lds + sizeof(MoePlan));   // [slot][K part][16 columns]
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
     const int32_t* ids = a.ids + t0 * m.top_k;
-    make_plan<kDownThreads, 16 * MT, false>(p, ids, slots, m.experts);
-
+    // LDS: partial sums [slot][K part][16 columns], the slots' weights, the plan
+    float4* part = reinterpret_cast<float4*>(lds);
+    float* share = reinterpret_cast<float*>(lds + (size_t)a.rows * 64);
+    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + (size_t)a.rows * 64 + (size_t)((a.slots + 3) / 4 * 16));
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     constexpr int kWaves = kDownThreads / 64;
+    WaveList list;
+    if constexpr (WAVE)
+        list = wave_list(ids, slots, m.experts);
+    else
+        make_plan<kDownThreads, 16 * MT, false>(p, ids, slots, m.experts);
+    const int units = WAVE ? list.units() : p.units;
     int ks = 1;   // K parts: as many as give every wave one, while there are few units
-    while (2 * ks * p.units <= kWaves && 2 * ks * slots <= a.rows && 2 * ks <= min(kWaves, m.i_steps)) ks *= 2;
+    while (2 * ks * units <= kWaves && 2 * ks * slots <= a.rows && 2 * ks <= min(kWaves, m.i_steps)) ks *= 2;
+    // slots without an expert add nothing
+    for (int s = threadIdx.x; s < slots; s += kDownThreads) {
+        const bool on = (uint32_t)ids[s] < (uint32_t)m.experts;
+        share[s] = on ? a.weights[t0 * m.top_k + s] : 0.0f;
+        if (!on)
+            for (int k = 0; k < 4 * ks; ++k) part[4 * s * ks + k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     const int c_pad = (m.i_steps + 3) / 4;
-    for (int item = wave; item < p.units * ks; item += kWaves) {
-        const uint32_t u = uniform(p.unit[item / ks]);
-        const int k = item % ks, cols = unit_slots(u);
-        const int64_t tile = unit_expert(u) * (m.hidden / 16) + blockIdx.x;
+    const uint8_t *x = m.v + t0 * m.top_k * m.inter, *e = m.ve + t0 * m.top_k * m.e_stride;
+    for (int item = wave; item < units * ks; item += kWaves) {
+        const int k = item % ks;
+        Unit<MT> u;
+        if constexpr (WAVE)
+            wave_unit(list, item / ks, u);
+        else
+            plan_unit(p, item / ks, u);
+        const int64_t tile = u.expert * (m.hidden / 16) + blockIdx.x;
         const uint8_t* wp = a.w + tile * c_pad * 4096;
         const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.s) + tile * c_pad * 64;
-        const uint8_t *x = m.v + t0 * m.top_k * m.inter, *e = m.ve + t0 * m.top_k * m.e_stride;
-        int slot[MT];
         uint32_t xo[MT], eo[MT];
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            slot[j] = p.list[unit_first(u) + min(16 * j + n, cols - 1)];
-            xo[j] = (uint32_t)slot[j] * (uint32_t)m.inter + 16 * g;
-            eo[j] = (uint32_t)slot[j] * (uint32_t)m.e_stride + 4 * g;
+            xo[j] = (uint32_t)u.slot[j] * (uint32_t)m.inter + 16 * g;
+            eo[j] = (uint32_t)u.slot[j] * (uint32_t)m.e_stride + 4 * g;
         }
         v4f acc[MT];
 #pragma unroll
@@ -366,34 +516,35 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
                                  r.e[j] >> (8 * (s & 3)));
         };
         const int s0 = m.i_steps * k / ks, s1 = m.i_steps * (k + 1) / ks;
-        DownStep<MT> ring[2];
-        load(s0, ring[0]);
-        for (int s = s0; s < s1; s += 2) {
-            if (s + 1 < s1) load(s + 1, ring[1]);
-            compute(s, ring[0]);
-            if (s + 2 < s1) load(s + 2, ring[0]);
-            if (s + 1 < s1) compute(s + 1, ring[1]);
+        DownStep<MT> ring[D];
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d)
+            if (s0 + d < s1) load(s0 + d, ring[d]);
+        for (int s = s0; s < s1; s += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (s + d + D - 1 < s1) load(s + d + D - 1, ring[(d + D - 1) % D]);
+                if (s + d < s1) compute(s + d, ring[d]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j)
-            if (16 * j + n < cols) part[(slot[j] * ks + k) * 4 + g] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+            if (16 * j + n < u.cols)
+                part[(u.slot[j] * ks + k) * 4 + g] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
     }
     __syncthreads();
     // four columns of a token to a thread: its slots in order
     for (int i = threadIdx.x; i < 4 * tokens; i += kDownThreads) {
         const int t = i >> 2, q = i & 3;
         v4f sum = v4f{0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < m.top_k; ++j) {
-            const int s = t * m.top_k + j;
-            if ((uint32_t)ids[s] >= (uint32_t)m.experts) continue;
+        for (int s = t * m.top_k; s < (t + 1) * m.top_k; ++s) {
             v4f v = v4f{0.f, 0.f, 0.f, 0.f};
             for (int k = 0; k < ks; ++k) {
                 const float4 f = part[(s * ks + k) * 4 + q];
                 v += v4f{f.x, f.y, f.z, f.w};
             }
-            const float w = a.weights[t0 * m.top_k + s];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(w, v[c], sum[c]);
+            for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(share[s], v[c], sum[c]);
         }
         *reinterpret_cast<uint2*>(a.out + (t0 + t) * m.hidden + 16 * blockIdx.x + 4 * q) =
             make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
@@ -401,35 +552,393 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// both products with the columns in LDS
+// ---------------------------------------------------------------------------
+// A workgroup takes a unit and eight waves' worth of weight rows; the unit's columns (up to
+// 16 MT) are staged for all eight in LDS, 512 k (a chunk of the scales) at a time, two
+// buffers.  A wave's weights for a whole chunk are in flight: each step's registers are
+// asked for again, one chunk on, as soon as its products are issued, and the next chunk's
+// columns are asked for before them, so that waiting for those leaves the weights in flight.
+// Every step of a chunk is computed: past K the columns are zeros, and the weights those of the
+// last step.  So are all MT column tiles: those without slots cost products that the
+// weights' arrival hides, conditions on them cost copies of the sums.
+constexpr int kTileThreads = 512, kChunkBytes = 512;
+
+template <int OPSEL>
+__device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmtFp4, kFmtFp8, OPSEL, (int)sw, 0, kUnitScale);
+}
+template <int OPSEL>
+__device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw, uint32_t sx) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmtFp4, kFmtFp8, OPSEL, (int)sw, OPSEL, (int)sx);
+}
+// 16-byte pieces of a column's 512, swapped within 256 by the column, so that the 16 columns of
+// a read meet all banks
+__device__ __forceinline__ int piece(int column, int c) { return column * kChunkBytes + 16 * (c ^ (column & 15)); }
+
+template <int MT>
+struct Stage {                 // what a thread brings of a chunk: piece tid % 32 of the columns tid / 32 + 16 i
+    u32x4 r[MT];
+    __device__ __forceinline__ void load(const uint8_t* x, const uint32_t (&row)[MT], int chunk, int64_t width, int cols) {
+        const int c = threadIdx.x & 31, col = threadIdx.x >> 5;
+        const uint32_t at = (uint32_t)chunk * kChunkBytes + 16 * c;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            if (16 * i + col < cols) r[i] = at < width ? *reinterpret_cast<const u32x4*>(x + row[i] + at) : u32x4{0u, 0u, 0u, 0u};
+    }
+    __device__ __forceinline__ void store(uint8_t* to, int cols) const {
+        const int c = threadIdx.x & 31, col = threadIdx.x >> 5;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            if (16 * i + col < cols) *reinterpret_cast<u32x4*>(to + piece(16 * i + col, c)) = r[i];
+    }
+};
+// Where a lane finds its two pieces of step s of column 16 j + n: pieces 8 s + g and 8 s + 4 + g, whose
+// swap leaves four addresses, and constants beside them.
+struct ColumnReader {
+    int at[4];
+    __device__ __forceinline__ ColumnReader() {
+        const int n = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = n * kChunkBytes + 16 * ((g ^ n) ^ (4 * i));
+    }
+    __device__ __forceinline__ v8i read(const uint8_t* from, int j, int s) const {
+        const int more = 16 * j * kChunkBytes + 256 * (s >> 1), i = 2 * (s & 1);
+        return frag_fp8(*reinterpret_cast<const u32x4*>(from + at[i] + more),
+                        *reinterpret_cast<const u32x4*>(from + at[i + 1] + more));
+    }
+};
+// f(integral_constant<int, 0>) .. <3>
+template <typename F>
+__device__ __forceinline__ void four_steps(F f) {
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
+}
+
+// a slot's exponents of a chunk; past K, where none were written, 2^0
+__device__ __forceinline__ u32x4 exponents(const uint8_t* row, int chunk, int steps) {
+    u32x4 e = *reinterpret_cast<const u32x4*>(row + 16 * chunk);
+    const int left = steps - 4 * chunk;
+    if (left < 4) {
+        const uint32_t keep = (1u << (8 * left)) - 1;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) e[g] = (e[g] & keep) | (0x7F7F7F7Fu & ~keep);
+    }
+    return e;
+}
+
+// The sums as they stand here: without it the compiler moves a step's products behind the loads
+// that are to take their operands' registers.
+template <int Q, int MT>
+__device__ __forceinline__ void hold(v4f (&acc)[Q][MT]) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[q][j]));
+}
+
+// R weight tiles of a wave: a chunk's codes and scale dwords
+template <int R>
+struct Tiles {
+    const uint8_t* w[R];
+    const uint32_t* s[R];
+    uint4 q[4][R];
+    uint32_t sc[R], next[R];
+    __device__ __forceinline__ void at(int r, const uint8_t* wt, const uint8_t* st, int64_t tile, int c_pad) {
+        w[r] = wt + tile * c_pad * 4096;
+        s[r] = reinterpret_cast<const uint32_t*>(st) + tile * c_pad * 64;
+    }
+    __device__ __forceinline__ void load(int step, int to) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int r = 0; r < R; ++r) q[to][r] = load_stream16(reinterpret_cast<const uint4*>(w[r] + step * 1024) + lane);
+    }
+    __device__ __forceinline__ void load_scales(int chunk) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int r = 0; r < R; ++r) next[r] = (s[r] + chunk * 64)[lane];
+    }
+    __device__ __forceinline__ void last_scales() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) sc[r] = next[r];
+    }
+    __device__ __forceinline__ void next_scales(int chunk) {
+        last_scales();
+        load_scales(chunk);
+    }
+};
+
+template <int MT>
+__global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int kBuf = 16 * MT * kChunkBytes;
+    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + 2 * kBuf);
+    const MoeShape& m = a.m;
+    const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
+    const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
+    make_plan<kTileThreads, 16 * MT, true>(p, a.ids + t0 * m.top_k, slots, m.experts);
+
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const ColumnReader cr;
+    const int blocks = (int)(m.inter / 32), groups = (blocks + 7) / 8, items = p.units * groups;
+    const int steps = m.h_steps, chunks = (steps + 3) / 4;
+    const int64_t tiles_i = m.inter / 16;
+    const uint8_t* x = a.x8 + t0 * m.hidden;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t u = uniform(p.unit[item / groups]);
+        const int first = unit_first(u), cols = unit_slots(u), blk = item % groups * 8 + wave;
+        const bool live = blk < blocks;   // a wave past the last block computes that one again
+        uint32_t row[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            row[i] = (uint32_t)(p.list[first + min(16 * i + (int)(threadIdx.x >> 5), cols - 1)] / m.top_k) * (uint32_t)m.hidden;
+        Stage<MT> st;
+        st.load(x, row, 0, m.hidden, cols);
+        Tiles<4> w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            w.at(q, a.w, a.s, (2 * unit_expert(u) + (q >> 1)) * tiles_i + 2 * (live ? blk : blocks - 1) + (q & 1), chunks);
+        w.load_scales(0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) w.load(min(s, steps - 1), s);
+        v4f acc[4][MT];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        st.store(lds, cols);
+        __syncthreads();
+        const auto products = [&](const uint8_t* buf, auto step) {
+            constexpr int s = decltype(step)::value;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const v8i b = cr.read(buf, j, s);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s][q]), b, acc[q][j], w.sc[q]);
+                if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);   // no more than two tiles' columns in registers
+            }
+        };
+        for (int c = 0; c + 1 < chunks; ++c) {
+            st.load(x, row, c + 1, m.hidden, cols);
+            w.next_scales(c + 1);
+            four_steps([&](auto step) {
+                constexpr int s = decltype(step)::value;
+                products(lds + (c & 1) * kBuf, step);
+                hold(acc);
+                __builtin_amdgcn_sched_barrier(0);
+                w.load(min(4 * (c + 1) + s, steps - 1), s);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            st.store(lds + ((c + 1) & 1) * kBuf, cols);
+            __syncthreads();
+        }
+        w.last_scales();
+        four_steps([&](auto step) {
+            products(lds + ((chunks - 1) & 1) * kBuf, step);
+            hold(acc);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        __syncthreads();   // before the next item's first columns
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                if (16 * j >= cols) continue;
+                const int slot = p.list[first + min(16 * j + n, cols - 1)];
+                const v4f r[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
+                store_v(m, r, a.xs[t0 + slot / m.top_k], a.act, t0 * m.top_k + slot, blk, g, 16 * j + n < cols);
+            }
+        }
+    }
+}
+
+// The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
+// device memory.
+template <int MT>
+__global__ __launch_bounds__(kTileThreads) void down_tile_kernel(DownTileArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int kCols = 16 * MT * kChunkBytes, kBuf = kCols + 16 * MT * 16;   // columns, then their exponents
+    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + 2 * kBuf);
+    const MoeShape& m = a.m;
+    const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
+    const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
+    make_plan<kTileThreads, 16 * MT, true>(p, a.ids + t0 * m.top_k, slots, m.experts);
+
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const ColumnReader cr;
+    const int tiles = (int)(m.hidden / 16), groups = (tiles + 15) / 16, items = p.units * groups * a.ks;
+    const int steps = m.i_steps, chunks = (steps + 3) / 4;
+    const uint8_t *x = m.v + t0 * m.top_k * m.inter, *xe = m.ve + t0 * m.top_k * m.e_stride;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int k = item % a.ks, grp = item / a.ks % groups;
+        const uint32_t u = uniform(p.unit[item / a.ks / groups]);
+        const int first = unit_first(u), cols = unit_slots(u), tile = grp * 16 + 2 * wave;
+        const bool live = tile < tiles;   // tiles are even; a wave past the last pair computes that one again
+        const int c0 = chunks * k / a.ks, c1 = chunks * (k + 1) / a.ks;
+        uint32_t row[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            row[i] = (uint32_t)p.list[first + min(16 * i + (int)(threadIdx.x >> 5), cols - 1)] * (uint32_t)m.inter;
+        const bool has_e = (int)threadIdx.x < cols;
+        const uint8_t* ep = xe + (uint32_t)p.list[first + min((int)threadIdx.x, cols - 1)] * (uint32_t)m.e_stride;
+        Stage<MT> st;
+        u32x4 er{};
+        st.load(x, row, c0, m.inter, cols);
+        if (has_e) er = exponents(ep, c0, steps);
+        Tiles<2> w;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, chunks);
+        w.load_scales(c0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) w.load(min(4 * c0 + s, steps - 1), s);
+        v4f acc[2][MT];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        const auto put = [&](uint8_t* to) {
+            st.store(to, cols);
+            if (has_e) *reinterpret_cast<u32x4*>(to + kCols + 16 * threadIdx.x) = er;
+        };
+        put(lds);
+        __syncthreads();
+        uint32_t e[MT];
+        const auto read_e = [&](const uint8_t* buf) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) e[j] = *reinterpret_cast<const uint32_t*>(buf + kCols + 16 * (16 * j + n) + 4 * g);
+        };
+        const auto products = [&](const uint8_t* buf, auto step) {
+            constexpr int s = decltype(step)::value;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const v8i b = cr.read(buf, j, s);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s][q]), b, acc[q][j], w.sc[q], e[j]);
+                if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        for (int c = c0; c + 1 < c1; ++c) {
+            const uint8_t* buf = lds + ((c - c0) & 1) * kBuf;
+            st.load(x, row, c + 1, m.inter, cols);
+            if (has_e) er = exponents(ep, c + 1, steps);
+            w.next_scales(c + 1);
+            read_e(buf);
+            four_steps([&](auto step) {
+                constexpr int s = decltype(step)::value;
+                products(buf, step);
+                hold(acc);
+                __builtin_amdgcn_sched_barrier(0);
+                w.load(min(4 * (c + 1) + s, steps - 1), s);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            put(lds + ((c - c0 + 1) & 1) * kBuf);
+            __syncthreads();
+        }
+        w.last_scales();
+        const uint8_t* buf = lds + ((c1 - 1 - c0) & 1) * kBuf;
+        read_e(buf);
+        four_steps([&](auto step) {
+            products(buf, step);
+            hold(acc);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        __syncthreads();   // before the next item's first columns
+        if (live) {
+            float* to = a.sums + ((int64_t)k * m.tokens * m.top_k + t0 * m.top_k) * m.hidden + 16 * tile + 4 * g;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                if (16 * j + n >= cols) continue;
+                const int64_t slot = p.list[first + 16 * j + n];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    *reinterpret_cast<float4*>(to + slot * m.hidden + 16 * q) =
+                        make_float4(acc[q][j][0], acc[q][j][1], acc[q][j][2], acc[q][j][3]);
+            }
+        }
+    }
+}
+
+// out from the partial sums: four columns of a token to a thread, its slots in order
+__global__ __launch_bounds__(256) void join_kernel(DownTileArgs a) {
+    const MoeShape& m = a.m;
+    const int64_t quads = m.hidden / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= m.tokens * quads) return;
+    const int64_t t = i / quads, col = 4 * (i - t * quads);
+    v4f sum = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < m.top_k; ++j) {
+        const int64_t s = t * m.top_k + j;
+        if ((uint32_t)a.ids[s] >= (uint32_t)m.experts) continue;
+        v4f v = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < a.ks; ++k) {
+            const float4 f = *reinterpret_cast<const float4*>(a.sums + ((int64_t)k * m.tokens * m.top_k + s) * m.hidden + col);
+            v += v4f{f.x, f.y, f.z, f.w};
+        }
+        const float w = a.weights[s];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(w, v[c], sum[c]);
+    }
+    *reinterpret_cast<uint2*>(a.out + t * m.hidden + col) = make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
+}
+
+// ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
+int64_t exponent_stride(int64_t inter) { return (inter + 511) / 512 * 16; }
+// rows of the partial sums: parts of K where slots are few
+constexpr int64_t kSumRows = 2048;
+
 struct MoeGrid {
-    int mt, kw, rows;
-    unsigned up, down, chunks;
+    int mt;                         // column tiles of a unit
+    bool wave, up_tiles, down_tiles;
+    int kw, rows, slots, ks;
+    unsigned up, down, join, chunks;
     size_t up_lds, down_lds;
 };
-int64_t exponent_stride(int64_t inter) { return (inter + 511) / 512 * 16; }
 
 MoeGrid moe_grid(const MoeArgs& a) {
     MoeGrid g{};
-    const int64_t chunk = moe_chunk_tokens(a.top_k);
+    const int64_t chunk = moe_chunk_tokens(a.top_k), cus = device_cus();
     g.chunks = (unsigned)((a.tokens + chunk - 1) / chunk);
-    const int64_t slots = (a.tokens < chunk ? a.tokens : chunk) * a.top_k;
-    // column tiles of a unit by the slots that an expert has on average
-    const int64_t each = slots / a.e.experts;
+    const int64_t slots = (a.tokens < chunk ? a.tokens : chunk) * a.top_k, experts = a.e.experts;
+    g.slots = (int)slots;
+    // experts met, about: were the slots spread at random
+    double missed = 1.0;
+    for (int64_t s = 0; s < slots && missed > 1e-3; ++s) missed *= 1.0 - 1.0 / (double)experts;
+    const int64_t met = (int64_t)((double)experts * (1.0 - missed) + 0.5);
+    const int64_t each = slots / experts;
+    const int64_t blocks = a.e.inter / 32, up_groups = (blocks + 7) / 8, down_groups = (a.e.hidden / 16 + 15) / 16;
+    g.up_tiles = slots > kWaveSlots && met * up_groups >= 128;
+    g.down_tiles = slots > kWaveSlots;
     g.mt = each <= 8 ? 1 : each <= 24 ? 2 : 4;
-    const int64_t most = slots < a.e.experts ? slots : a.e.experts + slots / (16 * g.mt);
-    const int64_t units = most < slots ? most : slots, items = units * (a.e.inter / 32);
-    const int64_t steps = a.e.hidden / 128;
-    g.kw = 8;
-    while (g.kw > 1 && (items * g.kw > 4096 || g.kw > steps || g.kw * g.mt > 16)) g.kw /= 2;
-    const int64_t groups = (items * g.kw + 7) / 8, room = 2 * (int64_t)device_cus();
-    g.up = (unsigned)(groups < room ? groups : room);
-    g.down = (unsigned)(a.e.hidden / 16);
-    g.up_lds = sizeof(MoePlan) + (g.kw > 1 ? (size_t)8 * 4 * g.mt * 1024 : 0);
-    // K parts of few slots: to 1024 rows
-    g.rows = (int)(slots >= 1024 ? slots : 16 * slots < 1024 ? 16 * slots : 1024);
-    g.down_lds = sizeof(MoePlan) + (size_t)g.rows * 64;
+    g.wave = g.mt == 1 && slots <= kWaveSlots;
+    const int64_t most = slots < experts ? slots : experts + slots / (16 * g.mt);
+    const int64_t units = most < slots ? most : slots;
+    const size_t plan = g.wave ? 0 : sizeof(MoePlan);
+    if (g.up_tiles) {
+        const int64_t items = units * up_groups;
+        g.up = (unsigned)(items < 2 * cus ? items : 2 * cus);
+    } else {
+        const int64_t items = units * blocks, steps = a.e.hidden / 128;
+        g.kw = 8;
+        while (g.kw > 1 && (items * g.kw > 8 * cus || g.kw > steps || g.kw * g.mt > 16)) g.kw /= 2;
+        const int64_t groups = (items * g.kw + 7) / 8;
+        g.up = (unsigned)(groups < 2 * cus ? groups : 2 * cus);
+        g.up_lds = plan + (g.kw > 1 ? (size_t)8 * 4 * g.mt * 1024 : 0);
+    }
+    if (g.down_tiles) {
+        const int64_t chunks_k = (a.e.inter + 511) / 512;
+        g.ks = 1;
+        while (2 * g.ks * met * down_groups <= 2 * cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k) g.ks *= 2;
+        const int64_t items = units * down_groups * g.ks;
+        g.down = (unsigned)(items < 2 * cus ? items : 2 * cus);
+        g.join = (unsigned)((a.tokens * (a.e.hidden / 4) + 255) / 256);
+    } else {
+        g.down = (unsigned)(a.e.hidden / 16);
+        // K parts of few slots: to 1024 rows
+        g.rows = (int)(slots >= 1024 ? slots : 16 * slots < 1024 ? 16 * slots : 1024);
+        g.down_lds = plan + (size_t)g.rows * 64 + (size_t)((slots + 3) / 4 * 16);
+    }
     return g;
 }
 
@@ -437,29 +946,68 @@ MoeGrid moe_grid(const MoeArgs& a) {
 hipError_t raise_lds(const void* f, size_t bytes) {
     return bytes <= 64 * 1024 ? hipSuccess : hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
 }
-
-template <int MT>
-hipError_t launch_mt(const MoeGrid& g, const UpArgs& up, const DownArgs& down, hipStream_t stream) {
-    hipError_t e = raise_lds((const void*)up_kernel<MT>, g.up_lds);
-    if (e == hipSuccess) e = raise_lds((const void*)down_kernel<MT>, g.down_lds);
+template <typename A>
+hipError_t launch_one(void (*f)(A), unsigned x, unsigned y, int threads, size_t bytes, hipStream_t stream, const A& a) {
+    const hipError_t e = raise_lds((const void*)f, bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(up_kernel<MT>, dim3(g.up, g.chunks), dim3(kUpThreads), g.up_lds, stream, up);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(down_kernel<MT>, dim3(g.down, g.chunks), dim3(kDownThreads), g.down_lds, stream, down);
+    hipLaunchKernelGGL(f, dim3(x, y), dim3(threads), bytes, stream, a);
     return hipGetLastError();
+}
+
+// column tiles of the tile kernels' units by the slots that an expert has on average, some to spare
+int tile_columns(const MoeGrid& g, int experts) {
+    const int64_t each = g.slots / experts;
+    return each <= 18 ? 2 : each <= 44 ? 4 : 6;
+}
+template <int MT>
+hipError_t launch_up_tiles(const MoeGrid& g, const UpArgs& a, hipStream_t stream) {
+    return launch_one(up_tile_kernel<MT>, g.up, g.chunks, kTileThreads, sizeof(MoePlan) + 2 * 16 * MT * kChunkBytes, stream, a);
+}
+template <int MT>
+hipError_t launch_down_tiles(const MoeGrid& g, const DownTileArgs& a, hipStream_t stream) {
+    return launch_one(down_tile_kernel<MT>, g.down, g.chunks, kTileThreads, sizeof(MoePlan) + 2 * 16 * MT * (kChunkBytes + 16),
+                      stream, a);
+}
+
+hipError_t launch_up(const MoeGrid& g, const UpArgs& a, hipStream_t stream) {
+    if (g.up_tiles) {
+        switch (tile_columns(g, a.m.experts)) {
+            case 2: return launch_up_tiles<2>(g, a, stream);
+            case 4: return launch_up_tiles<4>(g, a, stream);
+            default: return launch_up_tiles<6>(g, a, stream);
+        }
+    }
+    const auto f = g.wave ? up_kernel<1, 4, true> : g.mt == 1 ? up_kernel<1, 4, false> : g.mt == 2 ? up_kernel<2, 2, false> : up_kernel<4, 2, false>;
+    return launch_one(f, g.up, g.chunks, kUpThreads, g.up_lds, stream, a);
+}
+hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStream_t stream) {
+    if (g.down_tiles) {
+        const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks};
+        hipError_t e;
+        switch (tile_columns(g, a.m.experts)) {
+            case 2: e = launch_down_tiles<2>(g, d, stream); break;
+            case 4: e = launch_down_tiles<4>(g, d, stream); break;
+            default: e = launch_down_tiles<6>(g, d, stream);
+        }
+        return e != hipSuccess ? e : launch_one(join_kernel, g.join, 1, 256, 0, stream, d);
+    }
+    const auto f = g.wave ? down_kernel<1, 6, true> : g.mt == 1 ? down_kernel<1, 6, false> : g.mt == 2 ? down_kernel<2, 3, false> : down_kernel<4, 2, false>;
+    return launch_one(f, g.down, g.chunks, kDownThreads, g.down_lds, stream, a);
 }
 
 }  // namespace
 
-size_t moe_workspace_bytes(int64_t slots, int64_t inter) {
-    return (size_t)(slots * (inter + exponent_stride(inter)));
+// v's codes and exponents, then (16-byte aligned) the partial sums
+size_t moe_workspace_bytes(int64_t slots, int64_t hidden, int64_t inter) {
+    const int64_t rows = slots >= kSumRows ? slots : 4 * slots < kSumRows ? 4 * slots : kSumRows;
+    return (size_t)(slots * (inter + exponent_stride(inter)) + rows * hidden * 4);
 }
 
 int64_t moe_threads(const MoeArgs& a) {
     const MoeGrid g = moe_grid(a);
-    return (int64_t)g.chunks * ((int64_t)g.up * kUpThreads > (int64_t)g.down * kDownThreads ? (int64_t)g.up * kUpThreads
-                                                                                             : (int64_t)g.down * kDownThreads);
+    const int64_t up = (int64_t)g.chunks * g.up * kUpThreads, down = (int64_t)g.chunks * g.down * kDownThreads;
+    const int64_t join = (int64_t)g.join * 256, most = up > down ? up : down;
+    return most > join ? most : join;
 }
 
 hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
@@ -469,14 +1017,12 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
     m.experts = a.e.experts, m.top_k = a.top_k, m.chunk = (int)moe_chunk_tokens(a.top_k);
     m.h_steps = (int)(a.e.hidden / 128), m.i_steps = (int)(a.e.inter / 128);
     m.e_stride = exponent_stride(a.e.inter);
-    m.v = a.ws, m.ve = a.ws + a.tokens * a.top_k * a.e.inter;
-    const UpArgs up{m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw};
-    const DownArgs down{m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows};
-    switch (g.mt) {
-        case 1: return launch_mt<1>(g, up, down, stream);
-        case 2: return launch_mt<2>(g, up, down, stream);
-        default: return launch_mt<4>(g, up, down, stream);
-    }
+    const int64_t slots = a.tokens * a.top_k;
+    m.v = a.ws, m.ve = a.ws + slots * a.e.inter;
+    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw}, stream);
+    if (e != hipSuccess) return e;
+    return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows, g.slots},
+                       reinterpret_cast<float*>(m.ve + slots * m.e_stride), stream);
 }
 
 }  // namespace w4a8

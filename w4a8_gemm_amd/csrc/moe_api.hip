@@ -79,13 +79,13 @@ w4a8_status w4a8_moe_route(w4a8_float type, const void* d_logits, int64_t ld, in
     return hip_status(launch_moe_route(a, type, as_stream(stream)));
 }
 
-static bool moe_shape(int64_t tokens, int top_k, int64_t inter) {
-    return tokens >= 1 && top_k >= 1 && top_k <= kMaxTopK && inter >= 128 && inter <= kMaxWidth && inter % 128 == 0 &&
+static bool moe_shape(int64_t tokens, int top_k, int64_t hidden, int64_t inter) {
+    return hidden >= 128 && hidden <= kMaxWidth && hidden % 128 == 0 && tokens >= 1 && top_k >= 1 && top_k <= kMaxTopK && inter >= 128 && inter <= kMaxWidth && inter % 128 == 0 &&
            tokens < kMaxCount / top_k && tokens <= kMaxChunks * moe_chunk_tokens(top_k);
 }
 
-size_t w4a8_moe_workspace_bytes(int64_t tokens, int top_k, int64_t inter) {
-    return moe_shape(tokens, top_k, inter) ? moe_workspace_bytes(tokens * top_k, inter) : 0;
+size_t w4a8_moe_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inter) {
+    return moe_shape(tokens, top_k, hidden, inter) ? moe_workspace_bytes(tokens * top_k, hidden, inter) : 0;
 }
 
 w4a8_status w4a8_moe_mxfp4(const w4a8_experts_mxfp4* experts, const uint8_t* d_x_fp8, const float* d_x_scale,
@@ -100,17 +100,17 @@ w4a8_status w4a8_moe_mxfp4(const w4a8_experts_mxfp4* experts, const uint8_t* d_x
         !aligned(experts->down_s, 16) || !aligned(d_x_fp8, 16) || !aligned(d_x_scale, 4) || !aligned(d_ids, 4) ||
         !aligned(d_weights, 4) || !aligned(d_out, 8))
         return W4A8_ERR_INVALID_ARG;
-    if (experts->experts > kMaxExperts || top_k > experts->experts || experts->hidden % 128 || experts->hidden > kMaxWidth ||
-        !moe_shape(tokens, top_k, experts->inter))
+    if (experts->experts > kMaxExperts || top_k > experts->experts ||
+        !moe_shape(tokens, top_k, experts->hidden, experts->inter))
         return W4A8_ERR_UNSUPPORTED_SHAPE;
-    if (!d_ws || ws_bytes < moe_workspace_bytes(tokens * top_k, experts->inter) || !aligned(d_ws, 256))
-        return W4A8_ERR_WORKSPACE;
     MoeArgs a{};
     a.e = *experts;
     a.x8 = d_x_fp8, a.xs = d_x_scale, a.tokens = tokens;
     a.ids = d_ids, a.weights = d_weights, a.top_k = top_k, a.act = (int)act;
     a.out = d_out, a.ws = static_cast<uint8_t*>(d_ws);
     if (moe_threads(a) >= kGridThreads) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    if (!d_ws || ws_bytes < moe_workspace_bytes(tokens * top_k, experts->hidden, experts->inter) || !aligned(d_ws, 256))
+        return W4A8_ERR_WORKSPACE;
     return hip_status(launch_moe(a, as_stream(stream)));
 }
 

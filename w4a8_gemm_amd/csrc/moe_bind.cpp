@@ -183,7 +183,7 @@ PyObject* moe(PyObject* const* a, Py_ssize_t n) {
     if (tokens == 0) return THPVariable_Wrap(out);
     const c10::DeviceGuard guard(e.dev);
     const at::Tensor ws = a[6] != Py_None ? tensor(a[6], "workspace", at::kByte, e.dev)
-                                          : at::empty({(int64_t)w4a8_moe_workspace_bytes(tokens, (int)k, e.view.inter)}, x.options());
+                                          : at::empty({(int64_t)w4a8_moe_workspace_bytes(tokens, (int)k, e.view.hidden, e.view.inter)}, x.options());
     check(w4a8_moe_mxfp4(&e.view, static_cast<const uint8_t*>(x.const_data_ptr()), xs, tokens, ids.const_data_ptr<int32_t>(),
                          w.const_data_ptr<float>(), (int)k, act, static_cast<uint16_t*>(out.data_ptr()), ws.data_ptr(),
                          (size_t)ws.numel(), stream(e.dev)),

@@ -306,7 +306,7 @@ struct MoeArgs {
 // slots (token, j) that a workgroup lists at once, and the tokens of such a chunk
 constexpr int kMoeSlots = 2048;
 inline int64_t moe_chunk_tokens(int top_k) { return kMoeSlots / top_k; }
-size_t moe_workspace_bytes(int64_t slots, int64_t inter);
+size_t moe_workspace_bytes(int64_t slots, int64_t hidden, int64_t inter);
 int64_t moe_threads(const MoeArgs& a);
 hipError_t launch_moe(const MoeArgs& a, hipStream_t stream);
 

@@ -105,19 +105,19 @@ class ExpertsMXFP4:
         return cls(binding.mxfp4_prepare(up_packed, up_e8m0), binding.mxfp4_prepare(down_packed, down_e8m0), experts)
 
 
-def moe_workspace_bytes(tokens: int, top_k: int, inter: int) -> int:
-    return int(binding.lib().w4a8_moe_workspace_bytes(int(tokens), int(top_k), int(inter)))
+def moe_workspace_bytes(tokens: int, top_k: int, hidden: int, inter: int) -> int:
+    return int(binding.lib().w4a8_moe_workspace_bytes(int(tokens), int(top_k), int(hidden), int(inter)))
 
 
 class MoEWorkspace:
     """Caller-owned workspace of moe_mxfp4: what the first product hands to the second.  It
-    serves every call of at most these tokens with this top_k and inter.  Its contents
+    serves every call of at most these tokens with this top_k, hidden and inter.  Its contents
     mean nothing between calls; calls that share one must not overlap in time."""
 
     def __init__(self, tokens: int, top_k: int, experts: int, hidden: int, inter: int, device="cuda"):
         if min(tokens, top_k, experts, hidden, inter) < 1 or top_k > experts or hidden % 128 or inter % 128:
             raise ValueError("sizes must be positive, top_k at most experts, hidden and inter multiples of 128")
-        self.nbytes = moe_workspace_bytes(tokens, top_k, inter)
+        self.nbytes = moe_workspace_bytes(tokens, top_k, hidden, inter)
         if not self.nbytes:
             raise ValueError("sizes beyond what moe_mxfp4 serves")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
