@@ -53,42 +53,61 @@ __device__ __forceinline__ v4f product(v8i w, v8i x, v4f c, uint32_t sw, uint32_
 // slots by expert
 // ---------------------------------------------------------------------------
 struct alignas(16) MoePlan {
-    uint32_t count[kMaxExperts + 1];    // slots of each expert, then its first place in `list` (and the end of the last)
-    uint16_t list[kMoeSlots];           // slots (of the chunk) by expert
+    uint16_t list[kMoeSlots];           // slots (of the chunk) by expert, in order
     uint32_t unit[kMoeSlots];           // first place | (slots - 1) << 11 | expert << 18
     uint32_t part[16];
-    int units, several;                 // several: some expert has more than one unit
+    int units;
 };
 __device__ __forceinline__ int unit_first(uint32_t u) { return u & 2047; }
 __device__ __forceinline__ int unit_slots(uint32_t u) { return ((u >> 11) & 127) + 1; }
 __device__ __forceinline__ int unit_expert(uint32_t u) { return u >> 18; }
 
-// All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 128).  The atomics
-// list an expert's slots in any order.  Where workgroups share an expert of several units
-// (ORDER) they have to agree on which slots are whose: such an expert's are sorted, each
-// slot counting the smaller ones.
-template <int NT, int US, bool ORDER>
-__device__ void make_plan(MoePlan& p, const int32_t* ids, int slots, int experts) {
+// LDS that make_plan works in: how many slots of each 64 each expert has, and their first places
+size_t plan_scratch(int64_t slots, int64_t experts) { return (size_t)(((slots + 63) / 64 + 2) * ((experts + 3) / 4 * 4)); }
+
+// All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 128).  Slots keep their
+// order within an expert, so that all workgroups agree on the units: each wave ranks 64 slots
+// by the equal ids before them (ids compared bit by bit over the wave), and the counts of the
+// 64s are summed up for each expert.  No atomics.
+template <int NT, int US>
+__device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int slots, int experts) {
     constexpr int kPer = kMoeSlots / NT, kExp = kMaxExperts / NT;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int e = tid; e < experts; e += NT) p.count[e] = 0;
-    if (tid == 0) p.several = 0;
-    __syncthreads();
-    int id[kPer], at[kPer];
+    const int e4 = (experts + 3) / 4 * 4, lots = (slots + 63) / 64;
+    uint8_t* count = scratch;                                          // [64 slots][expert]
+    uint16_t* first = reinterpret_cast<uint16_t*>(scratch + lots * e4);
+    int id[kPer], rank[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int s = tid + i * NT;
         id[i] = s < slots ? ids[s] : -1;
         if ((uint32_t)id[i] >= (uint32_t)experts) id[i] = -1;
-        if (id[i] >= 0) at[i] = (int)atomicAdd(&p.count[id[i]], 1u);
+    }
+    for (int i = tid; i < lots * e4 / 4; i += NT) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    __syncthreads();
+    const int bits = 32 - __builtin_clz(experts);   // of ids, with a bit that only -1 has
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int lot = wave + i * (NT / 64);
+        if (lot >= lots) break;   // the same for the wave
+        uint64_t same = ~0ull;
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t on = __ballot((id[i] >> b) & 1);
+            same &= (id[i] >> b) & 1 ? on : ~on;
+        }
+        rank[i] = __popcll(same & ((1ull << lane) - 1));
+        if (id[i] >= 0 && rank[i] == 0) count[lot * e4 + id[i]] = (uint8_t)__popcll(same);
     }
     __syncthreads();
-    // exclusive sums over the experts of slots (low half) and units (high half)
+    // an expert's counts, summed over the 64s before each, and exclusive sums over the experts of slots
+    // (low half) and units (high half)
     uint32_t mine[kExp], sum = 0;
 #pragma unroll
     for (int i = 0; i < kExp; ++i) {
         const int e = tid * kExp + i;
-        const uint32_t c = e < experts ? p.count[e] : 0u;
+        uint32_t c = 0;
+        if (e < experts)
+            for (int l = 0; l < lots; ++l) c += count[l * e4 + e];
         mine[i] = c | ((c + US - 1) / US) << 16;
         sum += mine[i];
     }
@@ -102,41 +121,25 @@ __device__ void make_plan(MoePlan& p, const int32_t* ids, int slots, int experts
     __syncthreads();
     uint32_t before = incl - sum;
     for (int i = 0; i < wave; ++i) before += p.part[i];
-    if (tid == NT - 1) p.units = (int)((before + sum) >> 16), p.count[experts] = (before + sum) & 0xFFFFu;
+    if (tid == NT - 1) p.units = (int)((before + sum) >> 16);
 #pragma unroll
     for (int i = 0; i < kExp; ++i) {
-        const int e = tid * kExp + i, c = mine[i] & 0xFFFFu, first = before & 0xFFFFu;
+        const int e = tid * kExp + i, c = mine[i] & 0xFFFFu, at = before & 0xFFFFu;
         int u = before >> 16;
-        if (e < experts) p.count[e] = first;
-        if (ORDER && c > US) p.several = 1;
+        if (e < experts) first[e] = (uint16_t)at;
         for (int k = 0; k < c; k += US, ++u)
-            p.unit[u] = (uint32_t)(first + k) | (uint32_t)(min(c - k, US) - 1) << 11 | (uint32_t)e << 18;
+            p.unit[u] = (uint32_t)(at + k) | (uint32_t)(min(c - k, US) - 1) << 11 | (uint32_t)e << 18;
         before += mine[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (id[i] >= 0) p.list[p.count[id[i]] + at[i]] = (uint16_t)(tid + i * NT);
-    __syncthreads();
-    if constexpr (ORDER) {
-        if (!p.several) return;   // the same in all threads
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (id[i] < 0) continue;
-            const int first = p.count[id[i]], end = p.count[id[i] + 1], s = tid + i * NT;
-            if (end - first <= US) {
-                id[i] = -1;
-                continue;
-            }
-            at[i] = first;
-            for (int k = first; k < end; ++k) at[i] += p.list[k] < s;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (id[i] >= 0) p.list[at[i]] = (uint16_t)(tid + i * NT);
-        __syncthreads();
+    for (int i = 0; i < kPer; ++i) {
+        if (id[i] < 0) continue;
+        int at = first[id[i]] + rank[i];
+        for (int l = 0; l < wave + i * (NT / 64); ++l) at += count[l * e4 + id[i]];
+        p.list[at] = (uint16_t)(tid + i * NT);
     }
+    __syncthreads();
 }
 
 // Up to 64 slots: every wave lists them in its registers, lane s holding slot s.  No LDS, no
@@ -165,32 +168,29 @@ __device__ __forceinline__ WaveList wave_list(const int32_t* ids, int slots, int
     r.starts = __ballot(r.id >= 0 && (r.rank & 15) == 0);
     return r;
 }
-// A unit as a wave has it: lane n (of 16) of column tile j has slot[j] in column 16 j + n, the
-// columns past cols the last one's
-template <int MT>
+// A unit of up to 16 slots as a wave has it: lanes n, n + 16, ... have the slot of column n, those
+// past cols the last one's
 struct Unit {
-    int expert, cols;
-    int slot[MT];
+    int expert, cols, slot;
 };
-__device__ __forceinline__ void wave_unit(const WaveList& l, int u, Unit<1>& r) {
+__device__ __forceinline__ Unit wave_unit(const WaveList& l, int u) {
     const int lane = threadIdx.x & 63;
     const bool here = ((l.starts >> lane) & 1) && __popcll(l.starts & ((1ull << lane) - 1)) == u;
     const int at = __builtin_ctzll(__ballot(here));
     const int first = __builtin_amdgcn_readlane(l.rank, at);
+    Unit r;
     r.expert = __builtin_amdgcn_readlane(l.id, at);
     const bool in = l.id == r.expert && l.rank >= first && l.rank < first + 16;
     r.cols = __popcll(__ballot(in));
     // each slot to the lane of its column (the others to lanes that are not read)
     const int got = __builtin_amdgcn_ds_permute(4 * (in ? l.rank - first : 16 + (lane & 15)), lane);
-    r.slot[0] = __builtin_amdgcn_ds_bpermute(4 * min(lane & 15, r.cols - 1), got);
+    r.slot = __builtin_amdgcn_ds_bpermute(4 * min(lane & 15, r.cols - 1), got);
+    return r;
 }
-template <int MT>
-__device__ __forceinline__ void plan_unit(const MoePlan& p, int u, Unit<MT>& r) {
+__device__ __forceinline__ Unit plan_unit(const MoePlan& p, int u) {
     const uint32_t v = uniform(p.unit[u]);
-    r.expert = unit_expert(v);
-    r.cols = unit_slots(v);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) r.slot[j] = p.list[unit_first(v) + min(16 * j + (int)(threadIdx.x & 15), r.cols - 1)];
+    const int cols = unit_slots(v);
+    return {unit_expert(v), cols, p.list[unit_first(v) + min((int)(threadIdx.x & 15), cols - 1)]};
 }
 
 struct MoeShape {
@@ -206,6 +206,7 @@ struct UpArgs {
     const float* xs;
     const int32_t* ids;
     int act, kw;
+    int plan_at;                        // of the plan in LDS; before it the kernel's own, and the plan's making
 };
 struct DownArgs {
     MoeShape m;
@@ -213,7 +214,7 @@ struct DownArgs {
     const int32_t* ids;
     const float* weights;
     uint16_t* out;
-    int rows, slots;                    // of partial sums that LDS holds; of a chunk at most
+    int rows;                           // of partial sums that LDS holds, the slots' weights after them
 };
 struct DownTileArgs {
     MoeShape m;
@@ -223,6 +224,7 @@ struct DownTileArgs {
     uint16_t* out;
     float* sums;
     int ks;                             // K parts
+    int plan_at;
 };
 
 // ---------------------------------------------------------------------------
@@ -234,27 +236,17 @@ __device__ __forceinline__ float activated(float g, int act) {
     return g / (1.0f + expf(-2.0f * t));   // (1 + tanh t) / 2
 }
 
-// One step's products of a 16-row tile with 16 columns, for the first product.
+// One step's products of a 16-row tile with 16 columns, for the first product of few tokens.
 //
 // The e2m1 x e4m3 instruction aligns its 128 products to the largest and cuts what lies 2^-14
 // below it.  That is far under what bf16 outputs show, but v is rounded to four bits next, and a
 // value that the cut takes over the border of two codes moves by a whole step: for one token
 // such a step of a large value is the output's error (0.0036 of it for 0.0016, one token
-// through 8 of 128 experts).  Where tokens are few (BF16) the operands are widened instead, exact
-// as both are, and the products added in fp32; it takes 4 instructions for one, which a kernel
-// that waits for its weights has time for.  With more tokens the rare steps average out.
-template <bool BF16>
-struct Columns;
-template <>
-struct Columns<false> {
-    v8i x;
-    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) { x = frag_fp8(lo, hi); }
-    __device__ __forceinline__ v4f times(uint4 w, uint32_t scale, v4f c) const {
-        return product(frag_fp4(w), x, c, scale, kUnitScale);
-    }
-};
-template <>
-struct Columns<true> {
+// through 8 of 128 experts).  So here the operands are widened to bf16, exact as both are, and the
+// products added in fp32; it takes 4 instructions for one, which a kernel that waits for its
+// weights has time for.  With more tokens (the tile kernels) the rare steps average out.
+// A lane's 32 k are those of its weights, 32 g to 32 g + 31 of the step.
+struct Columns {
     v8bf x[4];
     __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
 #pragma unroll
@@ -285,11 +277,10 @@ struct Columns<true> {
     }
 };
 
-template <int MT>
 struct UpStep {
     uint4 w[4];            // gate rows i0 .. +15 and +16 .. +31, then the up rows
     uint32_t s[4];
-    u32x4 x[MT][2];
+    u32x4 x[2];
 };
 
 // v of 32 of inter (block blk) for 16 columns, from the sums of the tiles: a lane has 4 values of each half
@@ -321,21 +312,21 @@ __device__ __forceinline__ void store_v(const MoeShape& m, const v4f (&r)[4], fl
         m.ve[row * m.e_stride + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] = finite ? (uint8_t)(e + 127) : 255;
 }
 
-// WAVE: up to 64 slots, listed by every wave.  D: steps in flight.
-template <int MT, int D, bool WAVE>
+// WAVE: up to 64 slots, listed by every wave; else listed in LDS.  Four steps in flight.
+template <bool WAVE>
 __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
-    constexpr bool kBf16 = MT == 1;
+    constexpr int D = 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    MoePlan& p = *reinterpret_cast<MoePlan*>(lds);
-    float4* join = reinterpret_cast<float4*>(lds + (WAVE ? 0 : sizeof(MoePlan)));   // [wave][tile][MT][lane]
+    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
+    float4* join = reinterpret_cast<float4*>(lds);   // [wave][tile][lane]
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
     WaveList list;
     if constexpr (WAVE)
-        list = wave_list(a.ids + t0 * m.top_k, slots, m.experts);
+        list = wave_list(a.ids, slots, m.experts);
     else
-        make_plan<kUpThreads, 16 * MT, true>(p, a.ids + t0 * m.top_k, slots, m.experts);
+        make_plan<kUpThreads, 16>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int kw = a.kw, part = wave % kw, per_wg = 8 / kw;
@@ -348,20 +339,11 @@ __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
         const int item = base + wave / kw;
         const bool live = item < items;
         const int blk = live ? item % blocks : 0;
-        Unit<MT> u;
-        if constexpr (WAVE)
-            wave_unit(list, live ? item / blocks : 0, u);
-        else
-            plan_unit(p, live ? item / blocks : 0, u);
-        uint32_t xo[MT];
-        float sx[MT];
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            const int t = u.slot[j] / m.top_k;
-            xo[j] = (uint32_t)t * (uint32_t)m.hidden + (kBf16 ? 32 : 16) * g;
-            sx[j] = a.xs[t0 + t];
-        }
-        const uint8_t *wp[4];
+        const Unit u = WAVE ? wave_unit(list, live ? item / blocks : 0) : plan_unit(p, live ? item / blocks : 0);
+        const int t = u.slot / m.top_k;
+        const uint32_t xo = (uint32_t)t * (uint32_t)m.hidden + 32 * g;
+        const float sx = a.xs[t0 + t];
+        const uint8_t* wp[4];
         const uint32_t* sp[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -369,34 +351,26 @@ __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
             wp[q] = a.w + tile * c_pad * 4096;
             sp[q] = reinterpret_cast<const uint32_t*>(a.s) + tile * c_pad * 64;
         }
-        v4f acc[4][MT];
+        v4f acc[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        const auto load = [&](int s, UpStep<MT>& r) {
+        for (int q = 0; q < 4; ++q) acc[q] = v4f{0.f, 0.f, 0.f, 0.f};
+        const auto load = [&](int s, UpStep& r) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 r.w[q] = load_stream16(reinterpret_cast<const uint4*>(wp[q] + s * 1024) + lane);
                 r.s[q] = (sp[q] + (s >> 2) * 64)[lane];
             }
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                r.x[j][0] = *reinterpret_cast<const u32x4*>(x + 128 * s + xo[j]);
-                r.x[j][1] = *reinterpret_cast<const u32x4*>(x + 128 * s + (kBf16 ? 16 : 64) + xo[j]);
-            }
+            r.x[0] = *reinterpret_cast<const u32x4*>(x + 128 * s + xo);
+            r.x[1] = *reinterpret_cast<const u32x4*>(x + 128 * s + 16 + xo);
         };
-        const auto compute = [&](int s, const UpStep<MT>& r) {
+        const auto compute = [&](int s, const UpStep& r) {
+            Columns c;
+            c.set(r.x[0], r.x[1]);
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                Columns<kBf16> c;
-                c.set(r.x[j][0], r.x[j][1]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[q][j] = c.times(r.w[q], r.s[q] >> (8 * (s & 3)), acc[q][j]);
-            }
+            for (int q = 0; q < 4; ++q) acc[q] = c.times(r.w[q], r.s[q] >> (8 * (s & 3)), acc[q]);
         };
         if (live) {
-            UpStep<MT> ring[D];
+            UpStep ring[D];
 #pragma unroll
             for (int d = 0; d < D - 1; ++d)
                 if (s0 + d < s1) load(s0 + d, ring[d]);
@@ -410,30 +384,20 @@ __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
         }
         if (kw > 1) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    join[((wave * 4 + q) * MT + j) * 64 + lane] = make_float4(acc[q][j][0], acc[q][j][1], acc[q][j][2], acc[q][j][3]);
+            for (int q = 0; q < 4; ++q) join[(wave * 4 + q) * 64 + lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
             __syncthreads();
         }
-        // column tile j of the item by the wave of part j % kw: parts in order
+        if (live && part == 0) {
+            if (kw > 1) {   // the parts in order
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            if (!live || j % kw != part) continue;
-            v4f r[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (kw == 1) {
-                    r[q] = acc[q][j];
-                    continue;
-                }
-                r[q] = v4f{0.f, 0.f, 0.f, 0.f};
-                for (int k = 0; k < kw; ++k) {
-                    const float4 f = join[(((wave - part + k) * 4 + q) * MT + j) * 64 + lane];
-                    r[q] += v4f{f.x, f.y, f.z, f.w};
+                for (int q = 0; q < 4; ++q) {
+                    for (int k = 1; k < kw; ++k) {
+                        const float4 f = join[((wave + k) * 4 + q) * 64 + lane];
+                        acc[q] += v4f{f.x, f.y, f.z, f.w};
+                    }
                 }
             }
-            store_v(m, r, sx[j], a.act, t0 * m.top_k + u.slot[j], blk, g, 16 * j + n < u.cols);
+            store_v(m, acc, sx, a.act, t0 * m.top_k + u.slot, blk, g, n < u.cols);
         }
         if (kw > 1) __syncthreads();
     }
@@ -442,81 +406,54 @@ __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
 // ---------------------------------------------------------------------------
 // down
 // ---------------------------------------------------------------------------
-template <int MT>
 struct DownStep {
     uint4 w;
     uint32_t s;
-    u32x4 x[MT][2];
-    uint32_t e[MT];
+    u32x4 x[2];
+    uint32_t e;
 };
 
-template <int MT, int D, bool WAVE>
+// Up to 64 slots.  Six steps in flight.
 __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
+    constexpr int D = 6, kWaves = kDownThreads / 64;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const MoeShape& m = a.m;
-    const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
-    const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
-    const int32_t* ids = a.ids + t0 * m.top_k;
-    // LDS: partial sums [slot][K part][16 columns], the slots' weights, the plan
+    const int tokens = (int)m.tokens, slots = tokens * m.top_k;
+    // LDS: partial sums [slot][K part][16 columns], the slots' weights
     float4* part = reinterpret_cast<float4*>(lds);
     float* share = reinterpret_cast<float*>(lds + (size_t)a.rows * 64);
-    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + (size_t)a.rows * 64 + (size_t)((a.slots + 3) / 4 * 16));
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-    constexpr int kWaves = kDownThreads / 64;
-    WaveList list;
-    if constexpr (WAVE)
-        list = wave_list(ids, slots, m.experts);
-    else
-        make_plan<kDownThreads, 16 * MT, false>(p, ids, slots, m.experts);
-    const int units = WAVE ? list.units() : p.units;
+    const WaveList list = wave_list(a.ids, slots, m.experts);
+    const int units = list.units();
     int ks = 1;   // K parts: as many as give every wave one, while there are few units
     while (2 * ks * units <= kWaves && 2 * ks * slots <= a.rows && 2 * ks <= min(kWaves, m.i_steps)) ks *= 2;
     // slots without an expert add nothing
-    for (int s = threadIdx.x; s < slots; s += kDownThreads) {
-        const bool on = (uint32_t)ids[s] < (uint32_t)m.experts;
-        share[s] = on ? a.weights[t0 * m.top_k + s] : 0.0f;
-        if (!on)
-            for (int k = 0; k < 4 * ks; ++k) part[4 * s * ks + k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((int)threadIdx.x < slots) {
+        share[lane] = list.id >= 0 ? a.weights[lane] : 0.0f;
+        if (list.id < 0)
+            for (int k = 0; k < 4 * ks; ++k) part[4 * lane * ks + k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const int c_pad = (m.i_steps + 3) / 4;
-    const uint8_t *x = m.v + t0 * m.top_k * m.inter, *e = m.ve + t0 * m.top_k * m.e_stride;
     for (int item = wave; item < units * ks; item += kWaves) {
         const int k = item % ks;
-        Unit<MT> u;
-        if constexpr (WAVE)
-            wave_unit(list, item / ks, u);
-        else
-            plan_unit(p, item / ks, u);
+        const Unit u = wave_unit(list, item / ks);
         const int64_t tile = u.expert * (m.hidden / 16) + blockIdx.x;
         const uint8_t* wp = a.w + tile * c_pad * 4096;
         const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.s) + tile * c_pad * 64;
-        uint32_t xo[MT], eo[MT];
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            xo[j] = (uint32_t)u.slot[j] * (uint32_t)m.inter + 16 * g;
-            eo[j] = (uint32_t)u.slot[j] * (uint32_t)m.e_stride + 4 * g;
-        }
-        v4f acc[MT];
-#pragma unroll
-        for (int j = 0; j < MT; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
-        const auto load = [&](int s, DownStep<MT>& r) {
+        const uint32_t xo = (uint32_t)u.slot * (uint32_t)m.inter + 16 * g, eo = (uint32_t)u.slot * (uint32_t)m.e_stride + 4 * g;
+        v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+        const auto load = [&](int s, DownStep& r) {
             r.w = load_stream16(reinterpret_cast<const uint4*>(wp + s * 1024) + lane);
             r.s = (sp + (s >> 2) * 64)[lane];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                r.x[j][0] = *reinterpret_cast<const u32x4*>(x + 128 * s + xo[j]);
-                r.x[j][1] = *reinterpret_cast<const u32x4*>(x + 128 * s + 64 + xo[j]);
-                r.e[j] = *reinterpret_cast<const uint32_t*>(e + (s >> 2) * 16 + eo[j]);
-            }
+            r.x[0] = *reinterpret_cast<const u32x4*>(m.v + 128 * s + xo);
+            r.x[1] = *reinterpret_cast<const u32x4*>(m.v + 128 * s + 64 + xo);
+            r.e = *reinterpret_cast<const uint32_t*>(m.ve + (s >> 2) * 16 + eo);
         };
-        const auto compute = [&](int s, const DownStep<MT>& r) {
-#pragma unroll
-            for (int j = 0; j < MT; ++j)
-                acc[j] = product(frag_fp4(r.w), frag_fp8(r.x[j][0], r.x[j][1]), acc[j], r.s >> (8 * (s & 3)),
-                                 r.e[j] >> (8 * (s & 3)));
+        const auto compute = [&](int s, const DownStep& r) {
+            acc = product(frag_fp4(r.w), frag_fp8(r.x[0], r.x[1]), acc, r.s >> (8 * (s & 3)), r.e >> (8 * (s & 3)));
         };
         const int s0 = m.i_steps * k / ks, s1 = m.i_steps * (k + 1) / ks;
-        DownStep<MT> ring[D];
+        DownStep ring[D];
 #pragma unroll
         for (int d = 0; d < D - 1; ++d)
             if (s0 + d < s1) load(s0 + d, ring[d]);
@@ -527,15 +464,12 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
                 if (s + d < s1) compute(s + d, ring[d]);
             }
         }
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-            if (16 * j + n < u.cols)
-                part[(u.slot[j] * ks + k) * 4 + g] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        if (n < u.cols) part[(u.slot * ks + k) * 4 + g] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
     __syncthreads();
     // four columns of a token to a thread: its slots in order
-    for (int i = threadIdx.x; i < 4 * tokens; i += kDownThreads) {
-        const int t = i >> 2, q = i & 3;
+    if ((int)threadIdx.x < 4 * tokens) {
+        const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
         v4f sum = v4f{0.f, 0.f, 0.f, 0.f};
         for (int s = t * m.top_k; s < (t + 1) * m.top_k; ++s) {
             v4f v = v4f{0.f, 0.f, 0.f, 0.f};
@@ -546,7 +480,7 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(share[s], v[c], sum[c]);
         }
-        *reinterpret_cast<uint2*>(a.out + (t0 + t) * m.hidden + 16 * blockIdx.x + 4 * q) =
+        *reinterpret_cast<uint2*>(a.out + (int64_t)t * m.hidden + 16 * blockIdx.x + 4 * q) =
             make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
     }
 }
@@ -556,8 +490,8 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
 // ---------------------------------------------------------------------------
 // A workgroup takes a unit and eight waves' worth of weight rows; the unit's columns (up to
 // 16 MT) are staged for all eight in LDS, 512 k (a chunk of the scales) at a time, two
-// buffers.  A wave's weights for a whole chunk are in flight: each step's registers are
-// asked for again, one chunk on, as soon as its products are issued, and the next chunk's
+// buffers.  A wave's weights of D steps are in flight: each step's registers are
+// asked for again, D steps on, as soon as its products are issued, and the next chunk's
 // columns are asked for before them, so that waiting for those leaves the weights in flight.
 // Every step of a chunk is computed: past K the columns are zeros, and the weights those of the
 // last step.  So are all MT column tiles: those without slots cost products that the
@@ -639,18 +573,18 @@ __device__ __forceinline__ void hold(v4f (&acc)[Q][MT]) {
         for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[q][j]));
 }
 
-// R weight tiles of a wave: a chunk's codes and scale dwords
-template <int R>
+// R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk
+template <int R, int D>
 struct Tiles {
     const uint8_t* w[R];
     const uint32_t* s[R];
-    uint4 q[4][R];
+    uint4 q[D][R];
     uint32_t sc[R], next[R];
     __device__ __forceinline__ void at(int r, const uint8_t* wt, const uint8_t* st, int64_t tile, int c_pad) {
         w[r] = wt + tile * c_pad * 4096;
         s[r] = reinterpret_cast<const uint32_t*>(st) + tile * c_pad * 64;
     }
-    __device__ __forceinline__ void load(int step, int to) {
+    __device__ __forceinline__ void load(int step, int to) {   // to: step % D
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int r = 0; r < R; ++r) q[to][r] = load_stream16(reinterpret_cast<const uint4*>(w[r] + step * 1024) + lane);
@@ -670,15 +604,15 @@ struct Tiles {
     }
 };
 
-template <int MT>
+template <int MT, int D>
 __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int kBuf = 16 * MT * kChunkBytes;
-    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + 2 * kBuf);
+    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
-    make_plan<kTileThreads, 16 * MT, true>(p, a.ids + t0 * m.top_k, slots, m.experts);
+    make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const ColumnReader cr;
@@ -696,13 +630,13 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
             row[i] = (uint32_t)(p.list[first + min(16 * i + (int)(threadIdx.x >> 5), cols - 1)] / m.top_k) * (uint32_t)m.hidden;
         Stage<MT> st;
         st.load(x, row, 0, m.hidden, cols);
-        Tiles<4> w;
+        Tiles<4, D> w;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             w.at(q, a.w, a.s, (2 * unit_expert(u) + (q >> 1)) * tiles_i + 2 * (live ? blk : blocks - 1) + (q & 1), chunks);
         w.load_scales(0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) w.load(min(s, steps - 1), s);
+        for (int s = 0; s < D; ++s) w.load(min(s, steps - 1), s);
         v4f acc[4][MT];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -716,7 +650,7 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
             for (int j = 0; j < MT; ++j) {
                 const v8i b = cr.read(buf, j, s);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s][q]), b, acc[q][j], w.sc[q]);
+                for (int q = 0; q < 4; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s % D][q]), b, acc[q][j], w.sc[q]);
                 if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);   // no more than two tiles' columns in registers
             }
         };
@@ -728,7 +662,7 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
                 products(lds + (c & 1) * kBuf, step);
                 hold(acc);
                 __builtin_amdgcn_sched_barrier(0);
-                w.load(min(4 * (c + 1) + s, steps - 1), s);
+                w.load(min(4 * c + s + D, steps - 1), s % D);
                 __builtin_amdgcn_sched_barrier(0);
             });
             st.store(lds + ((c + 1) & 1) * kBuf, cols);
@@ -736,9 +670,11 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
         }
         w.last_scales();
         four_steps([&](auto step) {
+            constexpr int s = decltype(step)::value;
             products(lds + ((chunks - 1) & 1) * kBuf, step);
             hold(acc);
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (s + D < 4) w.load(min(4 * (chunks - 1) + s + D, steps - 1), s % D);
         });
         __syncthreads();   // before the next item's first columns
         if (live) {
@@ -755,15 +691,15 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
 
 // The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
 // device memory.
-template <int MT>
-__global__ __launch_bounds__(kTileThreads) void down_tile_kernel(DownTileArgs a) {
+template <int MT, int D>
+__global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kernel(DownTileArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int kCols = 16 * MT * kChunkBytes, kBuf = kCols + 16 * MT * 16;   // columns, then their exponents
-    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + 2 * kBuf);
+    MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
-    make_plan<kTileThreads, 16 * MT, true>(p, a.ids + t0 * m.top_k, slots, m.experts);
+    make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const ColumnReader cr;
@@ -786,12 +722,12 @@ __global__ __launch_bounds__(kTileThreads) void down_tile_kernel(DownTileArgs a)
         u32x4 er{};
         st.load(x, row, c0, m.inter, cols);
         if (has_e) er = exponents(ep, c0, steps);
-        Tiles<2> w;
+        Tiles<2, D> w;
 #pragma unroll
         for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, chunks);
         w.load_scales(c0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) w.load(min(4 * c0 + s, steps - 1), s);
+        for (int s = 0; s < D; ++s) w.load(min(4 * c0 + s, steps - 1), s);
         v4f acc[2][MT];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -814,7 +750,7 @@ __global__ __launch_bounds__(kTileThreads) void down_tile_kernel(DownTileArgs a)
             for (int j = 0; j < MT; ++j) {
                 const v8i b = cr.read(buf, j, s);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s][q]), b, acc[q][j], w.sc[q], e[j]);
+                for (int q = 0; q < 2; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s % D][q]), b, acc[q][j], w.sc[q], e[j]);
                 if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -829,7 +765,7 @@ __global__ __launch_bounds__(kTileThreads) void down_tile_kernel(DownTileArgs a)
                 products(buf, step);
                 hold(acc);
                 __builtin_amdgcn_sched_barrier(0);
-                w.load(min(4 * (c + 1) + s, steps - 1), s);
+                w.load(min(4 * c + s + D, steps - 1), s % D);
                 __builtin_amdgcn_sched_barrier(0);
             });
             put(lds + ((c - c0 + 1) & 1) * kBuf);
@@ -839,9 +775,11 @@ __global__ __launch_bounds__(kTileThreads) void down_tile_kernel(DownTileArgs a)
         const uint8_t* buf = lds + ((c1 - 1 - c0) & 1) * kBuf;
         read_e(buf);
         four_steps([&](auto step) {
+            constexpr int s = decltype(step)::value;
             products(buf, step);
             hold(acc);
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (s + D < 4) w.load(min(4 * (c1 - 1) + s + D, steps - 1), s % D);
         });
         __syncthreads();   // before the next item's first columns
         if (live) {
@@ -889,11 +827,11 @@ int64_t exponent_stride(int64_t inter) { return (inter + 511) / 512 * 16; }
 constexpr int64_t kSumRows = 2048;
 
 struct MoeGrid {
-    int mt;                         // column tiles of a unit
-    bool wave, up_tiles, down_tiles;
-    int kw, rows, slots, ks;
+    bool few, up_tiles;             // few: up to 64 slots
+    int mt;                         // column tiles of the tile kernels' units
+    int kw, rows, ks;
     unsigned up, down, join, chunks;
-    size_t up_lds, down_lds;
+    size_t up_at, down_at;          // LDS of the kernels before the plan
 };
 
 MoeGrid moe_grid(const MoeArgs& a) {
@@ -901,43 +839,44 @@ MoeGrid moe_grid(const MoeArgs& a) {
     const int64_t chunk = moe_chunk_tokens(a.top_k), cus = device_cus();
     g.chunks = (unsigned)((a.tokens + chunk - 1) / chunk);
     const int64_t slots = (a.tokens < chunk ? a.tokens : chunk) * a.top_k, experts = a.e.experts;
-    g.slots = (int)slots;
     // experts met, about: were the slots spread at random
     double missed = 1.0;
     for (int64_t s = 0; s < slots && missed > 1e-3; ++s) missed *= 1.0 - 1.0 / (double)experts;
     const int64_t met = (int64_t)((double)experts * (1.0 - missed) + 0.5);
-    const int64_t each = slots / experts;
     const int64_t blocks = a.e.inter / 32, up_groups = (blocks + 7) / 8, down_groups = (a.e.hidden / 16 + 15) / 16;
-    g.up_tiles = slots > kWaveSlots && met * up_groups >= 128;
-    g.down_tiles = slots > kWaveSlots;
-    g.mt = each <= 8 ? 1 : each <= 24 ? 2 : 4;
-    g.wave = g.mt == 1 && slots <= kWaveSlots;
-    const int64_t most = slots < experts ? slots : experts + slots / (16 * g.mt);
-    const int64_t units = most < slots ? most : slots;
-    const size_t plan = g.wave ? 0 : sizeof(MoePlan);
+    g.few = slots <= kWaveSlots;
+    g.up_tiles = !g.few && met * up_groups >= 128;
+    // by the slots that an expert has on average, with some to spare
+    const int64_t each = slots / experts;
+    g.mt = each <= 18 ? 2 : each <= 44 ? 4 : 6;
+    const auto units = [&](int64_t columns) {
+        const int64_t most = slots < experts ? slots : experts + slots / columns;
+        return most < slots ? most : slots;
+    };
+    const size_t scratch = g.few ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
+    const auto at = [&](int64_t bytes) { return (size_t)bytes > scratch ? (size_t)bytes : scratch; };
+    const auto grid = [&](int64_t groups) { return (unsigned)(groups < 2 * cus ? groups : 2 * cus); };
     if (g.up_tiles) {
-        const int64_t items = units * up_groups;
-        g.up = (unsigned)(items < 2 * cus ? items : 2 * cus);
+        g.up = grid(units(16 * g.mt) * up_groups);
+        g.up_at = at(2 * 16 * g.mt * kChunkBytes);
     } else {
-        const int64_t items = units * blocks, steps = a.e.hidden / 128;
+        const int64_t items = units(16) * blocks, steps = a.e.hidden / 128;
         g.kw = 8;
-        while (g.kw > 1 && (items * g.kw > 8 * cus || g.kw > steps || g.kw * g.mt > 16)) g.kw /= 2;
-        const int64_t groups = (items * g.kw + 7) / 8;
-        g.up = (unsigned)(groups < 2 * cus ? groups : 2 * cus);
-        g.up_lds = plan + (g.kw > 1 ? (size_t)8 * 4 * g.mt * 1024 : 0);
+        while (g.kw > 1 && (items * g.kw > 8 * cus || g.kw > steps)) g.kw /= 2;
+        g.up = grid((items * g.kw + 7) / 8);
+        g.up_at = at(g.kw > 1 ? 8 * 4 * 1024 : 0);
     }
-    if (g.down_tiles) {
+    if (g.few) {
+        g.down = (unsigned)(a.e.hidden / 16);
+        g.rows = (int)(16 * slots);
+        g.down_at = (size_t)g.rows * 64 + (size_t)slots * 4;
+    } else {
         const int64_t chunks_k = (a.e.inter + 511) / 512;
         g.ks = 1;
         while (2 * g.ks * met * down_groups <= 2 * cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k) g.ks *= 2;
-        const int64_t items = units * down_groups * g.ks;
-        g.down = (unsigned)(items < 2 * cus ? items : 2 * cus);
+        g.down = grid(units(16 * g.mt) * down_groups * g.ks);
+        g.down_at = at(2 * 16 * g.mt * (kChunkBytes + 16));
         g.join = (unsigned)((a.tokens * (a.e.hidden / 4) + 255) / 256);
-    } else {
-        g.down = (unsigned)(a.e.hidden / 16);
-        // K parts of few slots: to 1024 rows
-        g.rows = (int)(slots >= 1024 ? slots : 16 * slots < 1024 ? 16 * slots : 1024);
-        g.down_lds = plan + (size_t)g.rows * 64 + (size_t)((slots + 3) / 4 * 16);
     }
     return g;
 }
@@ -954,45 +893,33 @@ hipError_t launch_one(void (*f)(A), unsigned x, unsigned y, int threads, size_t 
     return hipGetLastError();
 }
 
-// column tiles of the tile kernels' units by the slots that an expert has on average, some to spare
-int tile_columns(const MoeGrid& g, int experts) {
-    const int64_t each = g.slots / experts;
-    return each <= 18 ? 2 : each <= 44 ? 4 : 6;
-}
 template <int MT>
-hipError_t launch_up_tiles(const MoeGrid& g, const UpArgs& a, hipStream_t stream) {
-    return launch_one(up_tile_kernel<MT>, g.up, g.chunks, kTileThreads, sizeof(MoePlan) + 2 * 16 * MT * kChunkBytes, stream, a);
+hipError_t launch_up_tiles(const MoeGrid& g, const UpArgs& a, size_t bytes, hipStream_t stream) {
+    return launch_one(up_tile_kernel<MT, MT == 6 ? 2 : 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
 }
-template <int MT>
-hipError_t launch_down_tiles(const MoeGrid& g, const DownTileArgs& a, hipStream_t stream) {
-    return launch_one(down_tile_kernel<MT>, g.down, g.chunks, kTileThreads, sizeof(MoePlan) + 2 * 16 * MT * (kChunkBytes + 16),
-                      stream, a);
+hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
+    a.plan_at = (int)g.up_at;
+    if (g.few) return launch_one(up_kernel<true>, g.up, 1, kUpThreads, g.up_at, stream, a);
+    const size_t bytes = g.up_at + sizeof(MoePlan);
+    if (!g.up_tiles) return launch_one(up_kernel<false>, g.up, g.chunks, kUpThreads, bytes, stream, a);
+    switch (g.mt) {
+        case 2: return launch_up_tiles<2>(g, a, bytes, stream);
+        case 4: return launch_up_tiles<4>(g, a, bytes, stream);
+        default: return launch_up_tiles<6>(g, a, bytes, stream);
+    }
 }
 
-hipError_t launch_up(const MoeGrid& g, const UpArgs& a, hipStream_t stream) {
-    if (g.up_tiles) {
-        switch (tile_columns(g, a.m.experts)) {
-            case 2: return launch_up_tiles<2>(g, a, stream);
-            case 4: return launch_up_tiles<4>(g, a, stream);
-            default: return launch_up_tiles<6>(g, a, stream);
-        }
-    }
-    const auto f = g.wave ? up_kernel<1, 4, true> : g.mt == 1 ? up_kernel<1, 4, false> : g.mt == 2 ? up_kernel<2, 2, false> : up_kernel<4, 2, false>;
-    return launch_one(f, g.up, g.chunks, kUpThreads, g.up_lds, stream, a);
+template <int MT>
+hipError_t launch_down_tiles(const MoeGrid& g, const DownTileArgs& a, hipStream_t stream) {
+    return launch_one(down_tile_kernel<MT, 4>, g.down, g.chunks, kTileThreads, g.down_at + sizeof(MoePlan), stream, a);
 }
 hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStream_t stream) {
-    if (g.down_tiles) {
-        const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks};
-        hipError_t e;
-        switch (tile_columns(g, a.m.experts)) {
-            case 2: e = launch_down_tiles<2>(g, d, stream); break;
-            case 4: e = launch_down_tiles<4>(g, d, stream); break;
-            default: e = launch_down_tiles<6>(g, d, stream);
-        }
-        return e != hipSuccess ? e : launch_one(join_kernel, g.join, 1, 256, 0, stream, d);
-    }
-    const auto f = g.wave ? down_kernel<1, 6, true> : g.mt == 1 ? down_kernel<1, 6, false> : g.mt == 2 ? down_kernel<2, 3, false> : down_kernel<4, 2, false>;
-    return launch_one(f, g.down, g.chunks, kDownThreads, g.down_lds, stream, a);
+    if (g.few) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
+    const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, (int)g.down_at};
+    const hipError_t e = g.mt == 2   ? launch_down_tiles<2>(g, d, stream)
+                         : g.mt == 4 ? launch_down_tiles<4>(g, d, stream)
+                                     : launch_down_tiles<6>(g, d, stream);
+    return e != hipSuccess ? e : launch_one(join_kernel, g.join, 1, 256, 0, stream, d);
 }
 
 }  // namespace
@@ -1019,9 +946,9 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
     m.e_stride = exponent_stride(a.e.inter);
     const int64_t slots = a.tokens * a.top_k;
     m.v = a.ws, m.ve = a.ws + slots * a.e.inter;
-    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw}, stream);
+    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, 0}, stream);
     if (e != hipSuccess) return e;
-    return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows, g.slots},
+    return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows},
                        reinterpret_cast<float*>(m.ve + slots * m.e_stride), stream);
 }
 
