@@ -62,13 +62,24 @@ __device__ __forceinline__ int unit_first(uint32_t u) { return u & 2047; }
 __device__ __forceinline__ int unit_slots(uint32_t u) { return ((u >> 11) & 127) + 1; }
 __device__ __forceinline__ int unit_expert(uint32_t u) { return u >> 18; }
 
+// lanes with the same id, which is in [0, experts) or -1: compared bit by bit over the wave
+__device__ __forceinline__ uint64_t equal_lanes(int id, int experts) {
+    const int bits = 32 - __builtin_clz(experts);   // 2^bits > experts: -1 is no other's low bits
+    uint64_t same = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t on = __ballot((id >> b) & 1);
+        same &= (id >> b) & 1 ? on : ~on;
+    }
+    return same;
+}
+
 // LDS that make_plan works in: how many slots of each 64 each expert has, and their first places
 size_t plan_scratch(int64_t slots, int64_t experts) { return (size_t)(((slots + 63) / 64 + 2) * ((experts + 3) / 4 * 4)); }
 
 // All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 128).  Slots keep their
 // order within an expert, so that all workgroups agree on the units: each wave ranks 64 slots
-// by the equal ids before them (ids compared bit by bit over the wave), and the counts of the
-// 64s are summed up for each expert.  No atomics.
+// by the equal ids before them, and the counts of the 64s are summed up for each expert.  No
+// atomics.
 template <int NT, int US>
 __device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int slots, int experts) {
     constexpr int kPer = kMoeSlots / NT, kExp = kMaxExperts / NT;
@@ -85,16 +96,11 @@ __device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int 
     }
     for (int i = tid; i < lots * e4 / 4; i += NT) reinterpret_cast<uint32_t*>(count)[i] = 0;
     __syncthreads();
-    const int bits = 32 - __builtin_clz(experts);   // of ids, with a bit that only -1 has
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int lot = wave + i * (NT / 64);
         if (lot >= lots) break;   // the same for the wave
-        uint64_t same = ~0ull;
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t on = __ballot((id[i] >> b) & 1);
-            same &= (id[i] >> b) & 1 ? on : ~on;
-        }
+        const uint64_t same = equal_lanes(id[i], experts);
         rank[i] = __popcll(same & ((1ull << lane) - 1));
         if (id[i] >= 0 && rank[i] == 0) count[lot * e4 + id[i]] = (uint8_t)__popcll(same);
     }
@@ -147,8 +153,7 @@ __device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int 
 constexpr int kWaveSlots = 64;
 struct WaveList {
     int id;              // the slot's expert, -1 if it has none
-    uint64_t same;       // slots of the same expert
-    int rank;            // how many of these come before it
+    int rank;            // how many slots of the same expert come before it
     uint64_t starts;     // slots that begin a unit of 16
     __device__ __forceinline__ int units() const { return __popcll(starts); }
 };
@@ -158,13 +163,7 @@ __device__ __forceinline__ WaveList wave_list(const int32_t* ids, int slots, int
     WaveList r;
     r.id = lane < slots ? ids[lane] : -1;
     if ((uint32_t)r.id >= (uint32_t)experts) r.id = -1;
-    r.same = 0;
-    for (int s = 0; s < slots; ++s) {
-        const int e = __builtin_amdgcn_readlane(r.id, s);
-        const uint64_t m = __ballot(r.id == e);
-        if (lane == s) r.same = m;
-    }
-    r.rank = __popcll(r.same & before);
+    r.rank = __popcll(equal_lanes(r.id, experts) & before);
     r.starts = __ballot(r.id >= 0 && (r.rank & 15) == 0);
     return r;
 }
@@ -510,15 +509,23 @@ __device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw, uint
 // a read meet all banks
 __device__ __forceinline__ int piece(int column, int c) { return column * kChunkBytes + 16 * (c ^ (column & 15)); }
 
+// Loads through a buffer resource: a scalar base and offset beside one vector offset, and zeros for
+// offsets past its end.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kNowhere = 0x7FFFFFFF;   // past every resource's end
+constexpr int kOnce = 2;                    // the non-temporal hint (load_stream16)
+
 template <int MT>
 struct Stage {                 // what a thread brings of a chunk: piece tid % 32 of the columns tid / 32 + 16 i
     u32x4 r[MT];
-    __device__ __forceinline__ void load(const uint8_t* x, const uint32_t (&row)[MT], int chunk, int64_t width, int cols) {
-        const int c = threadIdx.x & 31, col = threadIdx.x >> 5;
-        const uint32_t at = (uint32_t)chunk * kChunkBytes + 16 * c;
+    // row: the columns' offsets from x, kNowhere past the last; width of a row in bytes
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, const uint32_t (&row)[MT], int chunk, int width) {
+        const int c = 16 * (threadIdx.x & 31), at = chunk * kChunkBytes;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            if (16 * i + col < cols) r[i] = at < width ? *reinterpret_cast<const u32x4*>(x + row[i] + at) : u32x4{0u, 0u, 0u, 0u};
+            r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, at + c < width ? row[i] + c : kNowhere, at, 0));
     }
     __device__ __forceinline__ void store(uint8_t* to, int cols) const {
         const int c = threadIdx.x & 31, col = threadIdx.x >> 5;
@@ -576,23 +583,23 @@ __device__ __forceinline__ void hold(v4f (&acc)[Q][MT]) {
 // R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk
 template <int R, int D>
 struct Tiles {
-    const uint8_t* w[R];
-    const uint32_t* s[R];
+    __amdgpu_buffer_rsrc_t w[R], s[R];
     uint4 q[D][R];
     uint32_t sc[R], next[R];
     __device__ __forceinline__ void at(int r, const uint8_t* wt, const uint8_t* st, int64_t tile, int c_pad) {
-        w[r] = wt + tile * c_pad * 4096;
-        s[r] = reinterpret_cast<const uint32_t*>(st) + tile * c_pad * 64;
+        w[r] = resource(wt + tile * c_pad * 4096, c_pad * 4096);
+        s[r] = resource(st + tile * c_pad * 256, c_pad * 256);
     }
     __device__ __forceinline__ void load(int step, int to) {   // to: step % D
         const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int r = 0; r < R; ++r) q[to][r] = load_stream16(reinterpret_cast<const uint4*>(w[r] + step * 1024) + lane);
+        for (int r = 0; r < R; ++r)
+            q[to][r] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w[r], 16 * lane, step * 1024, kOnce));
     }
     __device__ __forceinline__ void load_scales(int chunk) {
         const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int r = 0; r < R; ++r) next[r] = (s[r] + chunk * 64)[lane];
+        for (int r = 0; r < R; ++r) next[r] = __builtin_amdgcn_raw_buffer_load_b32(s[r], 4 * lane, chunk * 256, 0);
     }
     __device__ __forceinline__ void last_scales() {
 #pragma unroll
@@ -605,7 +612,7 @@ struct Tiles {
 };
 
 template <int MT, int D>
-__global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
+__global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int kBuf = 16 * MT * kChunkBytes;
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
@@ -614,12 +621,12 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
     make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
-    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, col = threadIdx.x >> 5;
     const ColumnReader cr;
     const int blocks = (int)(m.inter / 32), groups = (blocks + 7) / 8, items = p.units * groups;
     const int steps = m.h_steps, chunks = (steps + 3) / 4;
     const int64_t tiles_i = m.inter / 16;
-    const uint8_t* x = a.x8 + t0 * m.hidden;
+    const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const uint32_t u = uniform(p.unit[item / groups]);
         const int first = unit_first(u), cols = unit_slots(u), blk = item % groups * 8 + wave;
@@ -627,9 +634,16 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
         uint32_t row[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            row[i] = (uint32_t)(p.list[first + min(16 * i + (int)(threadIdx.x >> 5), cols - 1)] / m.top_k) * (uint32_t)m.hidden;
+            row[i] = 16 * i + col < cols ? (uint32_t)(p.list[first + 16 * i + col] / m.top_k) * (uint32_t)m.hidden : kNowhere;
         Stage<MT> st;
-        st.load(x, row, 0, m.hidden, cols);
+        st.load(x, row, 0, (int)m.hidden);
+        int slot[MT];
+        float sx[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            slot[j] = p.list[first + min(16 * j + n, cols - 1)];
+            sx[j] = a.xs[t0 + slot[j] / m.top_k];
+        }
         Tiles<4, D> w;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -655,7 +669,7 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
             }
         };
         for (int c = 0; c + 1 < chunks; ++c) {
-            st.load(x, row, c + 1, m.hidden, cols);
+            st.load(x, row, c + 1, (int)m.hidden);
             w.next_scales(c + 1);
             four_steps([&](auto step) {
                 constexpr int s = decltype(step)::value;
@@ -681,9 +695,8 @@ __global__ __launch_bounds__(kTileThreads) void up_tile_kernel(UpArgs a) {
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 if (16 * j >= cols) continue;
-                const int slot = p.list[first + min(16 * j + n, cols - 1)];
                 const v4f r[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
-                store_v(m, r, a.xs[t0 + slot / m.top_k], a.act, t0 * m.top_k + slot, blk, g, 16 * j + n < cols);
+                store_v(m, r, sx[j], a.act, t0 * m.top_k + slot[j], blk, g, 16 * j + n < cols);
             }
         }
     }
@@ -701,11 +714,12 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kerne
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
     make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
-    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, col = threadIdx.x >> 5;
     const ColumnReader cr;
     const int tiles = (int)(m.hidden / 16), groups = (tiles + 15) / 16, items = p.units * groups * a.ks;
     const int steps = m.i_steps, chunks = (steps + 3) / 4;
-    const uint8_t *x = m.v + t0 * m.top_k * m.inter, *xe = m.ve + t0 * m.top_k * m.e_stride;
+    const __amdgpu_buffer_rsrc_t x = resource(m.v + t0 * m.top_k * m.inter, (uint32_t)(slots * m.inter));
+    const uint8_t* xe = m.ve + t0 * m.top_k * m.e_stride;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int k = item % a.ks, grp = item / a.ks % groups;
         const uint32_t u = uniform(p.unit[item / a.ks / groups]);
@@ -715,12 +729,12 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kerne
         uint32_t row[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            row[i] = (uint32_t)p.list[first + min(16 * i + (int)(threadIdx.x >> 5), cols - 1)] * (uint32_t)m.inter;
+            row[i] = 16 * i + col < cols ? (uint32_t)p.list[first + 16 * i + col] * (uint32_t)m.inter : kNowhere;
         const bool has_e = (int)threadIdx.x < cols;
         const uint8_t* ep = xe + (uint32_t)p.list[first + min((int)threadIdx.x, cols - 1)] * (uint32_t)m.e_stride;
         Stage<MT> st;
         u32x4 er{};
-        st.load(x, row, c0, m.inter, cols);
+        st.load(x, row, c0, (int)m.inter);
         if (has_e) er = exponents(ep, c0, steps);
         Tiles<2, D> w;
 #pragma unroll
@@ -756,7 +770,7 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kerne
         };
         for (int c = c0; c + 1 < c1; ++c) {
             const uint8_t* buf = lds + ((c - c0) & 1) * kBuf;
-            st.load(x, row, c + 1, m.inter, cols);
+            st.load(x, row, c + 1, (int)m.inter);
             if (has_e) er = exponents(ep, c + 1, steps);
             w.next_scales(c + 1);
             read_e(buf);
@@ -803,18 +817,25 @@ __global__ __launch_bounds__(256) void join_kernel(DownTileArgs a) {
     const int64_t quads = m.hidden / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= m.tokens * quads) return;
     const int64_t t = i / quads, col = 4 * (i - t * quads);
+    // eight slots' loads at a time; of a slot without an expert the sums hold anything
     v4f sum = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < m.top_k; ++j) {
-        const int64_t s = t * m.top_k + j;
-        if ((uint32_t)a.ids[s] >= (uint32_t)m.experts) continue;
-        v4f v = v4f{0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < a.ks; ++k) {
-            const float4 f = *reinterpret_cast<const float4*>(a.sums + ((int64_t)k * m.tokens * m.top_k + s) * m.hidden + col);
-            v += v4f{f.x, f.y, f.z, f.w};
-        }
-        const float w = a.weights[s];
+    for (int j0 = 0; j0 < m.top_k; j0 += 8) {
+        float w[8];
+        v4f v[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(w, v[c], sum[c]);
+        for (int j = 0; j < 8; ++j) {
+            const int64_t s = t * m.top_k + min(j0 + j, m.top_k - 1);
+            const bool on = j0 + j < m.top_k && (uint32_t)a.ids[s] < (uint32_t)m.experts;
+            w[j] = on ? a.weights[s] : 0.0f;
+            v[j] = *reinterpret_cast<const v4f*>(a.sums + s * m.hidden + col);
+            for (int k = 1; k < a.ks; ++k)
+                v[j] += *reinterpret_cast<const v4f*>(a.sums + ((int64_t)k * m.tokens * m.top_k + s) * m.hidden + col);
+            if (!on) v[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(w[j], v[j][c], sum[c]);
     }
     *reinterpret_cast<uint2*>(a.out + t * m.hidden + col) = make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
 }
@@ -895,7 +916,7 @@ hipError_t launch_one(void (*f)(A), unsigned x, unsigned y, int threads, size_t 
 
 template <int MT>
 hipError_t launch_up_tiles(const MoeGrid& g, const UpArgs& a, size_t bytes, hipStream_t stream) {
-    return launch_one(up_tile_kernel<MT, MT == 6 ? 2 : 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+    return launch_one(up_tile_kernel<MT, MT == 4 ? 4 : 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
 }
 hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
     a.plan_at = (int)g.up_at;
