@@ -192,9 +192,18 @@ __device__ __forceinline__ Unit plan_unit(const MoePlan& p, int u) {
     return {unit_expert(v), cols, p.list[unit_first(v) + min((int)(threadIdx.x & 15), cols - 1)]};
 }
 
+// n / d for n d < 2^32, by a product
+struct Divisor {
+    uint32_t d, m;
+    Divisor() = default;
+    explicit Divisor(int64_t by) : d((uint32_t)by), m(by > 1 ? (uint32_t)((1ull << 32) / (uint64_t)by + 1) : 0) {}
+    __device__ __forceinline__ int quotient(int n) const { return d == 1 ? n : (int)__umulhi((uint32_t)n, m); }
+    __device__ __forceinline__ int rest(int n, int q) const { return n - q * (int)d; }
+};
 struct MoeShape {
     int64_t tokens, hidden, inter;
     int experts, top_k, chunk;          // tokens of a chunk
+    Divisor by_top_k;                   // a slot's token
     int h_steps, i_steps;               // 128-wide steps of hidden and inter
     int64_t e_stride;                   // exponent bytes of a slot of v: 16 per 4 steps, [step / 4][k / 32 % 4][step % 4]
     uint8_t *v, *ve;                    // v's codes [slots][inter] and exponents
@@ -205,6 +214,7 @@ struct UpArgs {
     const float* xs;
     const int32_t* ids;
     int act, kw;
+    Divisor by_blocks, by_kw;           // items of a unit; K parts
     int plan_at;                        // of the plan in LDS; before it the kernel's own, and the plan's making
 };
 struct DownArgs {
@@ -223,16 +233,19 @@ struct DownTileArgs {
     uint16_t* out;
     float* sums;
     int ks;                             // K parts
+    Divisor by_items;                   // items of a unit: K parts x groups of columns, the parts first
     int plan_at;
 };
 
 // ---------------------------------------------------------------------------
 // up
 // ---------------------------------------------------------------------------
+// exp and 1 / x by the hardware's instructions, each within a unit in the last place: g to 2^6 comes out
+// within 2^-17, and v is rounded to four bits
 __device__ __forceinline__ float activated(float g, int act) {
-    if (act == W4A8_ACT_SILU) return g / (1.0f + expf(-g));
-    const float t = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-    return g / (1.0f + expf(-2.0f * t));   // (1 + tanh t) / 2
+    float z = g;
+    if (act != W4A8_ACT_SILU) z = 1.5957691216057308f * (g + 0.044715f * g * g * g);   // (1 + tanh(z / 2)) / 2
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
 // One step's products of a 16-row tile with 16 columns, for the first product of few tokens.
@@ -255,16 +268,11 @@ struct Columns {
             x[i] = __builtin_bit_cast(v8bf, r);
         }
     }
-    __device__ __forceinline__ v4f times(uint4 w, uint32_t scale, v4f c) const {
-        // the conversion reads the scale's exponent field alone: 2^(byte - 127), for 0 too
-        const float s = __uint_as_float((scale & 0xFFu) << 23);
-        const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const u32x4 r = {fp4<0>(d[i], s), fp4<1>(d[i], s), fp4<2>(d[i], s), fp4<3>(d[i], s)};
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, r), x[i], c, 0, 0, 0);
-        }
-        return c;
+    // eight of a lane's k with a tile's codes of them; of the scale the conversion reads the exponent
+    // field alone: 2^(byte - 127), for byte 0 too
+    __device__ __forceinline__ v4f times(int i, uint32_t codes, float scale, v4f c) const {
+        const u32x4 r = {fp4<0>(codes, scale), fp4<1>(codes, scale), fp4<2>(codes, scale), fp4<3>(codes, scale)};
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, r), x[i], c, 0, 0, 0);
     }
     template <bool HIGH>
     static __device__ __forceinline__ uint32_t pair(uint32_t codes) {
@@ -276,8 +284,16 @@ struct Columns {
     }
 };
 
+// Loads through a buffer resource: a scalar base and offset beside one vector offset, and zeros for
+// offsets past its end.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kNowhere = 0x7FFFFFFF;   // past every resource's end
+constexpr int kOnce = 2;                    // the non-temporal hint (load_stream16)
+
 struct UpStep {
-    uint4 w[4];            // gate rows i0 .. +15 and +16 .. +31, then the up rows
+    u32x4 w[4];            // gate rows i0 .. +15 and +16 .. +31, then the up rows
     uint32_t s[4];
     u32x4 x[2];
 };
@@ -311,13 +327,14 @@ __device__ __forceinline__ void store_v(const MoeShape& m, const v4f (&r)[4], fl
         m.ve[row * m.e_stride + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] = finite ? (uint8_t)(e + 127) : 255;
 }
 
-// WAVE: up to 64 slots, listed by every wave; else listed in LDS.  Four steps in flight.
+// WAVE: up to 64 slots, listed by every wave; else listed in LDS.  Two steps in flight, two workgroups
+// to a CU.
 template <bool WAVE>
-__global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
-    constexpr int D = 4;
+__global__ __launch_bounds__(kUpThreads, 4) void up_kernel(UpArgs a) {
+    constexpr int D = 2;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
-    float4* join = reinterpret_cast<float4*>(lds);   // [wave][tile][lane]
+    v4f* join = reinterpret_cast<v4f*>(lds);   // [wave][tile][lane]
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
@@ -328,72 +345,77 @@ __global__ __launch_bounds__(kUpThreads) void up_kernel(UpArgs a) {
         make_plan<kUpThreads, 16>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-    const int kw = a.kw, part = wave % kw, per_wg = 8 / kw;
+    const int kw = a.kw, mine = a.by_kw.quotient(wave), part = wave - mine * kw, per_wg = 8 / kw;   // kw: 1, 2, 4 or 8
     const int blocks = (int)(m.inter / 32), items = (WAVE ? list.units() : p.units) * blocks;
     const int c_pad = (m.h_steps + 3) / 4;
     const int64_t tiles_i = m.inter / 16;
     const int s0 = m.h_steps * part / kw, s1 = m.h_steps * (part + 1) / kw;
-    const uint8_t* x = a.x8 + t0 * m.hidden;
+    const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
     for (int base = blockIdx.x * per_wg; base < items; base += gridDim.x * per_wg) {   // the same in all waves
-        const int item = base + wave / kw;
-        const bool live = item < items;
-        const int blk = live ? item % blocks : 0;
-        const Unit u = WAVE ? wave_unit(list, live ? item / blocks : 0) : plan_unit(p, live ? item / blocks : 0);
-        const int t = u.slot / m.top_k;
+        const bool live = base + mine < items;
+        const int item = live ? base + mine : 0, of = a.by_blocks.quotient(item), blk = a.by_blocks.rest(item, of);
+        const Unit u = WAVE ? wave_unit(list, of) : plan_unit(p, of);
+        const int t = m.by_top_k.quotient(u.slot);
         const uint32_t xo = (uint32_t)t * (uint32_t)m.hidden + 32 * g;
         const float sx = a.xs[t0 + t];
-        const uint8_t* wp[4];
-        const uint32_t* sp[4];
+        __amdgpu_buffer_rsrc_t wr[4], sr[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int64_t tile = (2 * u.expert + (q >> 1)) * tiles_i + 2 * blk + (q & 1);
-            wp[q] = a.w + tile * c_pad * 4096;
-            sp[q] = reinterpret_cast<const uint32_t*>(a.s) + tile * c_pad * 64;
+            wr[q] = resource(a.w + tile * c_pad * 4096, c_pad * 4096);
+            sr[q] = resource(a.s + tile * c_pad * 256, c_pad * 256);
         }
         v4f acc[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[q] = v4f{0.f, 0.f, 0.f, 0.f};
         const auto load = [&](int s, UpStep& r) {
+            r.x[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, xo, 128 * s, 0));
+            r.x[1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, xo + 16, 128 * s, 0));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                r.w[q] = load_stream16(reinterpret_cast<const uint4*>(wp[q] + s * 1024) + lane);
-                r.s[q] = (sp[q] + (s >> 2) * 64)[lane];
+                r.s[q] = __builtin_amdgcn_raw_buffer_load_b32(sr[q], 4 * lane, (s >> 2) * 256, 0);
+                r.w[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr[q], 16 * lane, s * 1024, kOnce));
             }
-            r.x[0] = *reinterpret_cast<const u32x4*>(x + 128 * s + xo);
-            r.x[1] = *reinterpret_cast<const u32x4*>(x + 128 * s + 16 + xo);
         };
         const auto compute = [&](int s, const UpStep& r) {
             Columns c;
             c.set(r.x[0], r.x[1]);
+            float scale[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] = c.times(r.w[q], r.s[q] >> (8 * (s & 3)), acc[q]);
+            for (int q = 0; q < 4; ++q) scale[q] = __uint_as_float(((r.s[q] >> (8 * (s & 3))) & 0xFFu) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[q] = c.times(i, r.w[q][i], scale[q], acc[q]);
         };
         if (live) {
             UpStep ring[D];
 #pragma unroll
-            for (int d = 0; d < D - 1; ++d)
+            for (int d = 0; d < D; ++d)
                 if (s0 + d < s1) load(s0 + d, ring[d]);
             for (int s = s0; s < s1; s += D) {
 #pragma unroll
                 for (int d = 0; d < D; ++d) {
-                    if (s + d + D - 1 < s1) load(s + d + D - 1, ring[(d + D - 1) % D]);
                     if (s + d < s1) compute(s + d, ring[d]);
+                    if (s + d + D < s1) load(s + d + D, ring[d]);
                 }
             }
         }
         if (kw > 1) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) join[(wave * 4 + q) * 64 + lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+            for (int q = 0; q < 4; ++q) join[(wave * 4 + q) * 64 + lane] = acc[q];
             __syncthreads();
         }
         if (live && part == 0) {
-            if (kw > 1) {   // the parts in order
+            if (kw > 1) {   // the parts in order, seven reads at a time
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    for (int k = 1; k < kw; ++k) {
-                        const float4 f = join[((wave + k) * 4 + q) * 64 + lane];
-                        acc[q] += v4f{f.x, f.y, f.z, f.w};
-                    }
+                    v4f f[7];
+#pragma unroll
+                    for (int k = 1; k < 8; ++k) f[k - 1] = join[((wave + min(k, kw - 1)) * 4 + q) * 64 + lane];
+#pragma unroll
+                    for (int k = 1; k < 8; ++k)
+                        if (k < kw) acc[q] += f[k - 1];
                 }
             }
             store_v(m, acc, sx, a.act, t0 * m.top_k + u.slot, blk, g, n < u.cols);
@@ -420,6 +442,7 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
     const int tokens = (int)m.tokens, slots = tokens * m.top_k;
     // LDS: partial sums [slot][K part][16 columns], the slots' weights
     float4* part = reinterpret_cast<float4*>(lds);
+    const float* lds_sums = reinterpret_cast<const float*>(lds);
     float* share = reinterpret_cast<float*>(lds + (size_t)a.rows * 64);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const WaveList list = wave_list(a.ids, slots, m.experts);
@@ -466,21 +489,24 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
         if (n < u.cols) part[(u.slot * ks + k) * 4 + g] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
     __syncthreads();
-    // four columns of a token to a thread: its slots in order
-    if ((int)threadIdx.x < 4 * tokens) {
-        const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
-        v4f sum = v4f{0.f, 0.f, 0.f, 0.f};
-        for (int s = t * m.top_k; s < (t + 1) * m.top_k; ++s) {
-            v4f v = v4f{0.f, 0.f, 0.f, 0.f};
-            for (int k = 0; k < ks; ++k) {
-                const float4 f = part[(s * ks + k) * 4 + q];
-                v += v4f{f.x, f.y, f.z, f.w};
-            }
+    // a column of a token to a thread: its slots in order, eight reads at a time
+    if ((int)threadIdx.x < 16 * tokens) {
+        const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
+        const float* sums = lds_sums + c;
+        float sum = 0.0f;
+        for (int j0 = 0; j0 < m.top_k; j0 += 8) {
+            float v[8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(share[s], v[c], sum[c]);
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            for (int k = 0; k < ks; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] += sums[16 * ((t * m.top_k + min(j0 + j, m.top_k - 1)) * ks + k)];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j0 + j < m.top_k) sum = __builtin_fmaf(share[t * m.top_k + j0 + j], v[j], sum);
         }
-        *reinterpret_cast<uint2*>(a.out + (int64_t)t * m.hidden + 16 * blockIdx.x + 4 * q) =
-            make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
+        a.out[(int64_t)t * m.hidden + 16 * blockIdx.x + c] = (uint16_t)pack_bf16(sum, 0.0f);
     }
 }
 
@@ -508,14 +534,6 @@ __device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw, uint
 // 16-byte pieces of a column's 512, swapped within 256 by the column, so that the 16 columns of
 // a read meet all banks
 __device__ __forceinline__ int piece(int column, int c) { return column * kChunkBytes + 16 * (c ^ (column & 15)); }
-
-// Loads through a buffer resource: a scalar base and offset beside one vector offset, and zeros for
-// offsets past its end.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
-constexpr uint32_t kNowhere = 0x7FFFFFFF;   // past every resource's end
-constexpr int kOnce = 2;                    // the non-temporal hint (load_stream16)
 
 template <int MT>
 struct Stage {                 // what a thread brings of a chunk: piece tid % 32 of the columns tid / 32 + 16 i
@@ -628,13 +646,14 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(
     const int64_t tiles_i = m.inter / 16;
     const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const uint32_t u = uniform(p.unit[item / groups]);
-        const int first = unit_first(u), cols = unit_slots(u), blk = item % groups * 8 + wave;
+        const int of = a.by_blocks.quotient(item);
+        const uint32_t u = uniform(p.unit[of]);
+        const int first = unit_first(u), cols = unit_slots(u), blk = a.by_blocks.rest(item, of) * 8 + wave;
         const bool live = blk < blocks;   // a wave past the last block computes that one again
         uint32_t row[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            row[i] = 16 * i + col < cols ? (uint32_t)(p.list[first + 16 * i + col] / m.top_k) * (uint32_t)m.hidden : kNowhere;
+            row[i] = 16 * i + col < cols ? (uint32_t)m.by_top_k.quotient(p.list[first + 16 * i + col]) * (uint32_t)m.hidden : kNowhere;
         Stage<MT> st;
         st.load(x, row, 0, (int)m.hidden);
         int slot[MT];
@@ -642,7 +661,7 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             slot[j] = p.list[first + min(16 * j + n, cols - 1)];
-            sx[j] = a.xs[t0 + slot[j] / m.top_k];
+            sx[j] = a.xs[t0 + m.by_top_k.quotient(slot[j])];
         }
         Tiles<4, D> w;
 #pragma unroll
@@ -721,8 +740,9 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kerne
     const __amdgpu_buffer_rsrc_t x = resource(m.v + t0 * m.top_k * m.inter, (uint32_t)(slots * m.inter));
     const uint8_t* xe = m.ve + t0 * m.top_k * m.e_stride;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int k = item % a.ks, grp = item / a.ks % groups;
-        const uint32_t u = uniform(p.unit[item / a.ks / groups]);
+        const int of = a.by_items.quotient(item), rest = a.by_items.rest(item, of);
+        const int k = rest & (a.ks - 1), grp = rest >> (31 - __builtin_clz(a.ks));   // ks: a power of two
+        const uint32_t u = uniform(p.unit[of]);
         const int first = unit_first(u), cols = unit_slots(u), tile = grp * 16 + 2 * wave;
         const bool live = tile < tiles;   // tiles are even; a wave past the last pair computes that one again
         const int c0 = chunks * k / a.ks, c1 = chunks * (k + 1) / a.ks;
@@ -822,20 +842,26 @@ __global__ __launch_bounds__(256) void join_kernel(DownTileArgs a) {
     for (int j0 = 0; j0 < m.top_k; j0 += 8) {
         float w[8];
         v4f v[8];
+        bool on[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t s = t * m.top_k + min(j0 + j, m.top_k - 1);
-            const bool on = j0 + j < m.top_k && (uint32_t)a.ids[s] < (uint32_t)m.experts;
-            w[j] = on ? a.weights[s] : 0.0f;
+            on[j] = j0 + j < m.top_k && (uint32_t)a.ids[s] < (uint32_t)m.experts;
+            w[j] = a.weights[s];
             v[j] = *reinterpret_cast<const v4f*>(a.sums + s * m.hidden + col);
-            for (int k = 1; k < a.ks; ++k)
-                v[j] += *reinterpret_cast<const v4f*>(a.sums + ((int64_t)k * m.tokens * m.top_k + s) * m.hidden + col);
-            if (!on) v[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+        for (int k = 1; k < a.ks; ++k) {
+            v4f more[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                more[j] = *reinterpret_cast<const v4f*>(a.sums + ((int64_t)k * m.tokens * m.top_k + t * m.top_k + min(j0 + j, m.top_k - 1)) * m.hidden + col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += more[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(w[j], v[j][c], sum[c]);
+            for (int c = 0; c < 4; ++c) sum[c] = on[j] ? __builtin_fmaf(w[j], v[j][c], sum[c]) : sum[c];
     }
     *reinterpret_cast<uint2*>(a.out + t * m.hidden + col) = make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
 }
@@ -882,9 +908,13 @@ MoeGrid moe_grid(const MoeArgs& a) {
         g.up_at = at(2 * 16 * g.mt * kChunkBytes);
     } else {
         const int64_t items = units(16) * blocks, steps = a.e.hidden / 128;
-        g.kw = 8;
-        while (g.kw > 1 && (items * g.kw > 8 * cus || g.kw > steps)) g.kw /= 2;
-        g.up = grid((items * g.kw + 7) / 8);
+        // K parts while the workgroups are no more than the CUs, and so many that a wave has eight steps (one
+        // token of eight experts, hidden 2048: 14.7, 11.2, 7.7 and 5.9 us with 1, 2, 4 and 8; hidden 4096, four
+        // tokens of two large experts: 35 us with 1, 31 with 4, 37 with 8)
+        g.kw = 1;
+        while (2 * g.kw <= 8 && 2 * g.kw <= steps && (items * 2 * g.kw <= 8 * cus || 16 * g.kw <= steps)) g.kw *= 2;
+        const int64_t groups = (items * g.kw + 7) / 8;
+        g.up = (unsigned)(groups < 3 * cus ? groups : 3 * cus);
         g.up_at = at(g.kw > 1 ? 8 * 4 * 1024 : 0);
     }
     if (g.few) {
@@ -936,7 +966,7 @@ hipError_t launch_down_tiles(const MoeGrid& g, const DownTileArgs& a, hipStream_
 }
 hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStream_t stream) {
     if (g.few) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
-    const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, (int)g.down_at};
+    const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, Divisor((a.m.hidden / 16 + 15) / 16 * g.ks), (int)g.down_at};
     const hipError_t e = g.mt == 2   ? launch_down_tiles<2>(g, d, stream)
                          : g.mt == 4 ? launch_down_tiles<4>(g, d, stream)
                                      : launch_down_tiles<6>(g, d, stream);
@@ -962,12 +992,13 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
     const MoeGrid g = moe_grid(a);
     MoeShape m{};
     m.tokens = a.tokens, m.hidden = a.e.hidden, m.inter = a.e.inter;
+    m.by_top_k = Divisor(a.top_k);
     m.experts = a.e.experts, m.top_k = a.top_k, m.chunk = (int)moe_chunk_tokens(a.top_k);
     m.h_steps = (int)(a.e.hidden / 128), m.i_steps = (int)(a.e.inter / 128);
     m.e_stride = exponent_stride(a.e.inter);
     const int64_t slots = a.tokens * a.top_k;
     m.v = a.ws, m.ve = a.ws + slots * a.e.inter;
-    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, 0}, stream);
+    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(g.up_tiles ? (a.e.inter / 32 + 7) / 8 : a.e.inter / 32), Divisor(g.up_tiles ? 1 : g.kw), 0}, stream);
     if (e != hipSuccess) return e;
     return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows},
                        reinterpret_cast<float*>(m.ve + slots * m.e_stride), stream);
