@@ -27,7 +27,8 @@ def _check(logits, top_k, **kw):
 
 
 SHAPES = [(1, 1, 1), (1, 128, 8), (3, 2, 2), (5, 7, 3), (61, 60, 4), (17, 64, 32), (9, 65, 1), (33, 128, 8), (7, 200, 5),
-          (4, 256, 16), (11, 257, 8), (3, 512, 10), (2, 1000, 32), (5, 1024, 8), (1030, 8, 2), (130, 16, 16)]
+          (4, 256, 16), (11, 257, 8), (3, 512, 10), (2, 1000, 32), (5, 1024, 8), (1030, 8, 2), (130, 16, 16),
+          (1024, 1, 1), (2050, 60, 4), (1500, 16, 16), (1111, 256, 16), (1027, 200, 3), (1026, 32, 17), (1025, 128, 8)]
 
 
 @pytest.mark.parametrize("tokens,experts,top_k", SHAPES)
@@ -59,11 +60,11 @@ def test_groups(experts, groups, kept, top, top_k, score):
     _check(x, top_k, bias=0.2 * torch.randn(experts, generator=g).cuda(), **kw)
 
 
-@pytest.mark.parametrize("experts", [8, 100, 300])
-def test_masks_ties_and_what_is_no_number(experts):
-    say("moe_route masks", experts)
+@pytest.mark.parametrize("tokens,experts", [(16, 8), (16, 100), (16, 300), (1040, 8), (1040, 100)])
+def test_masks_ties_and_what_is_no_number(tokens, experts):
+    say("moe_route masks", tokens, experts)
     g = torch.Generator().manual_seed(experts)
-    x = torch.randn((16, experts), generator=g)
+    x = torch.randn((tokens, experts), generator=g)
     x[0] = float("-inf")
     x[1, 3:] = float("-inf")
     x[2] = float("nan")

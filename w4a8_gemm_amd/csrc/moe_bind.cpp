@@ -4,6 +4,10 @@
 // pointers, strides and the current stream, status codes as exceptions.  Every
 // function takes all of its arguments by position; the signatures, defaults and
 // documentation are in moe.py.
+#include <optional>
+
+#include <ATen/hip/EmptyTensor.h>
+
 #include "bind.h"
 
 namespace {
@@ -16,9 +20,13 @@ void matrix(const at::Tensor& t, const char* name, int64_t rows, int64_t cols) {
         refuse(PyExc_ValueError, "%s must be [%lld, %lld]", name, (long long)rows, (long long)cols);
     if (cols > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, "%s must have contiguous rows (unit last stride)", name);
 }
+// a new contiguous tensor, past the dispatcher
+at::Tensor fresh(at::Device dev, at::ScalarType type, at::IntArrayRef shape) {
+    return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
+}
 // the caller's contiguous output, or a new one
 at::Tensor target(PyObject* o, const char* name, const at::Tensor& like, at::ScalarType type, at::IntArrayRef shape) {
-    if (o == Py_None) return at::empty(shape, like.options().dtype(type));
+    if (o == Py_None) return fresh(like.device(), type, shape);
     const at::Tensor& t = tensor(o, name, type, like.device());
     if (t.sizes() != shape || !t.is_contiguous())
         refuse(PyExc_ValueError, "%s must be a contiguous tensor of the result's shape", name);
@@ -57,11 +65,12 @@ PyObject* residual_norm(PyObject* const* a, Py_ssize_t n) {
     const bool values = truth(a[7]), fp8 = truth(a[8]);
     if (!values && !fp8 && !r && a[9] == Py_None) refuse(PyExc_ValueError, "nothing to compute: values, fp8 or a residual");
     on_gpu(y, "y");
+    const c10::DeviceGuard guard(dev);
     at::Tensor ro, out, x8, xs;
     if (r || a[9] != Py_None) {
         const at::ScalarType rt = r ? r->scalar_type() : y.scalar_type();
         if (a[9] == Py_None) {
-            ro = at::empty({tokens, hidden}, y.options().dtype(rt));
+            ro = fresh(dev, rt, {tokens, hidden});
         } else {
             ro = tensor(a[9], "residual_out", rt, dev);
             matrix(ro, "residual_out", tokens, hidden);
@@ -74,7 +83,6 @@ PyObject* residual_norm(PyObject* const* a, Py_ssize_t n) {
         x8 = target(a[11], "x_fp8", y, at::kByte, at::IntArrayRef(shape, 2));
         xs = target(a[12], "x_scale", y, at::kFloat, at::IntArrayRef(shape, 1));
     }
-    const c10::DeviceGuard guard(dev);
     if (tokens)
         check(w4a8_residual_norm(type, static_cast<const uint16_t*>(y.const_data_ptr()), y.stride(0), tokens, hidden, pw,
                                  g ? static_cast<const uint16_t*>(g->const_data_ptr()) : nullptr, gs[0], gs[1], (float)scale,
@@ -113,10 +121,10 @@ PyObject* route(PyObject* const* a, Py_ssize_t n) {
     const bool renormalize = truth(a[7]);
     const double scale = number(a[8]);
     on_gpu(x, "logits");
+    const c10::DeviceGuard guard(dev);
     const int64_t shape[2] = {tokens, k};
     at::Tensor w = target(a[9], "weights", x, at::kFloat, at::IntArrayRef(shape, 2));
     at::Tensor ids = target(a[10], "ids", x, at::kInt, at::IntArrayRef(shape, 2));
-    const c10::DeviceGuard guard(dev);
     if (tokens)
         check(w4a8_moe_route(type, x.const_data_ptr(), x.stride(0), tokens, (int)experts, (int)k, score, bias, (int)groups,
                              (int)kept, (int)top, renormalize, (float)scale, static_cast<int32_t*>(ids.data_ptr()),
@@ -178,12 +186,12 @@ PyObject* moe(PyObject* const* a, Py_ssize_t n) {
     if (!ids.is_contiguous() || !w.is_contiguous()) refuse(PyExc_ValueError, "ids and weights must be contiguous");
     const w4a8_act act = (w4a8_act)integer(a[5], "act", 0, 1);
     on_gpu(x, "x_fp8");
+    const c10::DeviceGuard guard(e.dev);
     const int64_t shape[2] = {tokens, e.view.hidden};
     at::Tensor out = target(a[7], "out", x, at::kBFloat16, at::IntArrayRef(shape, 2));
     if (tokens == 0) return THPVariable_Wrap(out);
-    const c10::DeviceGuard guard(e.dev);
     const at::Tensor ws = a[6] != Py_None ? tensor(a[6], "workspace", at::kByte, e.dev)
-                                          : at::empty({(int64_t)w4a8_moe_workspace_bytes(tokens, (int)k, e.view.hidden, e.view.inter)}, x.options());
+                                          : fresh(e.dev, at::kByte, {(int64_t)w4a8_moe_workspace_bytes(tokens, (int)k, e.view.hidden, e.view.inter)});
     check(w4a8_moe_mxfp4(&e.view, static_cast<const uint8_t*>(x.const_data_ptr()), xs, tokens, ids.const_data_ptr<int32_t>(),
                          w.const_data_ptr<float>(), (int)k, act, static_cast<uint16_t*>(out.data_ptr()), ws.data_ptr(),
                          (size_t)ws.numel(), stream(e.dev)),

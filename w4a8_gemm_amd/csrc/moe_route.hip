@@ -11,7 +11,7 @@
 // exponentials in the same precision, rounded once to fp32.
 #include <type_traits>
 
-#include "w4a8_internal.h"
+#include "wave_ops.h"
 
 #pragma clang fp contract(off)
 
@@ -32,19 +32,11 @@ __device__ __forceinline__ uint64_t key_of(double v) {
     return b >> 63 ? ~b : b | (1ull << 63);
 }
 
-template <typename T, typename F>
-__device__ __forceinline__ T wave_reduce(T v, F f) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v = f(v, __shfl_xor(v, off));
-    return v;
-}
-template <typename T>
-__device__ __forceinline__ T wave_max(T v) {
-    return wave_reduce(v, [](T a, T b) { return a > b ? a : b; });
-}
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-    return wave_reduce(v, [](T a, T b) { return a + b; });
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) { return wave_reduce(v, Max()); }
+// the high halves first, then the low ones of the lanes that have the largest of these
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    const uint32_t hi = wave_max((uint32_t)(v >> 32));
+    return (uint64_t)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
 }
 
 __device__ __forceinline__ float exponential(float v) { return expf(v); }
@@ -81,7 +73,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
     }
     S total = 1;
     if (a.score == W4A8_SCORE_SOFTMAX) {
-        top = wave_max(top);
+        top = wave_reduce(top, Max());
         total = 0;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
@@ -90,7 +82,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
             p[i] = logit[i] > -inf ? exponential(d) : S(0);
             total += p[i];
         }
-        total = wave_sum(total);
+        total = wave_reduce(total, Add());
         if (!(total > 0)) total = 1;
     } else {
 #pragma unroll
@@ -99,7 +91,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         if constexpr (kByScore) {
-            p[i] = p[i] / total;
+            if (a.score == W4A8_SCORE_SOFTMAX) p[i] = p[i] / total;
             const int e = lane + 64 * i;
             const double by = a.bias && e < a.experts ? p[i] + (double)a.bias[e] : p[i];
             key[i] = logit[i] > -inf ? key_of(by) : 0;
@@ -117,6 +109,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
             uint64_t group = 0;
             if (lane < a.groups) {
                 double first = -__builtin_inf(), second = first;
+#pragma unroll 4
                 for (int i = 0; i < size; ++i) {
                     const double v = line[wave][lane * size + i];
                     second = fmax(second, fmin(first, v));
@@ -157,7 +150,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
             if (!have) continue;
             const int from = __builtin_ctzll(have);
             at = 64 * i + from;
-            w = __shfl(p[i], from);
+            w = lane_value(p[i], from);
             if (lane == from) key[i] = 0;
         }
         sum += w;
@@ -169,6 +162,90 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
         a.ids[token * a.top_k + lane] = id;
         a.weights[token * a.top_k + lane] = (float)(mine * S(a.scale));
     }
+}
+
+// Many tokens whose choice goes by the logits: four to a wave, 16 lanes each, lane L of them with the
+// experts L, L + 16, ...; a round's instructions serve four tokens (16384 tokens, 8 of 128 experts:
+// 8.6 us, a wave per token 11.8, both bound by their instructions).
+template <w4a8_float TYPE, int NL>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_rows_kernel(RouteArgs a) {
+    const int sub = threadIdx.x & 15;
+    const int64_t token = ((int64_t)blockIdx.x * (64 * kRouteWaves) + threadIdx.x) >> 4;
+    const int64_t at = token < a.tokens ? token : a.tokens - 1;   // lanes past the last compute it again
+    const void* row = static_cast<const uint8_t*>(a.logits) + at * a.ld * (TYPE == W4A8_FP32 ? 4 : 2);
+    const float inf = __builtin_inff();
+    float p[NL];
+    uint32_t key[NL];
+    float top = -inf;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int e = sub + 16 * i;
+        const float v = e < a.experts ? load_logit<TYPE>(row, e) : -inf;
+        p[i] = v == v ? v : -inf;
+        key[i] = key_of(p[i]);
+        top = fmaxf(top, p[i]);
+    }
+    float total = 1.0f;
+    if (a.score == W4A8_SCORE_SOFTMAX) {
+        top = row_reduce(top, Max());
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const float d = p[i] == top ? 0.0f : p[i] - top;
+            p[i] = p[i] > -inf ? expf(d) : 0.0f;
+            total += p[i];
+        }
+        total = row_reduce(total, Add());
+        if (!(total > 0.0f)) total = 1.0f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) p[i] = 1.0f / (1.0f + expf(-p[i]));
+    }
+    int id = -1;
+    float mine = 0.0f, sum = 0.0f;
+    for (int j = 0; j < a.top_k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) best = max(best, key[i]);
+        best = row_reduce(best, Max());
+        // ~expert, the largest: the lowest expert of those that hold it; 0 for none
+        uint32_t which = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) which = max(which, key[i] == best ? ~(uint32_t)(sub + 16 * i) : 0u);
+        which = row_reduce(which, Max());
+        float w = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            if (which == ~(uint32_t)(sub + 16 * i)) {
+                key[i] = 0;
+                w = p[i];
+            }
+        w = row_reduce(w, Add());   // of one lane, and zeros
+        if (best == 0) w = 0.0f;
+        sum += w;
+        if (sub == j && best) id = (int)~which, mine = w;
+    }
+    mine = mine / total, sum = sum / total;
+    if (a.renormalize) mine = sum > 0.0f ? mine / sum : 0.0f;
+    if (sub < a.top_k && token < a.tokens) {
+        a.ids[token * a.top_k + sub] = id;
+        a.weights[token * a.top_k + sub] = mine * a.scale;
+    }
+}
+
+bool by_rows(const RouteArgs& a) { return !a.bias && a.groups == 1 && a.experts <= 256 && a.top_k <= 16 && a.tokens >= 1024; }
+
+template <w4a8_float TYPE>
+hipError_t launch_rows(const RouteArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)((a.tokens + 4 * kRouteWaves - 1) / (4 * kRouteWaves))), block(64 * kRouteWaves);
+#define W4A8_ROUTE(NL) hipLaunchKernelGGL((route_rows_kernel<TYPE, NL>), grid, block, 0, stream, a)
+    if (a.experts <= 16) W4A8_ROUTE(1);
+    else if (a.experts <= 32) W4A8_ROUTE(2);
+    else if (a.experts <= 64) W4A8_ROUTE(4);
+    else if (a.experts <= 128) W4A8_ROUTE(8);
+    else W4A8_ROUTE(16);
+#undef W4A8_ROUTE
+    return hipGetLastError();
 }
 
 template <w4a8_float TYPE, typename S>
@@ -190,6 +267,10 @@ int64_t moe_route_threads(const RouteArgs& a) { return (a.tokens + kRouteWaves -
 
 hipError_t launch_moe_route(const RouteArgs& a, w4a8_float type, hipStream_t stream) {
     const bool by_score = a.bias || a.groups > 1;
+    if (by_rows(a))
+        return type == W4A8_FP32   ? launch_rows<W4A8_FP32>(a, stream)
+               : type == W4A8_FP16 ? launch_rows<W4A8_FP16>(a, stream)
+                                   : launch_rows<W4A8_BF16>(a, stream);
     switch (type) {
         case W4A8_FP32: return by_score ? launch_type<W4A8_FP32, double>(a, stream) : launch_type<W4A8_FP32, float>(a, stream);
         case W4A8_FP16: return by_score ? launch_type<W4A8_FP16, double>(a, stream) : launch_type<W4A8_FP16, float>(a, stream);

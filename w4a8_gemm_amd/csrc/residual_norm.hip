@@ -17,7 +17,7 @@
 // the wave; else a workgroup per row whose waves join sums through LDS.  Rows need
 // no alignment (16-byte loads at element alignment); the last, shorter run of a
 // row whose length is no multiple of eight goes element by element.
-#include "w4a8_internal.h"
+#include "wave_ops.h"
 
 #pragma clang fp contract(off)
 
@@ -50,25 +50,49 @@ __device__ __forceinline__ void widen8(u32x4 d, float (&x)[8]) {
     }
 }
 
-// values [at, at + 8) of a row of n, zeros past its end
-template <bool FP16>
+// Values [at, at + 8) of a row of n, zeros past its end.  The load is the same for all lanes, of a row's last
+// eight where the run is shorter; those lanes shift it, so that no second load is waited for.
 __device__ __forceinline__ u32x4 load8(const uint16_t* row, int at, int n) {
-    if (at + 8 <= n) return reinterpret_cast<const Half8*>(row + at)->d;
-    u32x4 d = {0u, 0u, 0u, 0u};
+    if (n < 8) {   // the same for all threads
+        u32x4 d = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (at + j < n) d[j >> 1] |= (uint32_t)row[at + j] << (16 * (j & 1));
+        for (int j = 0; j < 7; ++j)
+            if (at + j < n) d[j >> 1] |= (uint32_t)row[at + j] << (16 * (j & 1));
+        return d;
+    }
+    u32x4 d = reinterpret_cast<const Half8*>(row + min(at, n - 8))->d;
+    const int past = at + 8 - n;
+    if (past > 0) {
+        uint64_t lo = d[0] | (uint64_t)d[1] << 32, hi = d[2] | (uint64_t)d[3] << 32;
+        if (past >= 4) lo = hi, hi = 0;
+        if (past >= 8) lo = 0;
+        const int by = 16 * (past & 3);
+        if (by) lo = lo >> by | hi << (64 - by), hi >>= by;
+        d = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
     return d;
 }
 __device__ __forceinline__ void load8(const float* row, int at, int n, float (&x)[8]) {
-    if (at + 8 <= n) {
-        const f32x4 u = reinterpret_cast<const Float4*>(row + at)->v, v = reinterpret_cast<const Float4*>(row + at + 4)->v;
+    if (n < 8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = u[j], x[4 + j] = v[j];
+        for (int j = 0; j < 8; ++j) x[j] = at + j < n ? row[at + j] : 0.0f;
         return;
     }
+    const float* from = row + min(at, n - 8);
+    const f32x4 u = reinterpret_cast<const Float4*>(from)->v, v = reinterpret_cast<const Float4*>(from + 4)->v;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = at + j < n ? row[at + j] : 0.0f;
+    for (int j = 0; j < 4; ++j) x[j] = u[j], x[4 + j] = v[j];
+    const int past = at + 8 - n;
+    if (past > 0) {
+#pragma unroll
+        for (int b = 1; b <= 4; b *= 2)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (past & b) x[j] = j + b < 8 ? x[j + b] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (past >= 8) x[j] = 0.0f;
+    }
 }
 template <bool FP16>
 __device__ __forceinline__ void store8(uint16_t* row, int at, int n, const float (&x)[8]) {
@@ -111,23 +135,20 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int at, int n, const f
         if (at + j < n) row[at + j] = (uint8_t)(d[j >> 2] >> (8 * (j & 3)));
 }
 
-// sum (or, of magnitudes' bits, maximum) over a row's threads; `part` is this
+// sum (or, of magnitudes' bits, maximum) over a row's threads, zero for none; `part` is this
 // reduction's own words of LDS
 template <typename T, typename F>
-__device__ __forceinline__ T row_reduce(T v, F f, bool one_wave, T* part) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v = f(v, __shfl_xor(v, off));
+__device__ __forceinline__ T threads_reduce(T v, F f, bool one_wave, T* part) {
+    v = wave_reduce(v, f);
     if (one_wave) return v;
-    const int waves = blockDim.x >> 6;
+    const int waves = blockDim.x >> 6, lane = threadIdx.x & (kMaxWaves - 1);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = part[0];
-    for (int i = 1; i < waves; ++i) v = f(v, part[i]);
-    return v;
+    return row_reduce(lane < waves ? part[lane] : T(0), f);
 }
 
 template <bool FP16, int R>
-__global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(NormArgs a, bool one_wave) {
+__global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a, bool one_wave) {
     __shared__ float sums[2][kMaxWaves];
     __shared__ uint32_t tops[kMaxWaves];
     const int threads = one_wave ? 64 : blockDim.x, tid = one_wave ? threadIdx.x & 63 : threadIdx.x;
@@ -135,13 +156,12 @@ __global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(Norm
     if (row >= a.tokens) return;   // whole waves, and no barrier follows where rows are waves
     const int n = a.hidden;
     const float over_n = 1.0f / (float)n;
-    const auto add = [](float x, float y) { return x + y; };
 
     const uint16_t* y = a.y + row * a.ldy;
     u32x4 raw[R];
     float x[R][8], old[R][8];
 #pragma unroll
-    for (int i = 0; i < R; ++i) raw[i] = load8<FP16>(y, 8 * (tid + i * threads), n);
+    for (int i = 0; i < R; ++i) raw[i] = load8(y, 8 * (tid + i * threads), n);
     if (a.residual) {
         if (a.residual_fp32) {
             const float* p = static_cast<const float*>(a.residual) + row * a.ldr;
@@ -150,7 +170,7 @@ __global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(Norm
         } else {
             const uint16_t* p = static_cast<const uint16_t*>(a.residual) + row * a.ldr;
 #pragma unroll
-            for (int i = 0; i < R; ++i) widen8<FP16>(load8<FP16>(p, 8 * (tid + i * threads), n), old[i]);
+            for (int i = 0; i < R; ++i) widen8<FP16>(load8(p, 8 * (tid + i * threads), n), old[i]);
         }
     } else {
 #pragma unroll
@@ -167,7 +187,7 @@ __global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(Norm
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s = __builtin_fmaf(x[i][j], x[i][j], s);
-        s = row_reduce(s, add, one_wave, sums[0]);
+        s = threads_reduce(s, Add(), one_wave, sums[0]);
         const float k = 1.0f / __builtin_sqrtf(s * over_n + a.eps);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -183,7 +203,7 @@ __global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(Norm
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 float w[8];
-                widen8<FP16>(load8<FP16>(g, 8 * (tid + i * threads), n), w);
+                widen8<FP16>(load8(g, 8 * (tid + i * threads), n), w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[i][j] *= w[j];
             }
@@ -219,7 +239,7 @@ __global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(Norm
     }
     if (!a.out && !a.x8) return;
 
-    s = row_reduce(s, add, one_wave, sums[1]);
+    s = threads_reduce(s, Add(), one_wave, sums[1]);
     const float k = 1.0f / __builtin_sqrtf(s * over_n + a.eps);
     uint32_t top = 0u;   // bits of |h|: NaN over infinity over the finite ones
 #pragma unroll
@@ -243,7 +263,7 @@ __global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(Norm
         for (int i = 0; i < R; ++i) store8<FP16>(p, 8 * (tid + i * threads), n, x[i]);
     }
     if (!a.x8) return;
-    top = row_reduce(top, [](uint32_t p, uint32_t q) { return max(p, q); }, one_wave, tops);
+    top = threads_reduce(top, Max(), one_wave, tops);
     // s = amax / 448, the codes by its reciprocal: below 2^-110 that would pass fp32
     const float amax = top == 0u ? 448.0f : __uint_as_float(max(top, __float_as_uint(0x1p-110f)));
     const float to_code = 448.0f / amax;
@@ -260,15 +280,14 @@ __global__ __launch_bounds__(R == 8 ? 512 : 1024) void residual_norm_kernel(Norm
 struct NormShape {
     int threads, r;   // threads of a row (64: a wave, four rows to a workgroup) and runs of each
 };
-// As many runs per thread as leave a row at least four waves; one where rows are few.
+// Many rows: two runs to a thread (16384 rows of 5120: 106 us, with one 129, with four 111), but one where a
+// row has no more than a wave's (16384 rows of 256: 15 us, with two 23).  Few rows wait for their latency:
+// one run (a row of 5120: 4.1 us, with two 4.6).  More where 16 waves are too few.
 NormShape norm_shape(const NormArgs& a) {
     const int runs = (a.hidden + 7) / 8;
-    const auto waves = [&](int r) { return (runs + 64 * r - 1) / (64 * r); };
-    int r = 1;
-    const int least = a.tokens >= 512 ? 1 : 4;
-    while (r < 8 && (waves(r) > kMaxWaves || (a.tokens >= 64 && waves(2 * r) >= least))) r *= 2;
-    if (a.tokens >= 512 && r > 4 && waves(4) <= 4) r = 4;
-    return {64 * waves(r), r};
+    int r = runs <= 64 || a.tokens < 1024 ? 1 : 2;
+    while ((runs + 64 * r - 1) / (64 * r) > kMaxWaves) r *= 2;
+    return {64 * ((runs + 64 * r - 1) / (64 * r)), r};
 }
 
 template <bool FP16, int R>
@@ -285,8 +304,7 @@ hipError_t launch_norm_type(const NormArgs& a, hipStream_t stream) {
     switch (s.r) {
         case 1: return launch_norm<FP16, 1>(a, s.threads, stream);
         case 2: return launch_norm<FP16, 2>(a, s.threads, stream);
-        case 4: return launch_norm<FP16, 4>(a, s.threads, stream);
-        default: return launch_norm<FP16, 8>(a, s.threads, stream);
+        default: return launch_norm<FP16, 4>(a, s.threads, stream);
     }
 }
 
