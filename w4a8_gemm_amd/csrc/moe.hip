@@ -55,6 +55,7 @@ __device__ __forceinline__ v4f product(v8i w, v8i x, v4f c, uint32_t sw, uint32_
 struct alignas(16) MoePlan {
     uint16_t list[kMoeSlots];           // slots (of the chunk) by expert, in order
     uint32_t unit[kMoeSlots];           // first place | (slots - 1) << 11 | expert << 18
+    float scale[2][128];                // token scales of a unit's columns, of every other item
     uint32_t part[16];
     int units;
 };
@@ -298,33 +299,50 @@ struct UpStep {
     u32x4 x[2];
 };
 
-// v of 32 of inter (block blk) for 16 columns, from the sums of the tiles: a lane has 4 values of each half
+// Four values of v of a lane, from the sums of a gate's and an up tile; the bits of the largest magnitude
+struct Quad {
+    float v[4];
+    uint32_t top;
+};
+__device__ __forceinline__ Quad quad_of(const v4f& gate, const v4f& up, float sx, int act) {
+    Quad q;
+    q.top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q.v[i] = activated(sx * gate[i], act) * (sx * up[i]);
+        q.top = max(q.top, __float_as_uint(q.v[i]) & 0x7FFFFFFFu);
+    }
+    return q;
+}
+// over the four lanes of a column
+__device__ __forceinline__ uint32_t column_top(uint32_t top) {
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    return max(top, (uint32_t)__shfl_xor((int)top, 32));
+}
+// the block's exponent: the least e with top <= 448 2^e = 1.75 2^(e + 8), at least -127
+__device__ __forceinline__ int block_power(uint32_t top) {
+    return max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -127);
+}
+__device__ __forceinline__ void store_quad(const MoeShape& m, const Quad& q, uint32_t top, int64_t row, int at) {
+    const float to_code = __uint_as_float((uint32_t)(127 - block_power(top)) << 23);   // 2^-e, -e <= 127
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(q.v[0] * to_code, q.v[1] * to_code, 0, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(q.v[2] * to_code, q.v[3] * to_code, c, true);
+    *reinterpret_cast<int*>(m.v + row * m.inter + at) = top < 0x7F800000u ? c : 0x7F7F7F7F;
+}
+__device__ __forceinline__ void store_power(const MoeShape& m, uint32_t top, int64_t row, int blk) {
+    // block blk: k / 32 % 4 = blk % 4 of step blk / 4
+    m.ve[row * m.e_stride + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] =
+        top < 0x7F800000u ? (uint8_t)(block_power(top) + 127) : 255;
+}
+// v of 32 of inter (block blk) for 16 columns, from the sums of its four tiles: a lane has 4 values of each half
 __device__ __forceinline__ void store_v(const MoeShape& m, const v4f (&r)[4], float sx, int act, int64_t row, int blk, int g,
                                         bool mine) {
-    float v[2][4];
-    uint32_t top = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[h][i] = activated(sx * r[h][i], act) * (sx * r[2 + h][i]);
-            top = max(top, __float_as_uint(v[h][i]) & 0x7FFFFFFFu);
-        }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-    // the least e with top <= 448 2^e = 1.75 2^(e + 8)
-    const int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -127);
-    const bool finite = top < 0x7F800000u;
-    const float to_code = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e, -e <= 127
+    const Quad a = quad_of(r[0], r[2], sx, act), b = quad_of(r[1], r[3], sx, act);
+    const uint32_t top = column_top(max(a.top, b.top));
     if (!mine) return;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[h][0] * to_code, v[h][1] * to_code, 0, false);
-        c = __builtin_amdgcn_cvt_pk_fp8_f32(v[h][2] * to_code, v[h][3] * to_code, c, true);
-        *reinterpret_cast<int*>(m.v + row * m.inter + 32 * blk + 16 * h + 4 * g) = finite ? c : 0x7F7F7F7F;
-    }
-    if (g == 0)   // block blk: k / 32 % 4 = blk % 4 of step blk / 4
-        m.ve[row * m.e_stride + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] = finite ? (uint8_t)(e + 127) : 255;
+    store_quad(m, a, top, row, 32 * blk + 4 * g);
+    store_quad(m, b, top, row, 32 * blk + 16 + 4 * g);
+    if (g == 0) store_power(m, top, row, blk);
 }
 
 // WAVE: up to 64 slots, listed by every wave; else listed in LDS.  Two steps in flight, two workgroups
@@ -629,8 +647,11 @@ struct Tiles {
     }
 };
 
-template <int MT, int D>
-__global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(UpArgs a) {
+// R = 4: a wave takes 32 of inter, two tiles each of the gate's and the up rows; R = 2: 16 of inter, one
+// of each, the waves of a pair agreeing on their block's largest value through LDS.  R = 2 leaves
+// registers for more columns.
+template <int R, int MT, int D>
+__global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int kBuf = 16 * MT * kChunkBytes;
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
@@ -641,11 +662,13 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(
 
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, col = threadIdx.x >> 5;
     const ColumnReader cr;
-    const int blocks = (int)(m.inter / 32), groups = (blocks + 7) / 8, items = p.units * groups;
+    const int blocks = (int)(m.inter / (8 * R)), groups = (blocks + 7) / 8, items = p.units * groups;   // blocks of a wave
     const int steps = m.h_steps, chunks = (steps + 3) / 4;
     const int64_t tiles_i = m.inter / 16;
     const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
+    float* scale = p.scale[1];
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        scale = p.scale[scale == p.scale[1] ? 0 : 1];   // a slow wave may still read the last item's
         const int of = a.by_blocks.quotient(item);
         const uint32_t u = uniform(p.unit[of]);
         const int first = unit_first(u), cols = unit_slots(u), blk = a.by_blocks.rest(item, of) * 8 + wave;
@@ -656,26 +679,22 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(
             row[i] = 16 * i + col < cols ? (uint32_t)m.by_top_k.quotient(p.list[first + 16 * i + col]) * (uint32_t)m.hidden : kNowhere;
         Stage<MT> st;
         st.load(x, row, 0, (int)m.hidden);
-        int slot[MT];
-        float sx[MT];
+        float sx = 0.0f;
+        if ((int)threadIdx.x < cols) sx = a.xs[t0 + m.by_top_k.quotient(p.list[first + threadIdx.x])];
+        Tiles<R, D> w;
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            slot[j] = p.list[first + min(16 * j + n, cols - 1)];
-            sx[j] = a.xs[t0 + m.by_top_k.quotient(slot[j])];
-        }
-        Tiles<4, D> w;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            w.at(q, a.w, a.s, (2 * unit_expert(u) + (q >> 1)) * tiles_i + 2 * (live ? blk : blocks - 1) + (q & 1), chunks);
+        for (int q = 0; q < R; ++q)
+            w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), chunks);
         w.load_scales(0);
 #pragma unroll
         for (int s = 0; s < D; ++s) w.load(min(s, steps - 1), s);
-        v4f acc[4][MT];
+        v4f acc[R][MT];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < R; ++q)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
         st.store(lds, cols);
+        if ((int)threadIdx.x < cols) scale[threadIdx.x] = sx;
         __syncthreads();
         const auto products = [&](const uint8_t* buf, auto step) {
             constexpr int s = decltype(step)::value;
@@ -683,7 +702,7 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(
             for (int j = 0; j < MT; ++j) {
                 const v8i b = cr.read(buf, j, s);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s % D][q]), b, acc[q][j], w.sc[q]);
+                for (int q = 0; q < R; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s % D][q]), b, acc[q][j], w.sc[q]);
                 if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);   // no more than two tiles' columns in registers
             }
         };
@@ -710,12 +729,32 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void up_tile_kernel(
             if constexpr (s + D < 4) w.load(min(4 * (chunks - 1) + s + D, steps - 1), s % D);
         });
         __syncthreads();   // before the next item's first columns
-        if (live) {
+        if constexpr (R == 2) {   // blocks in pairs: every wave is live
+            uint32_t* tops = reinterpret_cast<uint32_t*>(lds);   // [wave][column]
+            Quad v[MT];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                v[j] = quad_of(acc[0][j], acc[1][j], scale[16 * j + n], a.act);
+                v[j].top = column_top(v[j].top);
+                if (g == 0) tops[wave * 16 * MT + 16 * j + n] = v[j].top;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const uint32_t top = max(v[j].top, tops[(wave ^ 1) * 16 * MT + 16 * j + n]);
+                if (16 * j + n >= cols) continue;
+                const int64_t at = t0 * m.top_k + p.list[first + 16 * j + n];
+                store_quad(m, v[j], top, at, 16 * blk + 4 * g);
+                if (g == 0 && !(wave & 1)) store_power(m, top, at, blk >> 1);
+            }
+            __syncthreads();
+        } else if (live) {
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 if (16 * j >= cols) continue;
                 const v4f r[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
-                store_v(m, r, sx[j], a.act, t0 * m.top_k + slot[j], blk, g, 16 * j + n < cols);
+                store_v(m, r, scale[16 * j + n], a.act, t0 * m.top_k + p.list[first + min(16 * j + n, cols - 1)], blk, g,
+                        16 * j + n < cols);
             }
         }
     }
@@ -876,7 +915,7 @@ constexpr int64_t kSumRows = 2048;
 struct MoeGrid {
     bool few, up_tiles;             // few: up to 64 slots
     int mt;                         // column tiles of the tile kernels' units
-    int kw, rows, ks;
+    int kw, rows, ks, up_groups;
     unsigned up, down, join, chunks;
     size_t up_at, down_at;          // LDS of the kernels before the plan
 };
@@ -890,12 +929,13 @@ MoeGrid moe_grid(const MoeArgs& a) {
     double missed = 1.0;
     for (int64_t s = 0; s < slots && missed > 1e-3; ++s) missed *= 1.0 - 1.0 / (double)experts;
     const int64_t met = (int64_t)((double)experts * (1.0 - missed) + 0.5);
-    const int64_t blocks = a.e.inter / 32, up_groups = (blocks + 7) / 8, down_groups = (a.e.hidden / 16 + 15) / 16;
-    g.few = slots <= kWaveSlots;
-    g.up_tiles = !g.few && met * up_groups >= 128;
+    const int64_t blocks = a.e.inter / 32, down_groups = (a.e.hidden / 16 + 15) / 16;
     // by the slots that an expert has on average, with some to spare
     const int64_t each = slots / experts;
-    g.mt = each <= 18 ? 2 : each <= 44 ? 4 : 6;
+    g.few = slots <= kWaveSlots;
+    g.mt = each <= 18 ? 2 : each <= 44 ? 4 : 8;
+    g.up_groups = (int)(g.mt == 2 ? (blocks + 7) / 8 : blocks / 4);
+    g.up_tiles = !g.few && met * g.up_groups >= 128;
     const auto units = [&](int64_t columns) {
         const int64_t most = slots < experts ? slots : experts + slots / columns;
         return most < slots ? most : slots;
@@ -904,7 +944,7 @@ MoeGrid moe_grid(const MoeArgs& a) {
     const auto at = [&](int64_t bytes) { return (size_t)bytes > scratch ? (size_t)bytes : scratch; };
     const auto grid = [&](int64_t groups) { return (unsigned)(groups < 2 * cus ? groups : 2 * cus); };
     if (g.up_tiles) {
-        g.up = grid(units(16 * g.mt) * up_groups);
+        g.up = grid(units(16 * g.mt) * g.up_groups);
         g.up_at = at(2 * 16 * g.mt * kChunkBytes);
     } else {
         const int64_t items = units(16) * blocks, steps = a.e.hidden / 128;
@@ -944,19 +984,15 @@ hipError_t launch_one(void (*f)(A), unsigned x, unsigned y, int threads, size_t 
     return hipGetLastError();
 }
 
-template <int MT>
-hipError_t launch_up_tiles(const MoeGrid& g, const UpArgs& a, size_t bytes, hipStream_t stream) {
-    return launch_one(up_tile_kernel<MT, MT == 4 ? 4 : 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
-}
 hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
     a.plan_at = (int)g.up_at;
     if (g.few) return launch_one(up_kernel<true>, g.up, 1, kUpThreads, g.up_at, stream, a);
     const size_t bytes = g.up_at + sizeof(MoePlan);
     if (!g.up_tiles) return launch_one(up_kernel<false>, g.up, g.chunks, kUpThreads, bytes, stream, a);
     switch (g.mt) {
-        case 2: return launch_up_tiles<2>(g, a, bytes, stream);
-        case 4: return launch_up_tiles<4>(g, a, bytes, stream);
-        default: return launch_up_tiles<6>(g, a, bytes, stream);
+        case 2: return launch_one(up_tile_kernel<4, 2, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+        case 4: return launch_one(up_tile_kernel<2, 4, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+        default: return launch_one(up_tile_kernel<2, 8, 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
     }
 }
 
@@ -969,7 +1005,7 @@ hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStre
     const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, Divisor((a.m.hidden / 16 + 15) / 16 * g.ks), (int)g.down_at};
     const hipError_t e = g.mt == 2   ? launch_down_tiles<2>(g, d, stream)
                          : g.mt == 4 ? launch_down_tiles<4>(g, d, stream)
-                                     : launch_down_tiles<6>(g, d, stream);
+                                     : launch_down_tiles<8>(g, d, stream);
     return e != hipSuccess ? e : launch_one(join_kernel, g.join, 1, 256, 0, stream, d);
 }
 
@@ -998,7 +1034,7 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
     m.e_stride = exponent_stride(a.e.inter);
     const int64_t slots = a.tokens * a.top_k;
     m.v = a.ws, m.ve = a.ws + slots * a.e.inter;
-    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(g.up_tiles ? (a.e.inter / 32 + 7) / 8 : a.e.inter / 32), Divisor(g.up_tiles ? 1 : g.kw), 0}, stream);
+    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(g.up_tiles ? g.up_groups : a.e.inter / 32), Divisor(g.up_tiles ? 1 : g.kw), 0}, stream);
     if (e != hipSuccess) return e;
     return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows},
                        reinterpret_cast<float*>(m.ve + slots * m.e_stride), stream);
