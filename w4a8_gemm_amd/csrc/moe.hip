@@ -563,11 +563,11 @@ struct Stage {                 // what a thread brings of a chunk: piece tid % 3
         for (int i = 0; i < MT; ++i)
             r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, at + c < width ? row[i] + c : kNowhere, at, 0));
     }
-    __device__ __forceinline__ void store(uint8_t* to, int cols) const {
+    // columns past the unit's last are zeros: their products cost least
+    __device__ __forceinline__ void store(uint8_t* to) const {
         const int c = threadIdx.x & 31, col = threadIdx.x >> 5;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-            if (16 * i + col < cols) *reinterpret_cast<u32x4*>(to + piece(16 * i + col, c)) = r[i];
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<u32x4*>(to + piece(16 * i + col, c)) = r[i];
     }
 };
 // Where a lane finds its two pieces of step s of column 16 j + n: pieces 8 s + g and 8 s + 4 + g, whose
@@ -693,7 +693,7 @@ __global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_ker
         for (int q = 0; q < R; ++q)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        st.store(lds, cols);
+        st.store(lds);
         if ((int)threadIdx.x < cols) scale[threadIdx.x] = sx;
         __syncthreads();
         const auto products = [&](const uint8_t* buf, auto step) {
@@ -717,7 +717,7 @@ __global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_ker
                 w.load(min(4 * c + s + D, steps - 1), s % D);
                 __builtin_amdgcn_sched_barrier(0);
             });
-            st.store(lds + ((c + 1) & 1) * kBuf, cols);
+            st.store(lds + ((c + 1) & 1) * kBuf);
             __syncthreads();
         }
         w.last_scales();
@@ -807,7 +807,7 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kerne
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
         const auto put = [&](uint8_t* to) {
-            st.store(to, cols);
+            st.store(to);
             if (has_e) *reinterpret_cast<u32x4*>(to + kCols + 16 * threadIdx.x) = er;
         };
         put(lds);
@@ -942,7 +942,9 @@ MoeGrid moe_grid(const MoeArgs& a) {
     };
     const size_t scratch = g.few ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
     const auto at = [&](int64_t bytes) { return (size_t)bytes > scratch ? (size_t)bytes : scratch; };
-    const auto grid = [&](int64_t groups) { return (unsigned)(groups < 2 * cus ? groups : 2 * cus); };
+    // as many workgroups of the tile kernels as the CUs hold at once: each lists the slots only once
+    const int64_t room = g.mt == 8 ? cus : 2 * cus;
+    const auto grid = [&](int64_t groups) { return (unsigned)(groups < room ? groups : room); };
     if (g.up_tiles) {
         g.up = grid(units(16 * g.mt) * g.up_groups);
         g.up_at = at(2 * 16 * g.mt * kChunkBytes);
@@ -992,7 +994,7 @@ hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
     switch (g.mt) {
         case 2: return launch_one(up_tile_kernel<4, 2, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
         case 4: return launch_one(up_tile_kernel<2, 4, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
-        default: return launch_one(up_tile_kernel<2, 8, 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+        default: return launch_one(up_tile_kernel<2, 8, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
     }
 }
 
