@@ -51,7 +51,9 @@ def _check(got, want, rows=None, name=""):
 SHAPES = [(1, 1, 1, 128, 128), (1, 8, 2, 256, 384), (1, 8, 8, 1152, 640), (3, 5, 3, 384, 128), (17, 4, 4, 128, 640),
           (64, 2, 2, 256, 256), (130, 2, 1, 128, 256), (200, 16, 8, 256, 128), (1030, 4, 2, 128, 128), (7, 300, 5, 128, 128),
           (2, 1024, 32, 128, 128), (5, 64, 6, 512, 896), (33, 8, 2, 2048, 1408), (64, 1, 1, 128, 1152), (300, 3, 3, 256, 128),
-          (40, 1, 1, 640, 256), (2049, 3, 1, 128, 128), (15, 16, 1, 256, 256), (16, 60, 4, 256, 2048), (4, 40, 2, 4096, 128)]
+          (40, 1, 1, 640, 256), (2049, 3, 1, 128, 128), (15, 16, 1, 256, 256), (16, 60, 4, 256, 2048), (4, 40, 2, 4096, 128),
+          (70, 1, 1, 128, 8192), (300, 1, 1, 256, 4096), (513, 2, 2, 128, 2048), (140, 3, 1, 1152, 1152), (260, 8, 2, 640, 2176),
+          (90, 30, 4, 384, 1152), (150, 1, 1, 5120, 128)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
@@ -134,6 +136,37 @@ def test_outputs_workspaces_and_rows_behind():
     with pytest.raises(ValueError, match="workspace"):
         c.run(workspace=small)
     assert w4.moe_mxfp4(c.x8[:0], c.xs[:0], c.ids[:0], c.w[:0], c.e).shape == (0, 256)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,hidden,inter", [
+    (70, 1, 1, 128, 8192), (65, 2, 1, 256, 16384), (300, 2, 1, 128, 8192), (64, 4, 1, 128, 128), (2, 33, 32, 128, 128),
+    (1000, 4, 3, 128, 512), (9, 8, 8, 384, 1152)])
+def test_nothing_is_written_past_the_workspace(tokens, experts, top_k, hidden, inter):
+    say("moe_mxfp4 end of the workspace", tokens, experts, top_k, hidden, inter)
+    c = Case(tokens, experts, top_k, hidden, inter)
+    ws = w4.MoEWorkspace(tokens, top_k, experts, hidden, inter)
+    guard = 4 << 20
+    whole = torch.full((ws.nbytes + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws.buf = whole[:ws.nbytes]
+    got = c.run(workspace=ws)
+    assert bool((whole[ws.nbytes:] == 0xA5).all())
+    _check(got, c.want())
+
+
+def test_captured_with_many_slots_to_an_expert():
+    say("moe_mxfp4 in a graph, many slots")
+    c = Case(200, 4, 2, 256, 384)
+    ws, out = w4.MoEWorkspace(200, 2, 4, 256, 384), torch.empty((200, 256), dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(workspace=ws, out=out)
+    for i in range(3):
+        c.ids.copy_(torch.roll(c.ids, 1 + i, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, c.run()), i
+        torch.cuda.synchronize()
+    _check(out, c.want())
 
 
 def test_weights_past_4_gib():

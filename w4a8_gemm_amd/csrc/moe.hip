@@ -909,8 +909,9 @@ __global__ __launch_bounds__(256) void join_kernel(DownTileArgs a) {
 // launch
 // ---------------------------------------------------------------------------
 int64_t exponent_stride(int64_t inter) { return (inter + 511) / 512 * 16; }
-// rows of the partial sums: parts of K where slots are few
+// Rows of the partial sums: one for each slot, or for up to four K parts of them within kSumRows
 constexpr int64_t kSumRows = 2048;
+int64_t moe_sum_rows(int64_t slots) { return slots >= kSumRows ? slots : 4 * slots < kSumRows ? 4 * slots : kSumRows; }
 
 struct MoeGrid {
     bool few, up_tiles;             // few: up to 64 slots
@@ -965,8 +966,9 @@ MoeGrid moe_grid(const MoeArgs& a) {
         g.down_at = (size_t)g.rows * 64 + (size_t)slots * 4;
     } else {
         const int64_t chunks_k = (a.e.inter + 511) / 512;
-        g.ks = 1;
-        while (2 * g.ks * met * down_groups <= 2 * cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k) g.ks *= 2;
+        g.ks = 1;   // 2 or 4 where there are too few units for the CUs, within moe_sum_rows
+        while (g.ks < 4 && 2 * g.ks * met * down_groups <= 2 * cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k)
+            g.ks *= 2;
         g.down = grid(units(16 * g.mt) * down_groups * g.ks);
         g.down_at = at(2 * 16 * g.mt * (kChunkBytes + 16));
         g.join = (unsigned)((a.tokens * (a.e.hidden / 4) + 255) / 256);
@@ -1015,8 +1017,7 @@ hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStre
 
 // v's codes and exponents, then (16-byte aligned) the partial sums
 size_t moe_workspace_bytes(int64_t slots, int64_t hidden, int64_t inter) {
-    const int64_t rows = slots >= kSumRows ? slots : 4 * slots < kSumRows ? 4 * slots : kSumRows;
-    return (size_t)(slots * (inter + exponent_stride(inter)) + rows * hidden * 4);
+    return (size_t)(slots * (inter + exponent_stride(inter)) + moe_sum_rows(slots) * hidden * 4);
 }
 
 int64_t moe_threads(const MoeArgs& a) {
