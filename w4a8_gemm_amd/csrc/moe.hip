@@ -539,7 +539,7 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
 // Every step of a chunk is computed: past K the columns are zeros, and the weights those of the
 // last step.  So are all MT column tiles: those without slots cost products that the
 // weights' arrival hides, conditions on them cost copies of the sums.
-constexpr int kTileThreads = 512, kChunkBytes = 512;
+constexpr int kTileThreads = 512;
 
 template <int OPSEL>
 __device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw) {
@@ -549,55 +549,75 @@ template <int OPSEL>
 __device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw, uint32_t sx) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmtFp4, kFmtFp8, OPSEL, (int)sw, OPSEL, (int)sx);
 }
-// 16-byte pieces of a column's 512, swapped within 256 by the column, so that the 16 columns of
-// a read meet all banks
-__device__ __forceinline__ int piece(int column, int c) { return column * kChunkBytes + 16 * (c ^ (column & 15)); }
+// C: steps of a chunk.  16-byte pieces of a column's 128 C, swapped within 256 by the column, so that the 16
+// columns of a read meet all banks
+template <int C>
+__device__ __forceinline__ int piece(int column, int c) { return column * 128 * C + 16 * (c ^ (column & 15)); }
 
-template <int MT>
-struct Stage {                 // what a thread brings of a chunk: piece tid % 32 of the columns tid / 32 + 16 i
-    u32x4 r[MT];
+template <int MT, int C>
+struct Stage {                 // what a thread brings of a chunk: piece tid % (8 C) of the columns tid / (8 C) + kRows i
+    static constexpr int kRows = kTileThreads / (8 * C), kPasses = 16 * MT / kRows;
+    u32x4 r[kPasses];
+    static __device__ __forceinline__ int column(int i) { return (int)threadIdx.x / (8 * C) + kRows * i; }
     // row: the columns' offsets from x, kNowhere past the last; width of a row in bytes
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, const uint32_t (&row)[MT], int chunk, int width) {
-        const int c = 16 * (threadIdx.x & 31), at = chunk * kChunkBytes;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, const uint32_t (&row)[kPasses], int chunk, int width) {
+        const int c = 16 * (threadIdx.x % (8 * C)), at = chunk * 128 * C;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < kPasses; ++i)
             r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, at + c < width ? row[i] + c : kNowhere, at, 0));
     }
-    // columns past the unit's last are zeros: their products cost least
-    __device__ __forceinline__ void store(uint8_t* to) const {
-        const int c = threadIdx.x & 31, col = threadIdx.x >> 5;
+    // the first chunk, with zeros past the unit's last column in both buffers: their products cost least
+    __device__ __forceinline__ void store_first(uint8_t* to, uint8_t* other, int cols) const {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) *reinterpret_cast<u32x4*>(to + piece(16 * i + col, c)) = r[i];
+        for (int i = 0; i < kPasses; ++i) {
+            const int at = piece<C>(column(i), threadIdx.x % (8 * C));
+            *reinterpret_cast<u32x4*>(to + at) = r[i];
+            if (C != 2 && column(i) >= cols) *reinterpret_cast<u32x4*>(other + at) = r[i];
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* to, int cols) const {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+            // with most columns the writes cost less than the condition (up: 68 us with 126 columns, 75 with it)
+            if (C == 2 || column(i) < cols) *reinterpret_cast<u32x4*>(to + piece<C>(column(i), threadIdx.x % (8 * C))) = r[i];
     }
 };
 // Where a lane finds its two pieces of step s of column 16 j + n: pieces 8 s + g and 8 s + 4 + g, whose
 // swap leaves four addresses, and constants beside them.
+template <int C>
 struct ColumnReader {
     int at[4];
     __device__ __forceinline__ ColumnReader() {
         const int n = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = n * kChunkBytes + 16 * ((g ^ n) ^ (4 * i));
+        for (int i = 0; i < 4; ++i) at[i] = n * 128 * C + 16 * ((g ^ n) ^ (4 * i));
     }
     __device__ __forceinline__ v8i read(const uint8_t* from, int j, int s) const {
-        const int more = 16 * j * kChunkBytes + 256 * (s >> 1), i = 2 * (s & 1);
+        const int more = 16 * j * 128 * C + 256 * (s >> 1), i = 2 * (s & 1);
         return frag_fp8(*reinterpret_cast<const u32x4*>(from + at[i] + more),
                         *reinterpret_cast<const u32x4*>(from + at[i + 1] + more));
     }
 };
-// f(integral_constant<int, 0>) .. <3>
-template <typename F>
-__device__ __forceinline__ void four_steps(F f) {
+// f(integral_constant<int, 0>) .. <C - 1>
+template <int C, typename F>
+__device__ __forceinline__ void each_step(F f) {
     f(std::integral_constant<int, 0>{});
     f(std::integral_constant<int, 1>{});
-    f(std::integral_constant<int, 2>{});
-    f(std::integral_constant<int, 3>{});
+    if constexpr (C == 4) {
+        f(std::integral_constant<int, 2>{});
+        f(std::integral_constant<int, 3>{});
+    }
+}
+// scale bytes of a chunk's steps first in the dword that has those of four
+template <int C>
+__device__ __forceinline__ uint32_t chunk_bytes(uint32_t four, int chunk) {
+    return C == 4 ? four : four >> (16 * (chunk & 1));
 }
 
-// a slot's exponents of a chunk; past K, where none were written, 2^0
-__device__ __forceinline__ u32x4 exponents(const uint8_t* row, int chunk, int steps) {
-    u32x4 e = *reinterpret_cast<const u32x4*>(row + 16 * chunk);
-    const int left = steps - 4 * chunk;
+// a slot's exponents of the four steps from `quad`'s; past K, where none were written, 2^0
+__device__ __forceinline__ u32x4 exponents(const uint8_t* row, int quad, int steps) {
+    u32x4 e = *reinterpret_cast<const u32x4*>(row + 16 * quad);
+    const int left = steps - 4 * quad;
     if (left < 4) {
         const uint32_t keep = (1u << (8 * left)) - 1;
 #pragma unroll
@@ -616,8 +636,8 @@ __device__ __forceinline__ void hold(v4f (&acc)[Q][MT]) {
         for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[q][j]));
 }
 
-// R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk
-template <int R, int D>
+// R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk of C
+template <int R, int D, int C>
 struct Tiles {
     __amdgpu_buffer_rsrc_t w[R], s[R];
     uint4 q[D][R];
@@ -635,35 +655,32 @@ struct Tiles {
     __device__ __forceinline__ void load_scales(int chunk) {
         const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int r = 0; r < R; ++r) next[r] = __builtin_amdgcn_raw_buffer_load_b32(s[r], 4 * lane, chunk * 256, 0);
+        for (int r = 0; r < R; ++r) next[r] = __builtin_amdgcn_raw_buffer_load_b32(s[r], 4 * lane, chunk * C / 4 * 256, 0);
     }
-    __device__ __forceinline__ void last_scales() {
+    // of the chunk that was asked for; then the next one's asked for
+    __device__ __forceinline__ void take_scales(int chunk) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) sc[r] = next[r];
-    }
-    __device__ __forceinline__ void next_scales(int chunk) {
-        last_scales();
-        load_scales(chunk);
+        for (int r = 0; r < R; ++r) sc[r] = chunk_bytes<C>(next[r], chunk);
     }
 };
 
 // R = 4: a wave takes 32 of inter, two tiles each of the gate's and the up rows; R = 2: 16 of inter, one
 // of each, the waves of a pair agreeing on their block's largest value through LDS.  R = 2 leaves
 // registers for more columns.
-template <int R, int MT, int D>
-__global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_kernel(UpArgs a) {
+template <int R, int MT, int D, int C, int WAVES>
+__global__ __launch_bounds__(kTileThreads, WAVES) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int kBuf = 16 * MT * kChunkBytes;
+    constexpr int kBuf = 16 * MT * 128 * C;
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
     make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
-    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, col = threadIdx.x >> 5;
-    const ColumnReader cr;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const ColumnReader<C> cr;
     const int blocks = (int)(m.inter / (8 * R)), groups = (blocks + 7) / 8, items = p.units * groups;   // blocks of a wave
-    const int steps = m.h_steps, chunks = (steps + 3) / 4;
+    const int steps = m.h_steps, chunks = (steps + C - 1) / C, c_pad = (steps + 3) / 4;
     const int64_t tiles_i = m.inter / 16;
     const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
     float* scale = p.scale[1];
@@ -673,18 +690,20 @@ __global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_ker
         const uint32_t u = uniform(p.unit[of]);
         const int first = unit_first(u), cols = unit_slots(u), blk = a.by_blocks.rest(item, of) * 8 + wave;
         const bool live = blk < blocks;   // a wave past the last block computes that one again
-        uint32_t row[MT];
+        Stage<MT, C> st;
+        uint32_t row[st.kPasses];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-            row[i] = 16 * i + col < cols ? (uint32_t)m.by_top_k.quotient(p.list[first + 16 * i + col]) * (uint32_t)m.hidden : kNowhere;
-        Stage<MT> st;
+        for (int i = 0; i < st.kPasses; ++i) {
+            const int col = st.column(i);
+            row[i] = col < cols ? (uint32_t)m.by_top_k.quotient(p.list[first + col]) * (uint32_t)m.hidden : kNowhere;
+        }
         st.load(x, row, 0, (int)m.hidden);
         float sx = 0.0f;
         if ((int)threadIdx.x < cols) sx = a.xs[t0 + m.by_top_k.quotient(p.list[first + threadIdx.x])];
-        Tiles<R, D> w;
+        Tiles<R, D, C> w;
 #pragma unroll
         for (int q = 0; q < R; ++q)
-            w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), chunks);
+            w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), c_pad);
         w.load_scales(0);
 #pragma unroll
         for (int s = 0; s < D; ++s) w.load(min(s, steps - 1), s);
@@ -693,7 +712,7 @@ __global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_ker
         for (int q = 0; q < R; ++q)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        st.store(lds);
+        st.store_first(lds, lds + kBuf, cols);
         if ((int)threadIdx.x < cols) scale[threadIdx.x] = sx;
         __syncthreads();
         const auto products = [&](const uint8_t* buf, auto step) {
@@ -708,25 +727,26 @@ __global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_ker
         };
         for (int c = 0; c + 1 < chunks; ++c) {
             st.load(x, row, c + 1, (int)m.hidden);
-            w.next_scales(c + 1);
-            four_steps([&](auto step) {
+            w.take_scales(c);
+            w.load_scales(c + 1);
+            each_step<C>([&](auto step) {
                 constexpr int s = decltype(step)::value;
                 products(lds + (c & 1) * kBuf, step);
                 hold(acc);
                 __builtin_amdgcn_sched_barrier(0);
-                w.load(min(4 * c + s + D, steps - 1), s % D);
+                w.load(min(C * c + s + D, steps - 1), s % D);
                 __builtin_amdgcn_sched_barrier(0);
             });
-            st.store(lds + ((c + 1) & 1) * kBuf);
+            st.store(lds + ((c + 1) & 1) * kBuf, cols);
             __syncthreads();
         }
-        w.last_scales();
-        four_steps([&](auto step) {
+        w.take_scales(chunks - 1);
+        each_step<C>([&](auto step) {
             constexpr int s = decltype(step)::value;
             products(lds + ((chunks - 1) & 1) * kBuf, step);
             hold(acc);
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (s + D < 4) w.load(min(4 * (chunks - 1) + s + D, steps - 1), s % D);
+            if constexpr (s + D < C) w.load(min(C * (chunks - 1) + s + D, steps - 1), s % D);
         });
         __syncthreads();   // before the next item's first columns
         if constexpr (R == 2) {   // blocks in pairs: every wave is live
@@ -762,20 +782,20 @@ __global__ __launch_bounds__(kTileThreads, R * MT <= 8 ? 4 : 2) void up_tile_ker
 
 // The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
 // device memory.
-template <int MT, int D>
-__global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kernel(DownTileArgs a) {
+template <int MT, int D, int C, int WAVES>
+__global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTileArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int kCols = 16 * MT * kChunkBytes, kBuf = kCols + 16 * MT * 16;   // columns, then their exponents
+    constexpr int kCols = 16 * MT * 128 * C, kBuf = kCols + 16 * MT * 16;   // columns, then their exponents
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
     make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
-    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, col = threadIdx.x >> 5;
-    const ColumnReader cr;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const ColumnReader<C> cr;
     const int tiles = (int)(m.hidden / 16), groups = (tiles + 15) / 16, items = p.units * groups * a.ks;
-    const int steps = m.i_steps, chunks = (steps + 3) / 4;
+    const int steps = m.i_steps, chunks = (steps + C - 1) / C, c_pad = (steps + 3) / 4;
     const __amdgpu_buffer_rsrc_t x = resource(m.v + t0 * m.top_k * m.inter, (uint32_t)(slots * m.inter));
     const uint8_t* xe = m.ve + t0 * m.top_k * m.e_stride;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -785,37 +805,40 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kerne
         const int first = unit_first(u), cols = unit_slots(u), tile = grp * 16 + 2 * wave;
         const bool live = tile < tiles;   // tiles are even; a wave past the last pair computes that one again
         const int c0 = chunks * k / a.ks, c1 = chunks * (k + 1) / a.ks;
-        uint32_t row[MT];
+        Stage<MT, C> st;
+        uint32_t row[st.kPasses];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-            row[i] = 16 * i + col < cols ? (uint32_t)p.list[first + 16 * i + col] * (uint32_t)m.inter : kNowhere;
+        for (int i = 0; i < st.kPasses; ++i) {
+            const int col = st.column(i);
+            row[i] = col < cols ? (uint32_t)p.list[first + col] * (uint32_t)m.inter : kNowhere;
+        }
         const bool has_e = (int)threadIdx.x < cols;
         const uint8_t* ep = xe + (uint32_t)p.list[first + min((int)threadIdx.x, cols - 1)] * (uint32_t)m.e_stride;
-        Stage<MT> st;
         u32x4 er{};
         st.load(x, row, c0, (int)m.inter);
-        if (has_e) er = exponents(ep, c0, steps);
-        Tiles<2, D> w;
+        if (has_e) er = exponents(ep, c0 * C / 4, steps);
+        Tiles<2, D, C> w;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, chunks);
+        for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, c_pad);
         w.load_scales(c0);
 #pragma unroll
-        for (int s = 0; s < D; ++s) w.load(min(4 * c0 + s, steps - 1), s);
+        for (int s = 0; s < D; ++s) w.load(min(C * c0 + s, steps - 1), s);
         v4f acc[2][MT];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        const auto put = [&](uint8_t* to) {
-            st.store(to);
+        const auto put_e = [&](uint8_t* to) {
             if (has_e) *reinterpret_cast<u32x4*>(to + kCols + 16 * threadIdx.x) = er;
         };
-        put(lds);
+        st.store_first(lds, lds + kBuf, cols);
+        put_e(lds);
         __syncthreads();
         uint32_t e[MT];
-        const auto read_e = [&](const uint8_t* buf) {
+        const auto read_e = [&](const uint8_t* buf, int chunk) {
 #pragma unroll
-            for (int j = 0; j < MT; ++j) e[j] = *reinterpret_cast<const uint32_t*>(buf + kCols + 16 * (16 * j + n) + 4 * g);
+            for (int j = 0; j < MT; ++j)
+                e[j] = chunk_bytes<C>(*reinterpret_cast<const uint32_t*>(buf + kCols + 16 * (16 * j + n) + 4 * g), chunk);
         };
         const auto products = [&](const uint8_t* buf, auto step) {
             constexpr int s = decltype(step)::value;
@@ -830,29 +853,31 @@ __global__ __launch_bounds__(kTileThreads, MT == 2 ? 4 : 2) void down_tile_kerne
         for (int c = c0; c + 1 < c1; ++c) {
             const uint8_t* buf = lds + ((c - c0) & 1) * kBuf;
             st.load(x, row, c + 1, (int)m.inter);
-            if (has_e) er = exponents(ep, c + 1, steps);
-            w.next_scales(c + 1);
-            read_e(buf);
-            four_steps([&](auto step) {
+            if (has_e) er = exponents(ep, (c + 1) * C / 4, steps);
+            w.take_scales(c);
+            w.load_scales(c + 1);
+            read_e(buf, c);
+            each_step<C>([&](auto step) {
                 constexpr int s = decltype(step)::value;
                 products(buf, step);
                 hold(acc);
                 __builtin_amdgcn_sched_barrier(0);
-                w.load(min(4 * c + s + D, steps - 1), s % D);
+                w.load(min(C * c + s + D, steps - 1), s % D);
                 __builtin_amdgcn_sched_barrier(0);
             });
-            put(lds + ((c - c0 + 1) & 1) * kBuf);
+            st.store(lds + ((c - c0 + 1) & 1) * kBuf, cols);
+            put_e(lds + ((c - c0 + 1) & 1) * kBuf);
             __syncthreads();
         }
-        w.last_scales();
+        w.take_scales(c1 - 1);
         const uint8_t* buf = lds + ((c1 - 1 - c0) & 1) * kBuf;
-        read_e(buf);
-        four_steps([&](auto step) {
+        read_e(buf, c1 - 1);
+        each_step<C>([&](auto step) {
             constexpr int s = decltype(step)::value;
             products(buf, step);
             hold(acc);
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (s + D < 4) w.load(min(4 * (c1 - 1) + s + D, steps - 1), s % D);
+            if constexpr (s + D < C) w.load(min(C * (c1 - 1) + s + D, steps - 1), s % D);
         });
         __syncthreads();   // before the next item's first columns
         if (live) {
@@ -913,6 +938,9 @@ int64_t exponent_stride(int64_t inter) { return (inter + 511) / 512 * 16; }
 constexpr int64_t kSumRows = 2048;
 int64_t moe_sum_rows(int64_t slots) { return slots >= kSumRows ? slots : 4 * slots < kSumRows ? 4 * slots : kSumRows; }
 
+// steps of the first product's chunks by the column tiles: two workgroups' buffers fit a CU
+constexpr int up_steps(int mt) { return mt == 8 ? 2 : 4; }
+
 struct MoeGrid {
     bool few, up_tiles;             // few: up to 64 slots
     int mt;                         // column tiles of the tile kernels' units
@@ -944,11 +972,10 @@ MoeGrid moe_grid(const MoeArgs& a) {
     const size_t scratch = g.few ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
     const auto at = [&](int64_t bytes) { return (size_t)bytes > scratch ? (size_t)bytes : scratch; };
     // as many workgroups of the tile kernels as the CUs hold at once: each lists the slots only once
-    const int64_t room = g.mt == 8 ? cus : 2 * cus;
-    const auto grid = [&](int64_t groups) { return (unsigned)(groups < room ? groups : room); };
+    const auto grid = [&](int64_t groups, int64_t room) { return (unsigned)(groups < room ? groups : room); };
     if (g.up_tiles) {
-        g.up = grid(units(16 * g.mt) * g.up_groups);
-        g.up_at = at(2 * 16 * g.mt * kChunkBytes);
+        g.up = grid(units(16 * g.mt) * g.up_groups, 2 * cus);
+        g.up_at = at(2 * 16 * g.mt * 128 * up_steps(g.mt));
     } else {
         const int64_t items = units(16) * blocks, steps = a.e.hidden / 128;
         // K parts while the workgroups are no more than the CUs, and so many that a wave has eight steps (one
@@ -969,8 +996,8 @@ MoeGrid moe_grid(const MoeArgs& a) {
         g.ks = 1;   // 2 or 4 where there are too few units for the CUs, within moe_sum_rows
         while (g.ks < 4 && 2 * g.ks * met * down_groups <= 2 * cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k)
             g.ks *= 2;
-        g.down = grid(units(16 * g.mt) * down_groups * g.ks);
-        g.down_at = at(2 * 16 * g.mt * (kChunkBytes + 16));
+        g.down = grid(units(16 * g.mt) * down_groups * g.ks, g.mt == 8 ? cus : 2 * cus);
+        g.down_at = at(2 * 16 * g.mt * (512 + 16));
         g.join = (unsigned)((a.tokens * (a.e.hidden / 4) + 255) / 256);
     }
     return g;
@@ -994,15 +1021,15 @@ hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
     const size_t bytes = g.up_at + sizeof(MoePlan);
     if (!g.up_tiles) return launch_one(up_kernel<false>, g.up, g.chunks, kUpThreads, bytes, stream, a);
     switch (g.mt) {
-        case 2: return launch_one(up_tile_kernel<4, 2, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
-        case 4: return launch_one(up_tile_kernel<2, 4, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
-        default: return launch_one(up_tile_kernel<2, 8, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+        case 2: return launch_one(up_tile_kernel<4, 2, 2, up_steps(2), 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+        case 4: return launch_one(up_tile_kernel<2, 4, 2, up_steps(4), 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+        default: return launch_one(up_tile_kernel<2, 8, 2, up_steps(8), 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
     }
 }
 
 template <int MT>
 hipError_t launch_down_tiles(const MoeGrid& g, const DownTileArgs& a, hipStream_t stream) {
-    return launch_one(down_tile_kernel<MT, 4>, g.down, g.chunks, kTileThreads, g.down_at + sizeof(MoePlan), stream, a);
+    return launch_one(down_tile_kernel<MT, 4, 4, MT == 2 ? 4 : 2>, g.down, g.chunks, kTileThreads, g.down_at + sizeof(MoePlan), stream, a);
 }
 hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStream_t stream) {
     if (g.few) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
