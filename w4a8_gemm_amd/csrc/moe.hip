@@ -549,69 +549,58 @@ template <int OPSEL>
 __device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw, uint32_t sx) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmtFp4, kFmtFp8, OPSEL, (int)sw, OPSEL, (int)sx);
 }
-// C: steps of a chunk.  16-byte pieces of a column's 128 C, swapped within 256 by the column, so that the 16
-// columns of a read meet all banks
-template <int C>
-__device__ __forceinline__ int piece(int column, int c) { return column * 128 * C + 16 * (c ^ (column & 15)); }
+// 16-byte pieces of a column's 512, swapped within 256 by the column, so that the 16 columns of a
+// read meet all banks
+__device__ __forceinline__ int piece(int column, int c) { return column * 512 + 16 * (c ^ (column & 15)); }
 
-template <int MT, int C>
-struct Stage {                 // what a thread brings of a chunk: piece tid % (8 C) of the columns tid / (8 C) + kRows i
-    static constexpr int kRows = kTileThreads / (8 * C), kPasses = 16 * MT / kRows;
-    u32x4 r[kPasses];
-    static __device__ __forceinline__ int column(int i) { return (int)threadIdx.x / (8 * C) + kRows * i; }
+template <int MT>
+struct Stage {                 // what a thread brings of a chunk: piece tid % 32 of the columns tid / 32 + 16 i
+    u32x4 r[MT];
+    static __device__ __forceinline__ int column(int i) { return (int)threadIdx.x / 32 + 16 * i; }
     // row: the columns' offsets from x, kNowhere past the last; width of a row in bytes
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, const uint32_t (&row)[kPasses], int chunk, int width) {
-        const int c = 16 * (threadIdx.x % (8 * C)), at = chunk * 128 * C;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, const uint32_t (&row)[MT], int chunk, int width) {
+        const int c = 16 * (threadIdx.x % 32), at = chunk * 512;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i)
+        for (int i = 0; i < MT; ++i)
             r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, at + c < width ? row[i] + c : kNowhere, at, 0));
     }
     // the first chunk, with zeros past the unit's last column in both buffers: their products cost least
     __device__ __forceinline__ void store_first(uint8_t* to, uint8_t* other, int cols) const {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int at = piece<C>(column(i), threadIdx.x % (8 * C));
+        for (int i = 0; i < MT; ++i) {
+            const int at = piece(column(i), threadIdx.x % 32);
             *reinterpret_cast<u32x4*>(to + at) = r[i];
-            if (C != 2 && column(i) >= cols) *reinterpret_cast<u32x4*>(other + at) = r[i];
+            if (column(i) >= cols) *reinterpret_cast<u32x4*>(other + at) = r[i];
         }
     }
     __device__ __forceinline__ void store(uint8_t* to, int cols) const {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i)
-            // with most columns the writes cost less than the condition (up: 68 us with 126 columns, 75 with it)
-            if (C == 2 || column(i) < cols) *reinterpret_cast<u32x4*>(to + piece<C>(column(i), threadIdx.x % (8 * C))) = r[i];
+        for (int i = 0; i < MT; ++i)
+            if (column(i) < cols) *reinterpret_cast<u32x4*>(to + piece(column(i), threadIdx.x % 32)) = r[i];
     }
 };
 // Where a lane finds its two pieces of step s of column 16 j + n: pieces 8 s + g and 8 s + 4 + g, whose
 // swap leaves four addresses, and constants beside them.
-template <int C>
 struct ColumnReader {
     int at[4];
     __device__ __forceinline__ ColumnReader() {
         const int n = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = n * 128 * C + 16 * ((g ^ n) ^ (4 * i));
+        for (int i = 0; i < 4; ++i) at[i] = n * 512 + 16 * ((g ^ n) ^ (4 * i));
     }
     __device__ __forceinline__ v8i read(const uint8_t* from, int j, int s) const {
-        const int more = 16 * j * 128 * C + 256 * (s >> 1), i = 2 * (s & 1);
+        const int more = 16 * 512 * j + 256 * (s >> 1), i = 2 * (s & 1);
         return frag_fp8(*reinterpret_cast<const u32x4*>(from + at[i] + more),
                         *reinterpret_cast<const u32x4*>(from + at[i + 1] + more));
     }
 };
-// f(integral_constant<int, 0>) .. <C - 1>
-template <int C, typename F>
+// f(integral_constant<int, 0>) .. <3>: the steps of a chunk
+template <typename F>
 __device__ __forceinline__ void each_step(F f) {
     f(std::integral_constant<int, 0>{});
     f(std::integral_constant<int, 1>{});
-    if constexpr (C == 4) {
-        f(std::integral_constant<int, 2>{});
-        f(std::integral_constant<int, 3>{});
-    }
-}
-// scale bytes of a chunk's steps first in the dword that has those of four
-template <int C>
-__device__ __forceinline__ uint32_t chunk_bytes(uint32_t four, int chunk) {
-    return C == 4 ? four : four >> (16 * (chunk & 1));
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
 }
 
 // a slot's exponents of the four steps from `quad`'s; past K, where none were written, 2^0
@@ -636,8 +625,8 @@ __device__ __forceinline__ void hold(v4f (&acc)[Q][MT]) {
         for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[q][j]));
 }
 
-// R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk of C
-template <int R, int D, int C>
+// R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk
+template <int R, int D>
 struct Tiles {
     __amdgpu_buffer_rsrc_t w[R], s[R];
     uint4 q[D][R];
@@ -655,22 +644,22 @@ struct Tiles {
     __device__ __forceinline__ void load_scales(int chunk) {
         const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int r = 0; r < R; ++r) next[r] = __builtin_amdgcn_raw_buffer_load_b32(s[r], 4 * lane, chunk * C / 4 * 256, 0);
+        for (int r = 0; r < R; ++r) next[r] = __builtin_amdgcn_raw_buffer_load_b32(s[r], 4 * lane, chunk * 256, 0);
     }
     // of the chunk that was asked for; then the next one's asked for
-    __device__ __forceinline__ void take_scales(int chunk) {
+    __device__ __forceinline__ void take_scales() {
 #pragma unroll
-        for (int r = 0; r < R; ++r) sc[r] = chunk_bytes<C>(next[r], chunk);
+        for (int r = 0; r < R; ++r) sc[r] = next[r];
     }
 };
 
 // R = 4: a wave takes 32 of inter, two tiles each of the gate's and the up rows; R = 2: 16 of inter, one
 // of each, the waves of a pair agreeing on their block's largest value through LDS.  R = 2 leaves
 // registers for more columns.
-template <int R, int MT, int D, int C, int WAVES>
-__global__ __launch_bounds__(kTileThreads, WAVES) void up_tile_kernel(UpArgs a) {
+template <int R, int MT, int D>
+__global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int kBuf = 16 * MT * 128 * C;
+    constexpr int kBuf = 16 * MT * 512;
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
@@ -678,9 +667,9 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void up_tile_kernel(UpArgs a) 
     make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const ColumnReader<C> cr;
+    const ColumnReader cr;
     const int blocks = (int)(m.inter / (8 * R)), groups = (blocks + 7) / 8, items = p.units * groups;   // blocks of a wave
-    const int steps = m.h_steps, chunks = (steps + C - 1) / C, c_pad = (steps + 3) / 4;
+    const int steps = m.h_steps, chunks = (steps + 3) / 4;
     const int64_t tiles_i = m.inter / 16;
     const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
     float* scale = p.scale[1];
@@ -690,20 +679,20 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void up_tile_kernel(UpArgs a) 
         const uint32_t u = uniform(p.unit[of]);
         const int first = unit_first(u), cols = unit_slots(u), blk = a.by_blocks.rest(item, of) * 8 + wave;
         const bool live = blk < blocks;   // a wave past the last block computes that one again
-        Stage<MT, C> st;
-        uint32_t row[st.kPasses];
+        Stage<MT> st;
+        uint32_t row[MT];
 #pragma unroll
-        for (int i = 0; i < st.kPasses; ++i) {
+        for (int i = 0; i < MT; ++i) {
             const int col = st.column(i);
             row[i] = col < cols ? (uint32_t)m.by_top_k.quotient(p.list[first + col]) * (uint32_t)m.hidden : kNowhere;
         }
         st.load(x, row, 0, (int)m.hidden);
         float sx = 0.0f;
         if ((int)threadIdx.x < cols) sx = a.xs[t0 + m.by_top_k.quotient(p.list[first + threadIdx.x])];
-        Tiles<R, D, C> w;
+        Tiles<R, D> w;
 #pragma unroll
         for (int q = 0; q < R; ++q)
-            w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), c_pad);
+            w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), chunks);
         w.load_scales(0);
 #pragma unroll
         for (int s = 0; s < D; ++s) w.load(min(s, steps - 1), s);
@@ -727,26 +716,26 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void up_tile_kernel(UpArgs a) 
         };
         for (int c = 0; c + 1 < chunks; ++c) {
             st.load(x, row, c + 1, (int)m.hidden);
-            w.take_scales(c);
+            w.take_scales();
             w.load_scales(c + 1);
-            each_step<C>([&](auto step) {
+            each_step([&](auto step) {
                 constexpr int s = decltype(step)::value;
                 products(lds + (c & 1) * kBuf, step);
                 hold(acc);
                 __builtin_amdgcn_sched_barrier(0);
-                w.load(min(C * c + s + D, steps - 1), s % D);
+                w.load(min(4 * c + s + D, steps - 1), s % D);
                 __builtin_amdgcn_sched_barrier(0);
             });
             st.store(lds + ((c + 1) & 1) * kBuf, cols);
             __syncthreads();
         }
-        w.take_scales(chunks - 1);
-        each_step<C>([&](auto step) {
+        w.take_scales();
+        each_step([&](auto step) {
             constexpr int s = decltype(step)::value;
             products(lds + ((chunks - 1) & 1) * kBuf, step);
             hold(acc);
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (s + D < C) w.load(min(C * (chunks - 1) + s + D, steps - 1), s % D);
+            if constexpr (s + D < 4) w.load(min(4 * (chunks - 1) + s + D, steps - 1), s % D);
         });
         __syncthreads();   // before the next item's first columns
         if constexpr (R == 2) {   // blocks in pairs: every wave is live
@@ -782,10 +771,10 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void up_tile_kernel(UpArgs a) 
 
 // The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
 // device memory.
-template <int MT, int D, int C, int WAVES>
+template <int MT, int D, int WAVES>
 __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTileArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int kCols = 16 * MT * 128 * C, kBuf = kCols + 16 * MT * 16;   // columns, then their exponents
+    constexpr int kCols = 16 * MT * 512, kBuf = kCols + 16 * MT * 16;   // columns, then their exponents
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
@@ -793,9 +782,9 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
     make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
 
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const ColumnReader<C> cr;
+    const ColumnReader cr;
     const int tiles = (int)(m.hidden / 16), groups = (tiles + 15) / 16, items = p.units * groups * a.ks;
-    const int steps = m.i_steps, chunks = (steps + C - 1) / C, c_pad = (steps + 3) / 4;
+    const int steps = m.i_steps, chunks = (steps + 3) / 4;
     const __amdgpu_buffer_rsrc_t x = resource(m.v + t0 * m.top_k * m.inter, (uint32_t)(slots * m.inter));
     const uint8_t* xe = m.ve + t0 * m.top_k * m.e_stride;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -805,10 +794,10 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
         const int first = unit_first(u), cols = unit_slots(u), tile = grp * 16 + 2 * wave;
         const bool live = tile < tiles;   // tiles are even; a wave past the last pair computes that one again
         const int c0 = chunks * k / a.ks, c1 = chunks * (k + 1) / a.ks;
-        Stage<MT, C> st;
-        uint32_t row[st.kPasses];
+        Stage<MT> st;
+        uint32_t row[MT];
 #pragma unroll
-        for (int i = 0; i < st.kPasses; ++i) {
+        for (int i = 0; i < MT; ++i) {
             const int col = st.column(i);
             row[i] = col < cols ? (uint32_t)p.list[first + col] * (uint32_t)m.inter : kNowhere;
         }
@@ -816,13 +805,13 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
         const uint8_t* ep = xe + (uint32_t)p.list[first + min((int)threadIdx.x, cols - 1)] * (uint32_t)m.e_stride;
         u32x4 er{};
         st.load(x, row, c0, (int)m.inter);
-        if (has_e) er = exponents(ep, c0 * C / 4, steps);
-        Tiles<2, D, C> w;
+        if (has_e) er = exponents(ep, c0, steps);
+        Tiles<2, D> w;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, c_pad);
+        for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, chunks);
         w.load_scales(c0);
 #pragma unroll
-        for (int s = 0; s < D; ++s) w.load(min(C * c0 + s, steps - 1), s);
+        for (int s = 0; s < D; ++s) w.load(min(4 * c0 + s, steps - 1), s);
         v4f acc[2][MT];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -835,10 +824,10 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
         put_e(lds);
         __syncthreads();
         uint32_t e[MT];
-        const auto read_e = [&](const uint8_t* buf, int chunk) {
+        const auto read_e = [&](const uint8_t* buf) {
 #pragma unroll
             for (int j = 0; j < MT; ++j)
-                e[j] = chunk_bytes<C>(*reinterpret_cast<const uint32_t*>(buf + kCols + 16 * (16 * j + n) + 4 * g), chunk);
+                e[j] = *reinterpret_cast<const uint32_t*>(buf + kCols + 16 * (16 * j + n) + 4 * g);
         };
         const auto products = [&](const uint8_t* buf, auto step) {
             constexpr int s = decltype(step)::value;
@@ -853,31 +842,31 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
         for (int c = c0; c + 1 < c1; ++c) {
             const uint8_t* buf = lds + ((c - c0) & 1) * kBuf;
             st.load(x, row, c + 1, (int)m.inter);
-            if (has_e) er = exponents(ep, (c + 1) * C / 4, steps);
-            w.take_scales(c);
+            if (has_e) er = exponents(ep, c + 1, steps);
+            w.take_scales();
             w.load_scales(c + 1);
-            read_e(buf, c);
-            each_step<C>([&](auto step) {
+            read_e(buf);
+            each_step([&](auto step) {
                 constexpr int s = decltype(step)::value;
                 products(buf, step);
                 hold(acc);
                 __builtin_amdgcn_sched_barrier(0);
-                w.load(min(C * c + s + D, steps - 1), s % D);
+                w.load(min(4 * c + s + D, steps - 1), s % D);
                 __builtin_amdgcn_sched_barrier(0);
             });
             st.store(lds + ((c - c0 + 1) & 1) * kBuf, cols);
             put_e(lds + ((c - c0 + 1) & 1) * kBuf);
             __syncthreads();
         }
-        w.take_scales(c1 - 1);
+        w.take_scales();
         const uint8_t* buf = lds + ((c1 - 1 - c0) & 1) * kBuf;
-        read_e(buf, c1 - 1);
-        each_step<C>([&](auto step) {
+        read_e(buf);
+        each_step([&](auto step) {
             constexpr int s = decltype(step)::value;
             products(buf, step);
             hold(acc);
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (s + D < C) w.load(min(C * (c1 - 1) + s + D, steps - 1), s % D);
+            if constexpr (s + D < 4) w.load(min(4 * (c1 - 1) + s + D, steps - 1), s % D);
         });
         __syncthreads();   // before the next item's first columns
         if (live) {
@@ -938,12 +927,9 @@ int64_t exponent_stride(int64_t inter) { return (inter + 511) / 512 * 16; }
 constexpr int64_t kSumRows = 2048;
 int64_t moe_sum_rows(int64_t slots) { return slots >= kSumRows ? slots : 4 * slots < kSumRows ? 4 * slots : kSumRows; }
 
-// steps of the first product's chunks by the column tiles: two workgroups' buffers fit a CU
-constexpr int up_steps(int mt) { return mt == 8 ? 2 : 4; }
-
 struct MoeGrid {
-    bool few, up_tiles;             // few: up to 64 slots
-    int mt;                         // column tiles of the tile kernels' units
+    bool few, few_down, up_tiles;   // few: up to 64 slots
+    int up_mt, down_mt;             // column tiles of the tile kernels' units
     int kw, rows, ks, up_groups;
     unsigned up, down, join, chunks;
     size_t up_at, down_at;          // LDS of the kernels before the plan
@@ -959,35 +945,53 @@ MoeGrid moe_grid(const MoeArgs& a) {
     for (int64_t s = 0; s < slots && missed > 1e-3; ++s) missed *= 1.0 - 1.0 / (double)experts;
     const int64_t met = (int64_t)((double)experts * (1.0 - missed) + 0.5);
     const int64_t blocks = a.e.inter / 32, down_groups = (a.e.hidden / 16 + 15) / 16;
-    // by the slots that an expert has on average, with some to spare
-    const int64_t each = slots / experts;
+    const int64_t each = slots / experts;   // slots of an expert, on average
     g.few = slots <= kWaveSlots;
-    g.mt = each <= 18 ? 2 : each <= 44 ? 4 : 8;
-    g.up_groups = (int)(g.mt == 2 ? (blocks + 7) / 8 : blocks / 4);
-    g.up_tiles = !g.few && met * g.up_groups >= 128;
+    // The first product: units of 64 slots and 16 of inter to a wave, which are more items for the same weights,
+    // or of 32 slots and 32 of inter, whose columns are read and staged half as often.  Microseconds (32 | 64) by
+    // tiles (16 of inter of an expert that is met) and slots of an expert: 1024 tiles, 6 slots 14.9 | 12.8;
+    // 3900, 1 22.4 | 24.0; 4096, 6 16.8 | 18.1; 4400, 1 21.4 | 23.3; 5400, 2 37.4 | 35.4; 6100, 4 40.2 | 37.0;
+    // 704, 47 19.0 | 13.9; 2048, 25 41.2 | 34.9; 4096, 16 54.0 | 51.3; 4096, 128 163 | 145.
+    // (Units of 128: 77 to 94 us for 74 to 76 with 8 experts, 63 slots each, hidden 4096, inter 8192.)
+    const int64_t tiles_up = met * (a.e.inter / 16);
+    g.up_mt = each < 8 && tiles_up > 2048 && tiles_up < 4800 ? 2 : 4;
+    // The second product, units of 32 or 64: the wider where they take an expert's slots in one for two or
+    // three (slots of an expert, 32 | 64: 16 27.6 | 33.6; 45 7.5 | 8.6; 50 25.9 | 26.9; 62 42.3 | 37.8; 63 55 | 47;
+    // 128 85 | 95; 256 151 | 157)
+    g.down_mt = each >= 56 && each <= 80 ? 4 : 2;
+    g.up_groups = (int)(g.up_mt == 2 ? (blocks + 7) / 8 : blocks / 4);
+    // with few items the tile kernel leaves CUs idle
+    g.up_tiles = !g.few && met * (each / (16 * g.up_mt) + 1) * g.up_groups >= 80;
     const auto units = [&](int64_t columns) {
         const int64_t most = slots < experts ? slots : experts + slots / columns;
         return most < slots ? most : slots;
     };
-    const size_t scratch = g.few ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
+    // Up to 64 slots: the down kernel's workgroups, one for each 16 columns, read inter of each expert met at some
+    // 30 GB/s, the tile kernels' together at 5.5 TB/s, but with a second list of the slots and a third launch,
+    // 6 us (seven tokens of 7 in 60 experts, hidden 512, inter 7936: 72 us for 15 + 5; hidden 2048, inter 768,
+    // eight tokens of 8 in 128: 17 us for 11 + 5)
+    const double read = (double)met * (double)a.e.inter * 8.5;   // bytes of 16 columns
+    g.few_down = g.few && read / 30e3 < read * (double)(a.e.hidden / 16) / 5.5e6 + 6.0;
+    const size_t scratch = g.few && g.few_down ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
     const auto at = [&](int64_t bytes) { return (size_t)bytes > scratch ? (size_t)bytes : scratch; };
     // as many workgroups of the tile kernels as the CUs hold at once: each lists the slots only once
     const auto grid = [&](int64_t groups, int64_t room) { return (unsigned)(groups < room ? groups : room); };
     if (g.up_tiles) {
-        g.up = grid(units(16 * g.mt) * g.up_groups, 2 * cus);
-        g.up_at = at(2 * 16 * g.mt * 128 * up_steps(g.mt));
+        g.up = grid(units(16 * g.up_mt) * g.up_groups, 2 * cus);
+        g.up_at = at(2 * 16 * g.up_mt * 512);
     } else {
         const int64_t items = units(16) * blocks, steps = a.e.hidden / 128;
-        // K parts while the workgroups are no more than the CUs, and so many that a wave has eight steps (one
-        // token of eight experts, hidden 2048: 14.7, 11.2, 7.7 and 5.9 us with 1, 2, 4 and 8; hidden 4096, four
-        // tokens of two large experts: 35 us with 1, 31 with 4, 37 with 8)
+        // K parts while there is about a workgroup for each CU, and four where a wave would have eight steps or more
+        // (microseconds with 1, 2, 4 and 8: hidden 2048, one token of eight experts 14.4, 10.9, 10.2, 5.9, four
+        // 15.5, 12.3, 13.4, 12.9, eight 18.5, 22.0, 19.9, 20.6; hidden 2688, 73 workgroups 24.4, 17.9, 12.9,
+        // 12.5; hidden 4096, 256 workgroups 37, 46, 32, 37)
         g.kw = 1;
-        while (2 * g.kw <= 8 && 2 * g.kw <= steps && (items * 2 * g.kw <= 8 * cus || 16 * g.kw <= steps)) g.kw *= 2;
+        while (g.kw < 8 && 2 * g.kw <= steps && (items * 2 * g.kw <= 9 * cus || (steps >= 32 && g.kw < 4))) g.kw *= 2;
         const int64_t groups = (items * g.kw + 7) / 8;
         g.up = (unsigned)(groups < 3 * cus ? groups : 3 * cus);
         g.up_at = at(g.kw > 1 ? 8 * 4 * 1024 : 0);
     }
-    if (g.few) {
+    if (g.few_down) {
         g.down = (unsigned)(a.e.hidden / 16);
         g.rows = (int)(16 * slots);
         g.down_at = (size_t)g.rows * 64 + (size_t)slots * 4;
@@ -996,8 +1000,8 @@ MoeGrid moe_grid(const MoeArgs& a) {
         g.ks = 1;   // 2 or 4 where there are too few units for the CUs, within moe_sum_rows
         while (g.ks < 4 && 2 * g.ks * met * down_groups <= 2 * cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k)
             g.ks *= 2;
-        g.down = grid(units(16 * g.mt) * down_groups * g.ks, g.mt == 8 ? cus : 2 * cus);
-        g.down_at = at(2 * 16 * g.mt * (512 + 16));
+        g.down = grid(units(16 * g.down_mt) * down_groups * g.ks, 2 * cus);
+        g.down_at = at(2 * 16 * g.down_mt * (512 + 16));
         g.join = (unsigned)((a.tokens * (a.e.hidden / 4) + 255) / 256);
     }
     return g;
@@ -1020,23 +1024,18 @@ hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
     if (g.few) return launch_one(up_kernel<true>, g.up, 1, kUpThreads, g.up_at, stream, a);
     const size_t bytes = g.up_at + sizeof(MoePlan);
     if (!g.up_tiles) return launch_one(up_kernel<false>, g.up, g.chunks, kUpThreads, bytes, stream, a);
-    switch (g.mt) {
-        case 2: return launch_one(up_tile_kernel<4, 2, 2, up_steps(2), 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
-        case 4: return launch_one(up_tile_kernel<2, 4, 2, up_steps(4), 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
-        default: return launch_one(up_tile_kernel<2, 8, 2, up_steps(8), 4>, g.up, g.chunks, kTileThreads, bytes, stream, a);
-    }
+    return g.up_mt == 2 ? launch_one(up_tile_kernel<4, 2, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a)
+                        : launch_one(up_tile_kernel<2, 4, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
 }
 
 template <int MT>
 hipError_t launch_down_tiles(const MoeGrid& g, const DownTileArgs& a, hipStream_t stream) {
-    return launch_one(down_tile_kernel<MT, 4, 4, MT == 2 ? 4 : 2>, g.down, g.chunks, kTileThreads, g.down_at + sizeof(MoePlan), stream, a);
+    return launch_one(down_tile_kernel<MT, 4, MT == 2 ? 4 : 2>, g.down, g.chunks, kTileThreads, g.down_at + sizeof(MoePlan), stream, a);
 }
 hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStream_t stream) {
-    if (g.few) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
+    if (g.few_down) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
     const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, Divisor((a.m.hidden / 16 + 15) / 16 * g.ks), (int)g.down_at};
-    const hipError_t e = g.mt == 2   ? launch_down_tiles<2>(g, d, stream)
-                         : g.mt == 4 ? launch_down_tiles<4>(g, d, stream)
-                                     : launch_down_tiles<8>(g, d, stream);
+    const hipError_t e = g.down_mt == 2 ? launch_down_tiles<2>(g, d, stream) : launch_down_tiles<4>(g, d, stream);
     return e != hipSuccess ? e : launch_one(join_kernel, g.join, 1, 256, 0, stream, d);
 }
 
