@@ -713,8 +713,11 @@ typedef enum { W4A8_ACT_SILU = 0, W4A8_ACT_GELU_TANH = 1 } w4a8_act;
  * d_x_scale fp32 [tokens]).  Products accumulate in fp32; the sum over j is fp32 in the order
  * of j, so that results do not depend on timing.  A slot whose id lies outside
  * [0, experts) is left out, its weight not looked at; a token without experts gives
- * zeros; the same expert twice counts twice.  Two kernels, nothing allocated, no atomics on
- * device memory.  Made for few tokens: every expert met is read once per 2048 / top_k tokens.
+ * zeros; the same expert twice counts twice.  Two or three kernels, nothing allocated, no atomics
+ * on device memory; which kernels depends on the sizes, and with them the last bits of a
+ * token's result on how many tokens are beside it.  Made for up to some hundreds of tokens
+ * per expert: an expert's weights are read once for every 32 or 64 of its slots, and anew for
+ * each 2048 / top_k tokens.
  * d_ws: w4a8_moe_workspace_bytes(...) bytes, 256-byte aligned, contents of no meaning between
  * calls; one sized for more tokens * top_k of the same hidden and inter serves fewer.  top_k from 1
  * to 32 and to experts, tokens * top_k < 2^30, at most 2^15 * (2048 / top_k) tokens (else

@@ -1,5 +1,8 @@
 """GPU: the calls of the expert half of a layer as they follow each other, on other streams, in
-captured graphs, and the measured cases at their own sizes."""
+captured graphs, the example, and the measured cases at their own sizes."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -142,6 +145,17 @@ def test_calls_on_two_streams(layer):
 
 
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24, torch.float8_e4m3fn: 2.0 ** -4}
+
+
+def test_the_layer_example():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_layer.py")
+    spec = importlib.util.spec_from_file_location("moe_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    say("expert block example")
+    # v is rounded to e4m3, at most 2^-4 of each value, errors of either sign over all of inter
+    assert example.main() < 2 ** -4
+    assert example.main(hidden=384, inter=640, experts=8, top_k=2, prompt=300, batch=40) < 2 ** -4
 
 
 @pytest.mark.parametrize("case", ops.listed(), ids=lambda c: c["name"])

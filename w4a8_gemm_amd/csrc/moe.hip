@@ -1,28 +1,33 @@
-// moe.hip -- a mixture of experts' gated products on MXFP4 weights, two kernels.
+// moe.hip -- a mixture of experts' gated products on MXFP4 weights.
 //
 //   g, u = x W_up[e]^T (halves),  v = act(g) u,  out[t] = sum_j w[t, j] v[t, j] W_down[e]^T
 //
-// with few tokens per expert: both products read each weight of the experts met once
-// and are bound by that.  The weights are in the fragment order of the prepared
-// linears (gemm_prepared.hip), so a wave's 16-row tile of 128 k is one 1 KiB load and
-// the e2m1 operand of one block-scaled 16x16x128 product; the activations of up to 16
-// tokens are its e4m3 operand, read from the cache as they are (their rows are
-// gathered, no copy in LDS: a tile's 2 KiB meet its 4 or 1 KiB of weights).
+// with up to some hundreds of tokens per expert: both products read each weight of the experts
+// met, and are bound by that, not by the matrix instructions (8 experts, hidden 4096, inter 8192: their 428 MB
+// take 69 us at 6.2 TB/s, the products of 502 slots 29 us at 3.5 PFLOP/s).  The weights are in the
+// fragment order of the prepared linears (gemm_prepared.hip), so a wave's 16-row tile of 128 k is one
+// 1 KiB load and the e2m1 operand of one block-scaled 16x16x128 product, whose e4m3 operand is 16 slots'
+// activations (a slot: token t, j).
 //
-// Between the products v is held as e4m3 with a power of two per 32 values, which the
-// matrix instruction takes as the operand's scale: a scale per token would need the
-// maximum over all of inter, which no workgroup of the first kernel sees.
+// Between the products v is held as e4m3 with a power of two per 32 values, which the matrix
+// instruction takes as the operand's scale: a scale per token would need the maximum over
+// all of inter, which no workgroup of the first product sees.
 //
-// Slots (token t, j), at most 2048 at a time (more tokens: more chunks in the same
-// launches), are listed by expert in LDS by every workgroup; runs of up to 16 MT
-// slots of one expert are the units of both kernels.  A unit's slots are the columns of
-// its products; which column a slot takes has no influence on its result.
+// Slots, at most 2048 at a time (more tokens: more chunks in the same launches), are listed by
+// expert by every workgroup itself, which spares a launch and the wait for it; runs of slots of one expert
+// are the units of all kernels.  A unit's slots are the columns of its products; which column a
+// slot takes has no influence on its result, but the kernel does, by roundings, and so do
+// the sizes that choose it.
 //
-//   up    an item is a unit and 32 of inter (two tiles each of gate and up rows), its
-//         K shared by KW waves and joined in LDS; v's blocks of 32 are then whole in a wave
-//   down  a workgroup per 16 columns of the output, its waves over the units (and parts
-//         of K where units are few); every slot's 16 partial sums meet in LDS, and are
-//         added in the order of j: no atomics, no third kernel
+//                    up to 64 slots                          more
+//   first product    up_kernel<true>, the list in registers  up_tile_kernel, the columns in LDS, or, with few
+//                                                            items, up_kernel<false>, which splits K over waves
+//   second product   down_kernel: a workgroup per 16         down_tile_kernel: a unit and 256 columns of the output
+//                    columns has all slots' partial sums      to a workgroup, partial sums to device memory;
+//                    in LDS and adds them                     join_kernel adds them (also for few slots, where
+//                                                             inter is long and hidden short)
+//
+// The partial sums of a token are added in the order of j, K parts of a slot first: no atomics.
 #include <type_traits>
 
 #include "w4a8_internal.h"
@@ -345,8 +350,14 @@ __device__ __forceinline__ void store_v(const MoeShape& m, const v4f (&r)[4], fl
     if (g == 0) store_power(m, top, row, blk);
 }
 
-// WAVE: up to 64 slots, listed by every wave; else listed in LDS.  Two steps in flight, two workgroups
-// to a CU.
+// An item is a unit of 16 slots and 32 of inter, two tiles each of the gate's and the up rows, so that v's
+// blocks of 32 are whole in a wave; kw waves share its K and are joined in LDS.  The columns are read from the
+// cache as they are, gathered, no copy in LDS.
+//
+// WAVE: up to 64 slots, listed by every wave; else listed in LDS.  Bound by how many bytes a CU has under way:
+// two steps of 5 KiB to a wave, two workgroups to a CU, of the registers that the widening leaves (one token
+// of eight experts, hidden 2048, inter 768: 13 MB in 5.9 us, of which 3 are the start, the list and the first loads' way;
+// eight tokens, 58 experts: 97 MB in 18.5 us, 5.2 TB/s).
 template <bool WAVE>
 __global__ __launch_bounds__(kUpThreads, 4) void up_kernel(UpArgs a) {
     constexpr int D = 2;
@@ -452,7 +463,10 @@ struct DownStep {
     uint32_t e;
 };
 
-// Up to 64 slots.  Six steps in flight.
+// Up to 64 slots.  A workgroup has 16 columns of the output and all slots: no partial sum leaves the CU, and no
+// third launch is needed.  Its waves take the units, or K parts of them where units are few; six steps in
+// flight.  Bound like the first product (one token of eight experts: 5.4 us; eight tokens, 58 experts:
+// 48 MB in 17.4 us, as the 128 workgroups of hidden 2048 fill half the CUs).
 __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
     constexpr int D = 6, kWaves = kDownThreads / 64;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -655,7 +669,10 @@ struct Tiles {
 
 // R = 4: a wave takes 32 of inter, two tiles each of the gate's and the up rows; R = 2: 16 of inter, one
 // of each, the waves of a pair agreeing on their block's largest value through LDS.  R = 2 leaves
-// registers for more columns.
+// registers for more columns (four sums of four tiles and two steps of weights are the 128 that two
+// workgroups to a CU leave a wave).  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 213 MB in 37 us,
+// 5.7 TB/s; 8 experts, hidden 4096, inter 8192, 63 slots each: 285 MB in 64 to 76 us, 3.8 to 4.4 TB/s, by how many
+// experts have more than 64 slots.
 template <int R, int MT, int D>
 __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -770,7 +787,9 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
 }
 
 // The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
-// device memory.
+// device memory: fp32, as the sum over the slots that follows is of terms of both signs.  A wave has two tiles of
+// output columns.  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 107 MB in 21 us, 5.1 TB/s; 8 experts,
+// hidden 4096, inter 8192: 143 MB in 46 to 53 us.
 template <int MT, int D, int WAVES>
 __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTileArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -884,7 +903,8 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
     }
 }
 
-// out from the partial sums: four columns of a token to a thread, its slots in order
+// out from the partial sums: four columns of a token to a thread, its slots in order.  They come from the L2
+// that the last kernel left them in, or from memory (512 x 2048: 3 us; 502 x 4096: 8 us, of which 3 are the launch).
 __global__ __launch_bounds__(256) void join_kernel(DownTileArgs a) {
     const MoeShape& m = a.m;
     const int64_t quads = m.hidden / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;

@@ -129,8 +129,9 @@ def moe_mxfp4(x_fp8: torch.Tensor, x_scale: torch.Tensor, ids: torch.Tensor, wei
     as bf16 [tokens, hidden], for the fp8 activations of quant_act_fp8_per_token or residual_norm
     (codes uint8 [tokens, hidden], scales [tokens]) and moe_route's ids and weights
     [tokens, top_k].  An id outside the experts, as -1 for padding or for an expert of another
-    GPU, is left out.  act: "silu" or "gelu_tanh".  Made for few tokens: the experts met are read
-    once for every 2048 / top_k of them.  Without a workspace one is allocated for the call."""
+    GPU, is left out.  act: "silu" or "gelu_tanh".  Made for up to some hundreds of tokens per expert: an
+    expert's weights are read once for every 32 or 64 of its slots, anew for each 2048 / top_k
+    tokens.  Without a workspace one is allocated for the call."""
     if not isinstance(experts, ExpertsMXFP4):
         raise TypeError("experts must be an ExpertsMXFP4")
     if workspace is not None and not isinstance(workspace, MoEWorkspace):
