@@ -53,7 +53,10 @@ SHAPES = [(1, 1, 1, 128, 128), (1, 8, 2, 256, 384), (1, 8, 8, 1152, 640), (3, 5,
           (2, 1024, 32, 128, 128), (5, 64, 6, 512, 896), (33, 8, 2, 2048, 1408), (64, 1, 1, 128, 1152), (300, 3, 3, 256, 128),
           (40, 1, 1, 640, 256), (2049, 3, 1, 128, 128), (15, 16, 1, 256, 256), (16, 60, 4, 256, 2048), (4, 40, 2, 4096, 128),
           (70, 1, 1, 128, 8192), (300, 1, 1, 256, 4096), (513, 2, 2, 128, 2048), (140, 3, 1, 1152, 1152), (260, 8, 2, 640, 2176),
-          (90, 30, 4, 384, 1152), (150, 1, 1, 5120, 128)]
+          (90, 30, 4, 384, 1152), (150, 1, 1, 5120, 128),
+          # many experts with few slots each; few slots and a long inter; the widest
+          (40, 1024, 8, 128, 128), (200, 1024, 8, 128, 128), (1, 8, 8, 128, 2816), (7, 9, 7, 128, 3968), (64, 8, 1, 128, 2944),
+          (8, 4, 2, 128, 8192), (3, 2, 2, 65536, 128), (3, 2, 1, 128, 65536), (70, 2, 1, 65536, 128), (70, 2, 1, 128, 65536)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
@@ -140,7 +143,7 @@ def test_outputs_workspaces_and_rows_behind():
 
 @pytest.mark.parametrize("tokens,experts,top_k,hidden,inter", [
     (70, 1, 1, 128, 8192), (65, 2, 1, 256, 16384), (300, 2, 1, 128, 8192), (64, 4, 1, 128, 128), (2, 33, 32, 128, 128),
-    (1000, 4, 3, 128, 512), (9, 8, 8, 384, 1152)])
+    (1000, 4, 3, 128, 512), (9, 8, 8, 384, 1152), (3, 8, 8, 128, 2816), (8, 4, 2, 128, 8192)])
 def test_nothing_is_written_past_the_workspace(tokens, experts, top_k, hidden, inter):
     say("moe_mxfp4 end of the workspace", tokens, experts, top_k, hidden, inter)
     c = Case(tokens, experts, top_k, hidden, inter)

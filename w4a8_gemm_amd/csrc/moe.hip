@@ -60,7 +60,7 @@ __device__ __forceinline__ v4f product(v8i w, v8i x, v4f c, uint32_t sw, uint32_
 struct alignas(16) MoePlan {
     uint16_t list[kMoeSlots];           // slots (of the chunk) by expert, in order
     uint32_t unit[kMoeSlots];           // first place | (slots - 1) << 11 | expert << 18
-    float scale[2][128];                // token scales of a unit's columns, of every other item
+    float scale[2][64];                 // token scales of a unit's columns, of every other item
     uint32_t part[16];
     int units;
 };
@@ -82,7 +82,7 @@ __device__ __forceinline__ uint64_t equal_lanes(int id, int experts) {
 // LDS that make_plan works in: how many slots of each 64 each expert has, and their first places
 size_t plan_scratch(int64_t slots, int64_t experts) { return (size_t)(((slots + 63) / 64 + 2) * ((experts + 3) / 4 * 4)); }
 
-// All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 128).  Slots keep their
+// All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 64).  Slots keep their
 // order within an expert, so that all workgroups agree on the units: each wave ranks 64 slots
 // by the equal ids before them, and the counts of the 64s are summed up for each expert.  No
 // atomics.
