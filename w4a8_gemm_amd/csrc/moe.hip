@@ -640,7 +640,7 @@ __device__ __forceinline__ void hold(v4f (&acc)[Q][MT]) {
 }
 
 // R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk
-template <int R, int D>
+template <int R, int D, int HINT>
 struct Tiles {
     __amdgpu_buffer_rsrc_t w[R], s[R];
     uint4 q[D][R];
@@ -653,7 +653,7 @@ struct Tiles {
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            q[to][r] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w[r], 16 * lane, step * 1024, kOnce));
+            q[to][r] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w[r], 16 * lane, step * 1024, HINT));
     }
     __device__ __forceinline__ void load_scales(int chunk) {
         const int lane = threadIdx.x & 63;
@@ -671,9 +671,9 @@ struct Tiles {
 // of each, the waves of a pair agreeing on their block's largest value through LDS.  R = 2 leaves
 // registers for more columns (four sums of four tiles and two steps of weights are the 128 that two
 // workgroups to a CU leave a wave).  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 213 MB in 37 us,
-// 5.7 TB/s; 8 experts, hidden 4096, inter 8192, 63 slots each: 285 MB in 64 to 76 us, 3.8 to 4.4 TB/s, by how many
+// 5.7 TB/s; 8 experts, hidden 4096, inter 8192, 63 slots each: 285 MB in 65 to 73 us, 3.9 to 4.4 TB/s, by how many
 // experts have more than 64 slots.
-template <int R, int MT, int D>
+template <int R, int MT, int D, int HINT>
 __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int kBuf = 16 * MT * 512;
@@ -706,7 +706,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
         st.load(x, row, 0, (int)m.hidden);
         float sx = 0.0f;
         if ((int)threadIdx.x < cols) sx = a.xs[t0 + m.by_top_k.quotient(p.list[first + threadIdx.x])];
-        Tiles<R, D> w;
+        Tiles<R, D, HINT> w;
 #pragma unroll
         for (int q = 0; q < R; ++q)
             w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), chunks);
@@ -789,8 +789,8 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
 // The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
 // device memory: fp32, as the sum over the slots that follows is of terms of both signs.  A wave has two tiles of
 // output columns.  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 107 MB in 21 us, 5.1 TB/s; 8 experts,
-// hidden 4096, inter 8192: 143 MB in 46 to 53 us.
-template <int MT, int D, int WAVES>
+// hidden 4096, inter 8192: 143 MB in 40 to 45 us.
+template <int MT, int D, int WAVES, int HINT>
 __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTileArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int kCols = 16 * MT * 512, kBuf = kCols + 16 * MT * 16;   // columns, then their exponents
@@ -825,7 +825,7 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
         u32x4 er{};
         st.load(x, row, c0, (int)m.inter);
         if (has_e) er = exponents(ep, c0, steps);
-        Tiles<2, D> w;
+        Tiles<2, D, HINT> w;
 #pragma unroll
         for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, chunks);
         w.load_scales(c0);
@@ -904,7 +904,7 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
 }
 
 // out from the partial sums: four columns of a token to a thread, its slots in order.  They come from the L2
-// that the last kernel left them in, or from memory (512 x 2048: 3 us; 502 x 4096: 8 us, of which 3 are the launch).
+// that the last kernel left them in, or from memory (512 x 2048: 4.4 us, 502 x 4096: 4.8, of which some 3 are the launch).
 __global__ __launch_bounds__(256) void join_kernel(DownTileArgs a) {
     const MoeShape& m = a.m;
     const int64_t quads = m.hidden / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -950,6 +950,7 @@ int64_t moe_sum_rows(int64_t slots) { return slots >= kSumRows ? slots : 4 * slo
 struct MoeGrid {
     bool few, few_down, up_tiles;   // few: up to 64 slots
     int up_mt, down_mt;             // column tiles of the tile kernels' units
+    bool up_shared, down_shared;    // several units of an expert read its weights
     int kw, rows, ks, up_groups;
     unsigned up, down, join, chunks;
     size_t up_at, down_at;          // LDS of the kernels before the plan
@@ -969,16 +970,20 @@ MoeGrid moe_grid(const MoeArgs& a) {
     g.few = slots <= kWaveSlots;
     // The first product: units of 64 slots and 16 of inter to a wave, which are more items for the same weights,
     // or of 32 slots and 32 of inter, whose columns are read and staged half as often.  Microseconds (32 | 64) by
-    // tiles (16 of inter of an expert that is met) and slots of an expert: 1024 tiles, 6 slots 14.9 | 12.8;
-    // 3900, 1 22.4 | 24.0; 4096, 6 16.8 | 18.1; 4400, 1 21.4 | 23.3; 5400, 2 37.4 | 35.4; 6100, 4 40.2 | 37.0;
-    // 704, 47 19.0 | 13.9; 2048, 25 41.2 | 34.9; 4096, 16 54.0 | 51.3; 4096, 128 163 | 145.
+    // tiles (16 of inter of an expert that is met) and slots of an expert: 1024 tiles, 6 slots 14.7 | 12.9;
+    // 3900, 1 23.1 | 24.7; 4096, 6 16.3 | 18.2; 4400, 1 21.2 | 23.4; 5400, 2 36.4 | 35.3; 6100, 4 38.6 | 36.5;
+    // 704, 47 17.6 | 14.1; 2048, 25 41.7 | 35.6; 4096, 16 54.1 | 51.3; 4096, 128 158 | 113.
     // (Units of 128: 77 to 94 us for 74 to 76 with 8 experts, 63 slots each, hidden 4096, inter 8192.)
     const int64_t tiles_up = met * (a.e.inter / 16);
     g.up_mt = each < 8 && tiles_up > 2048 && tiles_up < 4800 ? 2 : 4;
     // The second product, units of 32 or 64: the wider where they take an expert's slots in one for two or
-    // three (slots of an expert, 32 | 64: 16 27.6 | 33.6; 45 7.5 | 8.6; 50 25.9 | 26.9; 62 42.3 | 37.8; 63 55 | 47;
-    // 128 85 | 95; 256 151 | 157)
+    // three (slots of an expert, 32 | 64: 16 31.5 | 30.9; 45 8.8 | 8.3, the call 30.1 | 31.7; 50 13.2 | 14.9;
+    // 62 38.6 | 36.8; 63 53 | 44; 128 69 | 74; 256 110 | 113)
     g.down_mt = each >= 56 && each <= 80 ? 4 : 2;
+    // Weights that several units read are left in the caches, the others' loads have the hint (hidden 4096,
+    // inter 8192, 8 experts, both products, with | without: 63 slots of an expert 127 | 117; 128 223 | 178; 128
+    // experts, 4 slots each, hidden 2048, inter 768: 61 | 67)
+    g.up_shared = each >= 48, g.down_shared = each >= 24;
     g.up_groups = (int)(g.up_mt == 2 ? (blocks + 7) / 8 : blocks / 4);
     // with few items the tile kernel leaves CUs idle
     g.up_tiles = !g.few && met * (each / (16 * g.up_mt) + 1) * g.up_groups >= 80;
@@ -1016,9 +1021,12 @@ MoeGrid moe_grid(const MoeArgs& a) {
         g.rows = (int)(16 * slots);
         g.down_at = (size_t)g.rows * 64 + (size_t)slots * 4;
     } else {
-        const int64_t chunks_k = (a.e.inter + 511) / 512;
-        g.ks = 1;   // 2 or 4 where there are too few units for the CUs, within moe_sum_rows
-        while (g.ks < 4 && 2 * g.ks * met * down_groups <= 2 * cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k)
+        // 2 or 4 parts of K, within moe_sum_rows, while items are fewer than the CUs: parts cost their partial sums
+        // (microseconds of the call with 1, 2 and 4: 32 items, inter 8192 53, 44, 42; 60, 7936 57, 50, 50; 128, 4096
+        // 42, 45, 46; 128, 8192 92, 93, 94, and with units of 64 136, 142, 157)
+        const int64_t chunks_k = (a.e.inter + 511) / 512, items = met * (each / (16 * g.down_mt) + 1) * down_groups;
+        g.ks = 1;
+        while (g.ks < 4 && 2 * g.ks * items < cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k)
             g.ks *= 2;
         g.down = grid(units(16 * g.down_mt) * down_groups * g.ks, 2 * cus);
         g.down_at = at(2 * 16 * g.down_mt * (512 + 16));
@@ -1044,18 +1052,19 @@ hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
     if (g.few) return launch_one(up_kernel<true>, g.up, 1, kUpThreads, g.up_at, stream, a);
     const size_t bytes = g.up_at + sizeof(MoePlan);
     if (!g.up_tiles) return launch_one(up_kernel<false>, g.up, g.chunks, kUpThreads, bytes, stream, a);
-    return g.up_mt == 2 ? launch_one(up_tile_kernel<4, 2, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a)
-                        : launch_one(up_tile_kernel<2, 4, 2>, g.up, g.chunks, kTileThreads, bytes, stream, a);
+    return launch_one(g.up_mt == 2   ? up_tile_kernel<4, 2, 2, kOnce>
+                      : g.up_shared ? up_tile_kernel<2, 4, 2, 0>
+                                    : up_tile_kernel<2, 4, 2, kOnce>,
+                      g.up, g.chunks, kTileThreads, bytes, stream, a);
 }
 
-template <int MT>
-hipError_t launch_down_tiles(const MoeGrid& g, const DownTileArgs& a, hipStream_t stream) {
-    return launch_one(down_tile_kernel<MT, 4, MT == 2 ? 4 : 2>, g.down, g.chunks, kTileThreads, g.down_at + sizeof(MoePlan), stream, a);
-}
 hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStream_t stream) {
     if (g.few_down) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
     const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, Divisor((a.m.hidden / 16 + 15) / 16 * g.ks), (int)g.down_at};
-    const hipError_t e = g.down_mt == 2 ? launch_down_tiles<2>(g, d, stream) : launch_down_tiles<4>(g, d, stream);
+    const hipError_t e = launch_one(g.down_mt == 4     ? down_tile_kernel<4, 4, 2, 0>
+                                    : g.down_shared ? down_tile_kernel<2, 4, 4, 0>
+                                                    : down_tile_kernel<2, 4, 4, kOnce>,
+                                    g.down, g.chunks, kTileThreads, g.down_at + sizeof(MoePlan), stream, d);
     return e != hipSuccess ? e : launch_one(join_kernel, g.join, 1, 256, 0, stream, d);
 }
 
