@@ -102,11 +102,12 @@ def test_moe_refusals(L, kw, status):
 def test_workspace_bytes(L):
     b = L.w4a8_moe_workspace_bytes
     # one byte a value and an exponent byte for each of 32, in dwords of four steps; fp32 sums of the slots,
-    # up to four parts of each while there are no more than 2048 rows
-    assert b(1, 8, 2048, 768) == 8 * (768 + 32) + 32 * 2048 * 4
-    assert b(5, 2, 256, 512) == 10 * (512 + 16) + 40 * 256 * 4
-    assert b(500, 2, 256, 512) == 1000 * (512 + 16) + 2048 * 256 * 4
-    assert b(3000, 2, 256, 512) == 6000 * (512 + 16) + 6000 * 256 * 4
+    # up to four parts of each while there are no more than 2048 rows; the slots by expert, for each 2017 slots
+    plan = 2048 * 6 + 16
+    assert b(1, 8, 2048, 768) == 8 * (768 + 32) + 32 * 2048 * 4 + plan
+    assert b(5, 2, 256, 512) == 10 * (512 + 16) + 40 * 256 * 4 + plan
+    assert b(500, 2, 256, 512) == 1000 * (512 + 16) + 2048 * 256 * 4 + plan
+    assert b(3000, 2, 256, 512) == 6000 * (512 + 16) + 6000 * 256 * 4 + 3 * plan
     assert b(0, 2, 256, 512) == b(5, 0, 256, 512) == b(5, 33, 256, 512) == b(5, 2, 256, 64) == b(5, 2, 256, 130) == 0
     assert b(5, 2, 100, 512) == b(5, 2, 0, 512) == b(5, 2, 1 << 17, 512) == b(1 << 29, 2, 256, 128) == 0
     for t in (1, 7, 255, 300, 1023, 1024, 2000):

@@ -61,7 +61,13 @@ struct alignas(16) MoePlan {
     uint16_t list[kMoeSlots];           // slots (of the chunk) by expert, in order
     uint32_t unit[kMoeSlots];           // first place | (slots - 1) << 11 | expert << 18
     float scale[2][64];                 // token scales of a unit's columns, of every other item
-    uint32_t part[16];
+    uint32_t part[16];                  // of two sums over 512 threads
+    int units;
+};
+// what the first product's last workgroup leaves of it for the second, in the workspace
+struct alignas(16) StoredPlan {
+    uint32_t unit[kMoeSlots];           // with the second product's slots to a unit
+    uint16_t list[kMoeSlots];
     int units;
 };
 __device__ __forceinline__ int unit_first(uint32_t u) { return u & 2047; }
@@ -82,12 +88,35 @@ __device__ __forceinline__ uint64_t equal_lanes(int id, int experts) {
 // LDS that make_plan works in: how many slots of each 64 each expert has, and their first places
 size_t plan_scratch(int64_t slots, int64_t experts) { return (size_t)(((slots + 63) / 64 + 2) * ((experts + 3) / 4 * 4)); }
 
+// sum of v over the threads before this one, and over all NT; `part` is this sum's own words of LDS
+template <int NT>
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* part, uint32_t& all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t incl = v;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t w = __shfl_up(incl, off);
+        if (lane >= off) incl += w;
+    }
+    if (lane == 63) part[wave] = incl;
+    __syncthreads();
+    uint32_t before = incl - v;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) {
+        const uint32_t w = part[i];
+        if (i < wave) before += w;
+        all += w;
+    }
+    return before;
+}
+
 // All NT threads; `slots` of the chunk, its ids; US: slots to a unit (at most 64).  Slots keep their
 // order within an expert, so that all workgroups agree on the units: each wave ranks 64 slots
 // by the equal ids before them, and the counts of the 64s are summed up for each expert.  No
-// atomics.
+// atomics.  `out`, where given: also for units of out_us slots.
 template <int NT, int US>
-__device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int slots, int experts) {
+__device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int slots, int experts, StoredPlan* out, int out_us) {
     constexpr int kPer = kMoeSlots / NT, kExp = kMaxExperts / NT;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int e4 = (experts + 3) / 4 * 4, lots = (slots + 63) / 64;
@@ -123,17 +152,23 @@ __device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int 
         mine[i] = c | ((c + US - 1) / US) << 16;
         sum += mine[i];
     }
-    uint32_t incl = sum;
+    uint32_t all;
+    uint32_t before = sum_before<NT>(sum, p.part, all);
+    if (tid == 0) p.units = (int)(all >> 16);
+    if (out) {   // the same for all threads
+        uint32_t mine_out = 0;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const uint32_t v = __shfl_up(incl, off);
-        if (lane >= off) incl += v;
+        for (int i = 0; i < kExp; ++i) mine_out += ((mine[i] & 0xFFFFu) + out_us - 1) / out_us;
+        uint32_t u = sum_before<NT>(mine_out, p.part + NT / 64, all), at = before & 0xFFFFu;
+        if (tid == 0) out->units = (int)all;
+#pragma unroll
+        for (int i = 0; i < kExp; ++i) {
+            const int c = mine[i] & 0xFFFFu;
+            for (int k = 0; k < c; k += out_us, ++u)
+                out->unit[u] = (at + k) | (uint32_t)(min(c - k, out_us) - 1) << 11 | (uint32_t)(tid * kExp + i) << 18;
+            at += c;
+        }
     }
-    if (lane == 63) p.part[wave] = incl;
-    __syncthreads();
-    uint32_t before = incl - sum;
-    for (int i = 0; i < wave; ++i) before += p.part[i];
-    if (tid == NT - 1) p.units = (int)((before + sum) >> 16);
 #pragma unroll
     for (int i = 0; i < kExp; ++i) {
         const int e = tid * kExp + i, c = mine[i] & 0xFFFFu, at = before & 0xFFFFu;
@@ -151,6 +186,22 @@ __device__ void make_plan(MoePlan& p, uint8_t* scratch, const int32_t* ids, int 
         for (int l = 0; l < wave + i * (NT / 64); ++l) at += count[l * e4 + id[i]];
         p.list[at] = (uint16_t)(tid + i * NT);
     }
+    __syncthreads();
+    if (out)
+        for (int i = tid; i < (slots + 1) / 2; i += NT) reinterpret_cast<uint32_t*>(out->list)[i] = reinterpret_cast<uint32_t*>(p.list)[i];
+}
+
+// the plan as the first product left it: read in one round, units to the most that there can be
+template <int NT, int US>
+__device__ void read_plan(MoePlan& p, const StoredPlan& from, int slots, int experts) {
+    const int most = min(slots, experts + slots / US), lists = (slots + 7) / 8, units = (most + 3) / 4;
+    const int i = threadIdx.x;
+    uint4 list, unit;
+    if (i < lists) list = reinterpret_cast<const uint4*>(from.list)[i];
+    if (i < units) unit = reinterpret_cast<const uint4*>(from.unit)[i];
+    if (i == 0) p.units = from.units;
+    if (i < lists) reinterpret_cast<uint4*>(p.list)[i] = list;
+    if (i < units) reinterpret_cast<uint4*>(p.unit)[i] = unit;
     __syncthreads();
 }
 
@@ -222,6 +273,8 @@ struct UpArgs {
     int act, kw;
     Divisor by_blocks, by_kw;           // items of a unit; K parts
     int plan_at;                        // of the plan in LDS; before it the kernel's own, and the plan's making
+    StoredPlan* plans;                  // of each chunk, for the second product
+    int plan_slots;                     // to a unit of it
 };
 struct DownArgs {
     MoeShape m;
@@ -241,6 +294,7 @@ struct DownTileArgs {
     int ks;                             // K parts
     Divisor by_items;                   // items of a unit: K parts x groups of columns, the parts first
     int plan_at;
+    const StoredPlan* plans;
 };
 
 // ---------------------------------------------------------------------------
@@ -371,7 +425,8 @@ __global__ __launch_bounds__(kUpThreads, 4) void up_kernel(UpArgs a) {
     if constexpr (WAVE)
         list = wave_list(a.ids, slots, m.experts);
     else
-        make_plan<kUpThreads, 16>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
+        make_plan<kUpThreads, 16>(p, lds, a.ids + t0 * m.top_k, slots, m.experts,
+                                  blockIdx.x == gridDim.x - 1 ? a.plans + blockIdx.y : nullptr, a.plan_slots);
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int kw = a.kw, mine = a.by_kw.quotient(wave), part = wave - mine * kw, per_wg = 8 / kw;   // kw: 1, 2, 4 or 8
@@ -681,7 +736,8 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
-    make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
+    make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts,
+                                     blockIdx.x == gridDim.x - 1 ? a.plans + blockIdx.y : nullptr, a.plan_slots);
 
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const ColumnReader cr;
@@ -798,7 +854,7 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
-    make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts);
+    read_plan<kTileThreads, 16 * MT>(p, a.plans[blockIdx.y], slots, m.experts);
 
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const ColumnReader cr;
@@ -946,9 +1002,11 @@ int64_t exponent_stride(int64_t inter) { return (inter + 511) / 512 * 16; }
 // Rows of the partial sums: one for each slot, or for up to four K parts of them within kSumRows
 constexpr int64_t kSumRows = 2048;
 int64_t moe_sum_rows(int64_t slots) { return slots >= kSumRows ? slots : 4 * slots < kSumRows ? 4 * slots : kSumRows; }
+// Stored plans: of at least the chunks, which have 2048 / top_k tokens, 2017 slots or more
+int64_t moe_plans(int64_t slots) { return slots / 2017 + 1; }
 
 struct MoeGrid {
-    bool few, few_down, up_tiles;   // few: up to 64 slots
+    bool few, up_tiles;             // few: the kernels for up to 64 slots
     int up_mt, down_mt;             // column tiles of the tile kernels' units
     bool up_shared, down_shared;    // several units of an expert read its weights
     int kw, rows, ks, up_groups;
@@ -967,7 +1025,7 @@ MoeGrid moe_grid(const MoeArgs& a) {
     const int64_t met = (int64_t)((double)experts * (1.0 - missed) + 0.5);
     const int64_t blocks = a.e.inter / 32, down_groups = (a.e.hidden / 16 + 15) / 16;
     const int64_t each = slots / experts;   // slots of an expert, on average
-    g.few = slots <= kWaveSlots;
+    const bool small = slots <= kWaveSlots;
     // The first product: units of 64 slots and 16 of inter to a wave, which are more items for the same weights,
     // or of 32 slots and 32 of inter, whose columns are read and staged half as often.  Microseconds (32 | 64) by
     // tiles (16 of inter of an expert that is met) and slots of an expert: 1024 tiles, 6 slots 14.7 | 12.9;
@@ -986,7 +1044,7 @@ MoeGrid moe_grid(const MoeArgs& a) {
     g.up_shared = each >= 48, g.down_shared = each >= 24;
     g.up_groups = (int)(g.up_mt == 2 ? (blocks + 7) / 8 : blocks / 4);
     // with few items the tile kernel leaves CUs idle
-    g.up_tiles = !g.few && met * (each / (16 * g.up_mt) + 1) * g.up_groups >= 80;
+    g.up_tiles = !small && met * (each / (16 * g.up_mt) + 1) * g.up_groups >= 80;
     const auto units = [&](int64_t columns) {
         const int64_t most = slots < experts ? slots : experts + slots / columns;
         return most < slots ? most : slots;
@@ -996,8 +1054,8 @@ MoeGrid moe_grid(const MoeArgs& a) {
     // 6 us (seven tokens of 7 in 60 experts, hidden 512, inter 7936: 72 us for 15 + 5; hidden 2048, inter 768,
     // eight tokens of 8 in 128: 17 us for 11 + 5)
     const double read = (double)met * (double)a.e.inter * 8.5;   // bytes of 16 columns
-    g.few_down = g.few && read / 30e3 < read * (double)(a.e.hidden / 16) / 5.5e6 + 6.0;
-    const size_t scratch = g.few && g.few_down ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
+    g.few = small && read / 30e3 < read * (double)(a.e.hidden / 16) / 5.5e6 + 6.0;
+    const size_t scratch = g.few ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
     const auto at = [&](int64_t bytes) { return (size_t)bytes > scratch ? (size_t)bytes : scratch; };
     // as many workgroups of the tile kernels as the CUs hold at once: each lists the slots only once
     const auto grid = [&](int64_t groups, int64_t room) { return (unsigned)(groups < room ? groups : room); };
@@ -1016,7 +1074,7 @@ MoeGrid moe_grid(const MoeArgs& a) {
         g.up = (unsigned)(groups < 3 * cus ? groups : 3 * cus);
         g.up_at = at(g.kw > 1 ? 8 * 4 * 1024 : 0);
     }
-    if (g.few_down) {
+    if (g.few) {
         g.down = (unsigned)(a.e.hidden / 16);
         g.rows = (int)(16 * slots);
         g.down_at = (size_t)g.rows * 64 + (size_t)slots * 4;
@@ -1029,7 +1087,7 @@ MoeGrid moe_grid(const MoeArgs& a) {
         while (g.ks < 4 && 2 * g.ks * items < cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k)
             g.ks *= 2;
         g.down = grid(units(16 * g.down_mt) * down_groups * g.ks, 2 * cus);
-        g.down_at = at(2 * 16 * g.down_mt * (512 + 16));
+        g.down_at = (size_t)(2 * 16 * g.down_mt * (512 + 16));
         g.join = (unsigned)((a.tokens * (a.e.hidden / 4) + 255) / 256);
     }
     return g;
@@ -1058,9 +1116,9 @@ hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
                       g.up, g.chunks, kTileThreads, bytes, stream, a);
 }
 
-hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStream_t stream) {
-    if (g.few_down) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
-    const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, Divisor((a.m.hidden / 16 + 15) / 16 * g.ks), (int)g.down_at};
+hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, const StoredPlan* plans, hipStream_t stream) {
+    if (g.few) return launch_one(down_kernel, g.down, 1, kDownThreads, g.down_at, stream, a);
+    const DownTileArgs d{a.m, a.w, a.s, a.ids, a.weights, a.out, sums, g.ks, Divisor((a.m.hidden / 16 + 15) / 16 * g.ks), (int)g.down_at, plans};
     const hipError_t e = launch_one(g.down_mt == 4     ? down_tile_kernel<4, 4, 2, 0>
                                     : g.down_shared ? down_tile_kernel<2, 4, 4, 0>
                                                     : down_tile_kernel<2, 4, 4, kOnce>,
@@ -1070,9 +1128,9 @@ hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, hipStre
 
 }  // namespace
 
-// v's codes and exponents, then (16-byte aligned) the partial sums
+// v's codes and exponents, then (16-byte aligned) the partial sums and the plans
 size_t moe_workspace_bytes(int64_t slots, int64_t hidden, int64_t inter) {
-    return (size_t)(slots * (inter + exponent_stride(inter)) + moe_sum_rows(slots) * hidden * 4);
+    return (size_t)(slots * (inter + exponent_stride(inter)) + moe_sum_rows(slots) * hidden * 4) + (size_t)moe_plans(slots) * sizeof(StoredPlan);
 }
 
 int64_t moe_threads(const MoeArgs& a) {
@@ -1092,10 +1150,12 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
     m.e_stride = exponent_stride(a.e.inter);
     const int64_t slots = a.tokens * a.top_k;
     m.v = a.ws, m.ve = a.ws + slots * a.e.inter;
-    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(g.up_tiles ? g.up_groups : a.e.inter / 32), Divisor(g.up_tiles ? 1 : g.kw), 0}, stream);
+    float* sums = reinterpret_cast<float*>(m.ve + slots * m.e_stride);
+    StoredPlan* plans = reinterpret_cast<StoredPlan*>(sums + moe_sum_rows(slots) * a.e.hidden);
+    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(g.up_tiles ? g.up_groups : a.e.inter / 32),
+                                       Divisor(g.up_tiles ? 1 : g.kw), 0, plans, 16 * g.down_mt}, stream);
     if (e != hipSuccess) return e;
-    return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows},
-                       reinterpret_cast<float*>(m.ve + slots * m.e_stride), stream);
+    return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows}, sums, plans, stream);
 }
 
 }  // namespace w4a8
