@@ -716,7 +716,7 @@ typedef enum { W4A8_ACT_SILU = 0, W4A8_ACT_GELU_TANH = 1 } w4a8_act;
  * zeros; the same expert twice counts twice.  Two or three kernels, nothing allocated, no atomics
  * on device memory; which kernels depends on the sizes, and with them the last bits of a
  * token's result on how many tokens are beside it.  Made for up to some hundreds of tokens
- * per expert: an expert's weights are read once for every 32 or 64 of its slots, and anew for
+ * per expert: an expert's weights are read once for every 16 to 64 of its slots, and anew for
  * each 2048 / top_k tokens.
  * d_ws: w4a8_moe_workspace_bytes(...) bytes, 256-byte aligned, contents of no meaning between
  * calls; one sized for more tokens * top_k of the same hidden and inter serves fewer.  top_k from 1

@@ -14,8 +14,8 @@
 // all of inter, which no workgroup of the first product sees.
 //
 // Slots, at most 2048 at a time (more tokens: more chunks in the same launches), are listed by
-// expert by every workgroup itself, which spares a launch and the wait for it; runs of slots of one expert
-// are the units of all kernels.  A unit's slots are the columns of its products; which column a
+// expert by every workgroup of the first product itself (2 to 4 us), which spares a launch and the wait for it,
+// and read by the second's as the last one left them (1 us); runs of slots of one expert are the units of all kernels.  A unit's slots are the columns of its products; which column a
 // slot takes has no influence on its result, but the kernel does, by roundings, and so do
 // the sizes that choose it.
 //
@@ -844,8 +844,8 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
 
 // The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
 // device memory: fp32, as the sum over the slots that follows is of terms of both signs.  A wave has two tiles of
-// output columns.  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 107 MB in 21 us, 5.1 TB/s; 8 experts,
-// hidden 4096, inter 8192: 143 MB in 40 to 45 us.
+// output columns.  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 107 MB in 20 us, 5.3 TB/s; 8 experts,
+// hidden 4096, inter 8192: 143 MB in 39 to 44 us.
 template <int MT, int D, int WAVES, int HINT>
 __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTileArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -1050,8 +1050,8 @@ MoeGrid moe_grid(const MoeArgs& a) {
         return most < slots ? most : slots;
     };
     // Up to 64 slots: the down kernel's workgroups, one for each 16 columns, read inter of each expert met at some
-    // 30 GB/s, the tile kernels' together at 5.5 TB/s, but with a second list of the slots and a third launch,
-    // 6 us (seven tokens of 7 in 60 experts, hidden 512, inter 7936: 72 us for 15 + 5; hidden 2048, inter 768,
+    // 30 GB/s, the tile kernels' together at 5.5 TB/s, but with a list of the slots and a third launch, 6 us
+    // (seven tokens of 7 in 60 experts, hidden 512, inter 7936: 72 us for 15 + 5; hidden 2048, inter 768,
     // eight tokens of 8 in 128: 17 us for 11 + 5)
     const double read = (double)met * (double)a.e.inter * 8.5;   // bytes of 16 columns
     g.few = small && read / 30e3 < read * (double)(a.e.hidden / 16) / 5.5e6 + 6.0;

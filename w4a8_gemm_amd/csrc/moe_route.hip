@@ -3,7 +3,7 @@
 // A wave takes a token: lane L holds the experts L, L + 64, ...  Each round of the
 // choice takes the largest key of the wave (unsigned keys in the scores' order, so
 // a maximum is one instruction a step) and, of those that hold it, the lowest
-// expert: the lanes' equal keys as a 64-bit mask per held expert.
+// expert.
 //
 // Without bias and groups the choice goes by the logits themselves.  With them it
 // goes by scores in fp64: which expert a token meets should follow from the inputs,
@@ -33,10 +33,18 @@ __device__ __forceinline__ uint64_t key_of(double v) {
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) { return wave_reduce(v, Max()); }
-// the high halves first, then the low ones of the lanes that have the largest of these
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-    const uint32_t hi = wave_max((uint32_t)(v >> 32));
-    return (uint64_t)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+// the lanes that hold the largest key, which is not 0; none if all are.  The low halves are looked at only
+// where several lanes share the high one.
+__device__ __forceinline__ uint64_t lanes_of_max(uint64_t v) {
+    const uint32_t hi = (uint32_t)(v >> 32);
+    const uint32_t most = wave_max(hi);
+    uint64_t have = most ? __ballot(hi == most) : 0;
+    if (have & (have - 1)) {
+        const bool in = (have >> (threadIdx.x & 63)) & 1;
+        const uint32_t top = wave_max(in ? (uint32_t)v : 0u);
+        have = __ballot(in && (uint32_t)v == top);
+    }
+    return have;
 }
 
 __device__ __forceinline__ float exponential(float v) { return expf(v); }
@@ -102,56 +110,81 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
     }
     if constexpr (kByScore) {
         if (a.groups > 1) {
-            // lane g: the group's largest scores.  The wave's own lines: its LDS accesses are in order.
+            // 2^by lanes to a group: its largest scores.  The wave's own lines: its LDS accesses are in order.
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
-            const int size = a.experts / a.groups;
-            uint64_t group = 0;
-            if (lane < a.groups) {
-                double first = -__builtin_inf(), second = first;
+            const int size = a.experts / a.groups, by = __builtin_clz(a.groups - 1) - 26;
+            const int g = lane >> by;
+            double first = -__builtin_inf(), second = first;
+            if (g < a.groups)
 #pragma unroll 4
-                for (int i = 0; i < size; ++i) {
-                    const double v = line[wave][lane * size + i];
+                for (int i = lane & ((1 << by) - 1); i < size; i += 1 << by) {
+                    const double v = line[wave][g * size + i];
                     second = fmax(second, fmin(first, v));
                     first = fmax(first, v);
                 }
-                const double sum = a.group_top == 2 && size > 1 ? first + second : first;
-                // a group with too few experts is behind all others, but not behind nothing
-                group = sum > -__builtin_inf() ? key_of(sum) : 1;
+            for (int off = 1; off < 1 << by; off <<= 1) {
+                const double f = __shfl_xor(first, off), t = __shfl_xor(second, off);
+                second = fmax(fmin(first, f), fmax(second, t));
+                first = fmax(first, f);
             }
-            uint64_t kept = 0;
-            for (int j = 0; j < a.groups_kept; ++j) {
-                const uint64_t best = wave_max(group);
-                const int at = __builtin_ctzll(__ballot(group == best));
-                kept |= 1ull << at;
-                if (lane == at) group = 0;
+            const double sum = a.group_top == 2 && size > 1 ? first + second : first;
+            // a group with too few experts is behind all others
+            const uint64_t group = sum > -__builtin_inf() ? key_of(sum) : 0;
+            // its place: the groups that are better, or as good and before it
+            int place = 0;
+            for (int o = 0; o < a.groups; ++o) {
+                const uint64_t other = lane_value(group, o << by);
+                place += other > group || (other == group && o < g);
             }
+            const uint64_t best = __ballot(g < a.groups && place < a.groups_kept);   // a group's first lane speaks for it
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int e = lane + 64 * i;
-                if (e < a.experts && !((kept >> (e / size)) & 1)) key[i] = 0;
+                if (e < a.experts && !((best >> ((e / size) << by)) & 1)) key[i] = 0;
             }
         }
     }
     int id = -1;
     S mine = 0, sum = 0;
     for (int j = 0; j < a.top_k; ++j) {
-        Key best = 0;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) best = key[i] > best ? key[i] : best;
-        best = wave_max(best);
-        if (best == 0) break;   // the same in all lanes: nothing is left
         int at = -1;
         S w = 0;
+        if constexpr (kByScore) {
+            // a lane's largest, of equals the lowest expert; the lane, and of several the one with the lowest expert
+            Key best = 0;
+            int held = 0;
+            S value = 0;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            if (at >= 0) continue;
-            const uint64_t have = __ballot(key[i] == best);
-            if (!have) continue;
-            const int from = __builtin_ctzll(have);
-            at = 64 * i + from;
-            w = lane_value(p[i], from);
-            if (lane == from) key[i] = 0;
+            for (int i = 0; i < NL; ++i)
+                if (key[i] > best) best = key[i], held = i, value = p[i];
+            const uint64_t have = lanes_of_max(best);
+            if (have == 0) break;   // the same in all lanes: nothing is left
+            int from = __builtin_ctzll(have);
+            if (have & (have - 1)) from = ~wave_max((have >> lane) & 1 ? ~(uint32_t)(64 * held + lane) : 0u) & 63;
+            at = 64 * (int)lane_value((uint32_t)held, from) + from;
+            w = lane_value(value, from);
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                if (lane == from && held == i) key[i] = 0;
+        } else {
+            // one reduction, then the lanes that hold it, for each held expert (the other way 3.2 us for one
+            // token's eight of 128, this way 2.9 to 3.1)
+            Key best = 0;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) best = key[i] > best ? key[i] : best;
+            best = wave_max(best);
+            if (best == 0) break;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                if (at >= 0) continue;
+                const uint64_t have = __ballot(key[i] == best);
+                if (!have) continue;
+                const int from = __builtin_ctzll(have);
+                at = 64 * i + from;
+                w = lane_value(p[i], from);
+                if (lane == from) key[i] = 0;
+            }
         }
         sum += w;
         if (lane == j) id = at, mine = w;

@@ -25,10 +25,11 @@ __device__ __forceinline__ double swap_lanes(double v) {
 }
 __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
 __device__ __forceinline__ float lane_value(float v, int lane) { return __uint_as_float(lane_value(__float_as_uint(v), lane)); }
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+    return lane_value((uint32_t)v, lane) | (uint64_t)lane_value((uint32_t)(v >> 32), lane) << 32;
+}
 __device__ __forceinline__ double lane_value(double v, int lane) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint64_t lo = lane_value((uint32_t)b, lane), hi = lane_value((uint32_t)(b >> 32), lane);
-    return __builtin_bit_cast(double, lo | hi << 32);
+    return __builtin_bit_cast(double, lane_value(__builtin_bit_cast(uint64_t, v), lane));
 }
 
 // over each row of 16 lanes, in all of them

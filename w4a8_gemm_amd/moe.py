@@ -130,7 +130,7 @@ def moe_mxfp4(x_fp8: torch.Tensor, x_scale: torch.Tensor, ids: torch.Tensor, wei
     (codes uint8 [tokens, hidden], scales [tokens]) and moe_route's ids and weights
     [tokens, top_k].  An id outside the experts, as -1 for padding or for an expert of another
     GPU, is left out.  act: "silu" or "gelu_tanh".  Made for up to some hundreds of tokens per expert: an
-    expert's weights are read once for every 32 or 64 of its slots, anew for each 2048 / top_k
+    expert's weights are read once for every 16 to 64 of its slots, anew for each 2048 / top_k
     tokens.  Without a workspace one is allocated for the call."""
     if not isinstance(experts, ExpertsMXFP4):
         raise TypeError("experts must be an ExpertsMXFP4")
