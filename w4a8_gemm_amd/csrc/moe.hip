@@ -14,10 +14,11 @@
 // all of inter, which no workgroup of the first product sees.
 //
 // Slots, at most 2048 at a time (more tokens: more chunks in the same launches), are listed by
-// expert by every workgroup of the first product itself (2 to 4 us), which spares a launch and the wait for it,
-// and read by the second's as the last one left them (1 us); runs of slots of one expert are the units of all kernels.  A unit's slots are the columns of its products; which column a
-// slot takes has no influence on its result, but the kernel does, by roundings, and so do
-// the sizes that choose it.
+// expert by every workgroup of the first product itself (2 to 4 us), which spares a launch and the
+// wait for it, and read by the second's as the last one left them (1 us); runs of slots of one
+// expert are the units of all kernels.  A unit's slots are the columns of its products; which
+// column a slot takes has no influence on its result, but the kernel does, by roundings, and so
+// do the sizes that choose it.
 //
 //                    up to 64 slots                          more
 //   first product    up_kernel<true>, the list in registers  up_tile_kernel, the columns in LDS, or, with few
