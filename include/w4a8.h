@@ -710,12 +710,15 @@ typedef enum { W4A8_ACT_SILU = 0, W4A8_ACT_GELU_TANH = 1 } w4a8_act;
  *          inter, the least that keeps the 32 within 448 (at least 2^-127); a block with a NaN
  *          or infinite value is NaN
  * for activations as the linears take them (d_x_fp8 e4m3 [tokens][hidden], 16-byte aligned,
- * d_x_scale fp32 [tokens]).  Products accumulate in fp32; the sum over j is fp32 in the order
- * of j, so that results do not depend on timing.  A slot whose id lies outside
+ * d_x_scale fp32 [tokens]).  g and u are fp32 sums of exact products; the second product's are the linears'
+ * (of each 128, the matrix instruction cuts what lies 2^-14 below the largest), the rest of its sum and
+ * the sum over j fp32 in the order of j, so that results do not depend on timing.  Exponent bytes of the up weights
+ * are 252 at most (values of 2^128 and more become infinite).  A slot whose id lies outside
  * [0, experts) is left out, its weight not looked at; a token without experts gives
  * zeros; the same expert twice counts twice.  Two or three kernels, nothing allocated, no atomics
- * on device memory; which kernels depends on the sizes, and with them the last bits of a
- * token's result on how many tokens are beside it.  Made for up to some hundreds of tokens
+ * on device memory; which kernels depends on the sizes, and with them the order of
+ * fp32 sums: a token's last bits, and the code of a v next to a border of two, may change with the tokens
+ * beside it.  Made for up to some hundreds of tokens
  * per expert: an expert's weights are read once for every 16 to 64 of its slots, and anew for
  * each 2048 / top_k tokens.
  * d_ws: w4a8_moe_workspace_bytes(...) bytes, 256-byte aligned, contents of no meaning between

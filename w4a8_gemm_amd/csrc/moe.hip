@@ -6,8 +6,8 @@
 // met, and are bound by that, not by the matrix instructions (8 experts, hidden 4096, inter 8192: their 428 MB
 // take 69 us at 6.2 TB/s, the products of 502 slots 29 us at 3.5 PFLOP/s).  The weights are in the
 // fragment order of the prepared linears (gemm_prepared.hip), so a wave's 16-row tile of 128 k is one
-// 1 KiB load and the e2m1 operand of one block-scaled 16x16x128 product, whose e4m3 operand is 16 slots'
-// activations (a slot: token t, j).
+// 1 KiB load.  The second product takes it as the e2m1 operand of one block-scaled 16x16x128 instruction, whose e4m3
+// operand is 16 slots' v (a slot: token t, j); the first widens it and the slots' activations to bf16.
 //
 // Between the products v is held as e4m3 with a power of two per 32 values, which the matrix
 // instruction takes as the operand's scale: a scale per token would need the maximum over
@@ -41,7 +41,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kFmtFp8 = 0, kFmtFp4 = 4, kUnitScale = 127;
+constexpr int kFmtFp8 = 0, kFmtFp4 = 4;
 constexpr int kMaxExperts = 1024;
 constexpr int kUpThreads = 512, kDownThreads = 1024;
 
@@ -50,7 +50,9 @@ __device__ __forceinline__ v8i frag_fp8(u32x4 lo, u32x4 hi) {
     return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
-// scales in the low byte of each dword
+// The second product's: scales in the low byte of each dword.  Here the instruction's cut (widen_fp8) is left as it is, as in the
+// linears: no code is chosen by the sums, and 2^-14 of a step's largest product is under what bf16 shows of them
+// (a token's error 0.00166 of its result, the rounding's).
 __device__ __forceinline__ v4f product(v8i w, v8i x, v4f c, uint32_t sw, uint32_t sx) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmtFp4, kFmtFp8, 0, (int)sw, 0, (int)sx);
 }
@@ -309,41 +311,34 @@ __device__ __forceinline__ float activated(float g, int act) {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
-// One step's products of a 16-row tile with 16 columns, for the first product of few tokens.
-//
-// The e2m1 x e4m3 instruction aligns its 128 products to the largest and cuts what lies 2^-14
-// below it.  That is far under what bf16 outputs show, but v is rounded to four bits next, and a
-// value that the cut takes over the border of two codes moves by a whole step: for one token
-// such a step of a large value is the output's error (0.0036 of it for 0.0016, one token
-// through 8 of 128 experts).  So here the operands are widened to bf16, exact as both are, and the
-// products added in fp32; it takes 4 instructions for one, which a kernel that waits for its
-// weights has time for.  With more tokens (the tile kernels) the rare steps average out.
-// A lane's 32 k are those of its weights, 32 g to 32 g + 31 of the step.
-struct Columns {
-    v8bf x[4];
-    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t a = i < 2 ? lo[2 * i] : hi[2 * i - 4], b = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
-            const u32x4 r = {pair<false>(a), pair<true>(a), pair<false>(b), pair<true>(b)};
-            x[i] = __builtin_bit_cast(v8bf, r);
-        }
-    }
-    // eight of a lane's k with a tile's codes of them; of the scale the conversion reads the exponent
-    // field alone: 2^(byte - 127), for byte 0 too
-    __device__ __forceinline__ v4f times(int i, uint32_t codes, float scale, v4f c) const {
-        const u32x4 r = {fp4<0>(codes, scale), fp4<1>(codes, scale), fp4<2>(codes, scale), fp4<3>(codes, scale)};
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, r), x[i], c, 0, 0, 0);
-    }
-    template <bool HIGH>
-    static __device__ __forceinline__ uint32_t pair(uint32_t codes) {
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HIGH));
-    }
-    template <int B>
-    static __device__ __forceinline__ uint32_t fp4(uint32_t codes, float s) {
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, B));
-    }
-};
+// The first product's operands are widened to bf16, exact as both are, and its products added in fp32
+// by the bf16 instruction.  The e2m1 x e4m3 instruction that takes them as they are aligns its 128 products to
+// the largest and cuts what lies 2^-14 below it.  That is far under what bf16 outputs show, but v is rounded to
+// four bits next, and a value that the cut takes over the border of two codes moves by a whole step: a
+// step of a large value is that token's error (up to 0.0135 of its result, 0.0018 with widened operands;
+// 77 tokens, 3 of 32 experts, 640 x 384), and large products that cancel take the small ones with them.  It costs
+// four instructions of half the time for one, and the conversions, which the weights' arrival hides but for full
+// units (64 tokens, 8 of 128 experts, 2048 x 768: 62.7 us cut, 60.2 widened, with the empty column tiles left out;
+// 251 tokens, 2 of 8, 4096 x 8192: 113 cut, 134 widened).
+__device__ __forceinline__ v8bf widen_fp8(uint32_t a, uint32_t b) {
+    const auto two = [](uint32_t codes, auto high) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, decltype(high)::value));
+    };
+    const u32x4 r = {two(a, std::false_type{}), two(a, std::true_type{}), two(b, std::false_type{}), two(b, std::true_type{})};
+    return __builtin_bit_cast(v8bf, r);
+}
+// of the scale the conversion reads the exponent field alone: 2^(byte - 127), for byte 0 too
+__device__ __forceinline__ v8bf widen_fp4(uint32_t codes, float scale) {
+    const auto two = [&](auto at) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, decltype(at)::value));
+    };
+    const u32x4 r = {two(std::integral_constant<int, 0>{}), two(std::integral_constant<int, 1>{}),
+                     two(std::integral_constant<int, 2>{}), two(std::integral_constant<int, 3>{})};
+    return __builtin_bit_cast(v8bf, r);
+}
+// the exponent byte of step s % 4 of a scale dword, for widen_fp4
+__device__ __forceinline__ float scale_at(uint32_t sc, int s) { return __uint_as_float(((sc >> (8 * (s & 3))) & 0xFFu) << 23); }
+__device__ __forceinline__ v4f product_wide(v8bf w, v8bf x, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0); }
 
 // Loads through a buffer resource: a scalar base and offset beside one vector offset, and zeros for
 // offsets past its end.
@@ -463,15 +458,14 @@ __global__ __launch_bounds__(kUpThreads, 4) void up_kernel(UpArgs a) {
             }
         };
         const auto compute = [&](int s, const UpStep& r) {
-            Columns c;
-            c.set(r.x[0], r.x[1]);
-            float scale[4];
+            // a lane's 32 k are those of its weights, 32 g to 32 g + 31 of the step
 #pragma unroll
-            for (int q = 0; q < 4; ++q) scale[q] = __uint_as_float(((r.s[q] >> (8 * (s & 3))) & 0xFFu) << 23);
+            for (int i = 0; i < 4; ++i) {
+                const u32x4& from = r.x[i / 2];
+                const v8bf c = widen_fp8(from[2 * (i & 1)], from[2 * (i & 1) + 1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[q] = c.times(i, r.w[q][i], scale[q], acc[q]);
+                for (int q = 0; q < 4; ++q) acc[q] = product_wide(widen_fp4(r.w[q][i], scale_at(r.s[q], s)), c, acc[q]);
+            }
         };
         if (live) {
             UpStep ring[D];
@@ -607,14 +601,11 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
 // asked for again, D steps on, as soon as its products are issued, and the next chunk's
 // columns are asked for before them, so that waiting for those leaves the weights in flight.
 // Every step of a chunk is computed: past K the columns are zeros, and the weights those of the
-// last step.  So are all MT column tiles: those without slots cost products that the
-// weights' arrival hides, conditions on them cost copies of the sums.
+// last step.  The first product, which widens its operands, takes a unit's own column tiles (1, 2 or 4) by code of
+// their own; the second all MT: those without slots cost products that the weights' arrival
+// hides, conditions on them cost copies of the sums.
 constexpr int kTileThreads = 512;
 
-template <int OPSEL>
-__device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmtFp4, kFmtFp8, OPSEL, (int)sw, 0, kUnitScale);
-}
 template <int OPSEL>
 __device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw, uint32_t sx) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmtFp4, kFmtFp8, OPSEL, (int)sw, OPSEL, (int)sx);
@@ -628,10 +619,11 @@ struct Stage {                 // what a thread brings of a chunk: piece tid % 3
     u32x4 r[MT];
     static __device__ __forceinline__ int column(int i) { return (int)threadIdx.x / 32 + 16 * i; }
     // row: the columns' offsets from x, kNowhere past the last; width of a row in bytes
+    template <int I0 = 0, int I1 = MT>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, const uint32_t (&row)[MT], int chunk, int width) {
         const int c = 16 * (threadIdx.x % 32), at = chunk * 512;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = I0; i < I1; ++i)
             r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, at + c < width ? row[i] + c : kNowhere, at, 0));
     }
     // the first chunk, with zeros past the unit's last column in both buffers: their products cost least
@@ -643,9 +635,10 @@ struct Stage {                 // what a thread brings of a chunk: piece tid % 3
             if (column(i) >= cols) *reinterpret_cast<u32x4*>(other + at) = r[i];
         }
     }
+    template <int I0 = 0, int I1 = MT>
     __device__ __forceinline__ void store(uint8_t* to, int cols) const {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = I0; i < I1; ++i)
             if (column(i) < cols) *reinterpret_cast<u32x4*>(to + piece(column(i), threadIdx.x % 32)) = r[i];
     }
 };
@@ -723,16 +716,142 @@ struct Tiles {
     }
 };
 
+// Where a lane finds eight of its k, from 32 g + 8 i on, of step s of column 16 j + n, for the bf16 products: in piece
+// 8 s + 2 g + i / 2.
+struct WideReader {
+    int at[4];
+    __device__ __forceinline__ WideReader() {
+        const int n = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = n * 512 + 16 * ((2 * g + (i & 1) + 8 * (i >> 1)) ^ n);
+    }
+    __device__ __forceinline__ uint2 read(const uint8_t* from, int j, int s, int i) const {
+        return *reinterpret_cast<const uint2*>(from + at[2 * (s & 1) + i / 2] + 16 * 512 * j + 256 * (s >> 1) + 8 * (i & 1));
+    }
+};
+
+// An item of the first product: the unit's NT column tiles, 8 R of inter to a wave.  R = 2: the waves of a pair agree on
+// their block's largest value through LDS.
+template <int R, int MT, int NT, int D, int HINT>
+__device__ __forceinline__ void up_item(const UpArgs& a, const MoePlan& p, uint8_t* lds, float* scale, __amdgpu_buffer_rsrc_t x,
+                                        int64_t t0, uint32_t u, int blk, int blocks) {
+    constexpr int kBuf = 16 * MT * 512;
+    const MoeShape& m = a.m;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const WideReader cr;
+    const int first = unit_first(u), cols = unit_slots(u), steps = m.h_steps, chunks = (steps + 3) / 4;
+    const int64_t tiles_i = m.inter / 16;
+    const bool live = blk < blocks;   // a wave past the last block computes that one again
+    Stage<NT> st;
+    uint32_t row[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int col = st.column(i);
+        row[i] = col < cols ? (uint32_t)m.by_top_k.quotient(p.list[first + col]) * (uint32_t)m.hidden : kNowhere;
+    }
+    st.load(x, row, 0, (int)m.hidden);
+    float sx = 0.0f;
+    if ((int)threadIdx.x < cols) sx = a.xs[t0 + m.by_top_k.quotient(p.list[first + threadIdx.x])];
+    Tiles<R, D, HINT> w;
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+        w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), chunks);
+    w.load_scales(0);
+#pragma unroll
+    for (int s = 0; s < D; ++s) w.load(min(s, steps - 1), s);
+    v4f acc[R][NT];
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    st.store_first(lds, lds + kBuf, cols);
+    if ((int)threadIdx.x < cols) scale[threadIdx.x] = sx;
+    __syncthreads();
+    const auto products = [&](const uint8_t* buf, auto step) {
+        constexpr int s = decltype(step)::value;
+        float sw[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) sw[q] = scale_at(w.sc[q], s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // eight of a lane's 32 k
+            v8bf wide[R];
+#pragma unroll
+            for (int q = 0; q < R; ++q) wide[q] = widen_fp4((&w.q[s % D][q].x)[i], sw[q]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint2 codes = cr.read(buf, j, s, i);
+                const v8bf b = widen_fp8(codes.x, codes.y);
+#pragma unroll
+                for (int q = 0; q < R; ++q) acc[q][j] = product_wide(wide[q], b, acc[q][j]);
+                __builtin_amdgcn_sched_barrier(0);   // no more than a tile's columns in registers
+            }
+        }
+    };
+    for (int c = 0; c + 1 < chunks; ++c) {
+        w.take_scales();
+        w.load_scales(c + 1);
+        each_step([&](auto step) {
+            constexpr int s = decltype(step)::value;
+            // half of the next chunk's columns at a time, for the registers
+            if constexpr (s == 0) st.template load<0, (NT + 1) / 2>(x, row, c + 1, (int)m.hidden);
+            if constexpr (s == 2) st.template load<(NT + 1) / 2, NT>(x, row, c + 1, (int)m.hidden);
+            __builtin_amdgcn_sched_barrier(0);
+            products(lds + (c & 1) * kBuf, step);
+            hold(acc);
+            __builtin_amdgcn_sched_barrier(0);
+            w.load(min(4 * c + s + D, steps - 1), s % D);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (s == 1) st.template store<0, (NT + 1) / 2>(lds + ((c + 1) & 1) * kBuf, cols);
+            if constexpr (s == 3) st.template store<(NT + 1) / 2, NT>(lds + ((c + 1) & 1) * kBuf, cols);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        __syncthreads();
+    }
+    w.take_scales();
+    each_step([&](auto step) {
+        constexpr int s = decltype(step)::value;
+        products(lds + ((chunks - 1) & 1) * kBuf, step);
+        hold(acc);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (s + D < 4) w.load(min(4 * (chunks - 1) + s + D, steps - 1), s % D);
+    });
+    __syncthreads();   // before the next item's first columns
+    if constexpr (R == 2) {   // blocks in pairs: every wave is live
+        uint32_t* tops = reinterpret_cast<uint32_t*>(lds);   // [wave][column]
+        Quad v[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            v[j] = quad_of(acc[0][j], acc[1][j], scale[16 * j + n], a.act);
+            v[j].top = column_top(v[j].top);
+            if (g == 0) tops[wave * 16 * NT + 16 * j + n] = v[j].top;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint32_t top = max(v[j].top, tops[(wave ^ 1) * 16 * NT + 16 * j + n]);
+            if (16 * j + n >= cols) continue;
+            const int64_t at = t0 * m.top_k + p.list[first + 16 * j + n];
+            store_quad(m, v[j], top, at, 16 * blk + 4 * g);
+            if (g == 0 && !(wave & 1)) store_power(m, top, at, blk >> 1);
+        }
+        __syncthreads();
+    } else if (live) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (16 * j >= cols) continue;
+            const v4f r[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
+            store_v(m, r, scale[16 * j + n], a.act, t0 * m.top_k + p.list[first + min(16 * j + n, cols - 1)], blk, g,
+                    16 * j + n < cols);
+        }
+    }
+}
+
 // R = 4: a wave takes 32 of inter, two tiles each of the gate's and the up rows; R = 2: 16 of inter, one
-// of each, the waves of a pair agreeing on their block's largest value through LDS.  R = 2 leaves
-// registers for more columns (four sums of four tiles and two steps of weights are the 128 that two
-// workgroups to a CU leave a wave).  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 213 MB in 37 us,
-// 5.7 TB/s; 8 experts, hidden 4096, inter 8192, 63 slots each: 285 MB in 65 to 73 us, 3.9 to 4.4 TB/s, by how many
-// experts have more than 64 slots.
+// of each.  R = 2 leaves registers for more columns (four sums of four tiles and two steps of weights are the 128 that two
+// workgroups to a CU leave a wave).
 template <int R, int MT, int D, int HINT>
 __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int kBuf = 16 * MT * 512;
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
@@ -740,106 +859,20 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts,
                                      blockIdx.x == gridDim.x - 1 ? a.plans + blockIdx.y : nullptr, a.plan_slots);
 
-    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const ColumnReader cr;
     const int blocks = (int)(m.inter / (8 * R)), groups = (blocks + 7) / 8, items = p.units * groups;   // blocks of a wave
-    const int steps = m.h_steps, chunks = (steps + 3) / 4;
-    const int64_t tiles_i = m.inter / 16;
     const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
     float* scale = p.scale[1];
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         scale = p.scale[scale == p.scale[1] ? 0 : 1];   // a slow wave may still read the last item's
-        const int of = a.by_blocks.quotient(item);
+        const int of = a.by_blocks.quotient(item), blk = a.by_blocks.rest(item, of) * 8 + uniform(threadIdx.x >> 6);
         const uint32_t u = uniform(p.unit[of]);
-        const int first = unit_first(u), cols = unit_slots(u), blk = a.by_blocks.rest(item, of) * 8 + wave;
-        const bool live = blk < blocks;   // a wave past the last block computes that one again
-        Stage<MT> st;
-        uint32_t row[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int col = st.column(i);
-            row[i] = col < cols ? (uint32_t)m.by_top_k.quotient(p.list[first + col]) * (uint32_t)m.hidden : kNowhere;
-        }
-        st.load(x, row, 0, (int)m.hidden);
-        float sx = 0.0f;
-        if ((int)threadIdx.x < cols) sx = a.xs[t0 + m.by_top_k.quotient(p.list[first + threadIdx.x])];
-        Tiles<R, D, HINT> w;
-#pragma unroll
-        for (int q = 0; q < R; ++q)
-            w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), chunks);
-        w.load_scales(0);
-#pragma unroll
-        for (int s = 0; s < D; ++s) w.load(min(s, steps - 1), s);
-        v4f acc[R][MT];
-#pragma unroll
-        for (int q = 0; q < R; ++q)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        st.store_first(lds, lds + kBuf, cols);
-        if ((int)threadIdx.x < cols) scale[threadIdx.x] = sx;
-        __syncthreads();
-        const auto products = [&](const uint8_t* buf, auto step) {
-            constexpr int s = decltype(step)::value;
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const v8i b = cr.read(buf, j, s);
-#pragma unroll
-                for (int q = 0; q < R; ++q) acc[q][j] = product_at<s>(frag_fp4(w.q[s % D][q]), b, acc[q][j], w.sc[q]);
-                if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);   // no more than two tiles' columns in registers
-            }
-        };
-        for (int c = 0; c + 1 < chunks; ++c) {
-            st.load(x, row, c + 1, (int)m.hidden);
-            w.take_scales();
-            w.load_scales(c + 1);
-            each_step([&](auto step) {
-                constexpr int s = decltype(step)::value;
-                products(lds + (c & 1) * kBuf, step);
-                hold(acc);
-                __builtin_amdgcn_sched_barrier(0);
-                w.load(min(4 * c + s + D, steps - 1), s % D);
-                __builtin_amdgcn_sched_barrier(0);
-            });
-            st.store(lds + ((c + 1) & 1) * kBuf, cols);
-            __syncthreads();
-        }
-        w.take_scales();
-        each_step([&](auto step) {
-            constexpr int s = decltype(step)::value;
-            products(lds + ((chunks - 1) & 1) * kBuf, step);
-            hold(acc);
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (s + D < 4) w.load(min(4 * (chunks - 1) + s + D, steps - 1), s % D);
-        });
-        __syncthreads();   // before the next item's first columns
-        if constexpr (R == 2) {   // blocks in pairs: every wave is live
-            uint32_t* tops = reinterpret_cast<uint32_t*>(lds);   // [wave][column]
-            Quad v[MT];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                v[j] = quad_of(acc[0][j], acc[1][j], scale[16 * j + n], a.act);
-                v[j].top = column_top(v[j].top);
-                if (g == 0) tops[wave * 16 * MT + 16 * j + n] = v[j].top;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const uint32_t top = max(v[j].top, tops[(wave ^ 1) * 16 * MT + 16 * j + n]);
-                if (16 * j + n >= cols) continue;
-                const int64_t at = t0 * m.top_k + p.list[first + 16 * j + n];
-                store_quad(m, v[j], top, at, 16 * blk + 4 * g);
-                if (g == 0 && !(wave & 1)) store_power(m, top, at, blk >> 1);
-            }
-            __syncthreads();
-        } else if (live) {
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                if (16 * j >= cols) continue;
-                const v4f r[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
-                store_v(m, r, scale[16 * j + n], a.act, t0 * m.top_k + p.list[first + min(16 * j + n, cols - 1)], blk, g,
-                        16 * j + n < cols);
-            }
-        }
+        const int tiles = (unit_slots(u) + 15) / 16;   // the same for all threads
+        if (tiles == 1)
+            up_item<R, MT, 1, D, HINT>(a, p, lds, scale, x, t0, u, blk, blocks);
+        else if (MT == 2 || tiles == 2)
+            up_item<R, MT, 2, D, HINT>(a, p, lds, scale, x, t0, u, blk, blocks);
+        else if constexpr (MT == 4)
+            up_item<R, MT, 4, D, HINT>(a, p, lds, scale, x, t0, u, blk, blocks);
     }
 }
 
