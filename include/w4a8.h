@@ -679,7 +679,8 @@ w4a8_status w4a8_residual_norm(w4a8_float type, const uint16_t *d_y, int64_t ld_
  *       group_top (1 or 2) largest choice scores, and only the groups_kept best runs take part
  *   the top_k largest, ties to the lower index, in descending order: d_ids [tokens][top_k]
  *   d_weights [tokens][top_k] = scale p, or scale p / (sum of the chosen p) with
- *       renormalize != 0 (0 where that sum is 0)
+ *       renormalize != 0 (0 where that sum is 0: in fp64 the sigmoid of a logit below -709
+ *       is, and the softmax score of one 745 below the top, where groups or a bias left out the top)
  * A logit of -inf or NaN (with a bias also a score of -inf or NaN) is an expert that is off:
  * it is never chosen and counts as 0 in the softmax; where fewer than top_k are left the
  * row ends in ids of -1 with weights of 0.  Logits of +inf share the softmax evenly.

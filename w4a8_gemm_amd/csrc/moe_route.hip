@@ -8,7 +8,8 @@
 // Without bias and groups the choice goes by the logits themselves.  With them it
 // goes by scores in fp64: which expert a token meets should follow from the inputs,
 // not from how an exponential or a sum was rounded.  Weights are sums and
-// exponentials in the same precision, rounded once to fp32.
+// exponentials in the same precision, but for the sigmoids of experts chosen by their logits,
+// which are fp64 too.
 #include <type_traits>
 
 #include "wave_ops.h"
@@ -45,6 +46,13 @@ __device__ __forceinline__ uint64_t lanes_of_max(uint64_t v) {
         have = __ballot(in && (uint32_t)v == top);
     }
     return have;
+}
+
+// A chosen expert's sigmoid where the choice went by the logits, its lane's alone: in fp64, as 1 + exp(-logit) leaves
+// fp32 below a logit of -88, and of such scores renormalized ones are not zeros.
+__device__ __forceinline__ double chosen_sigmoid(int id, float logit) { return id >= 0 ? 1.0 / (1.0 + exp(-(double)logit)) : 0.0; }
+__device__ __forceinline__ float scaled_share(double w, double sum, const RouteArgs& a) {
+    return (float)((a.renormalize ? (sum > 0.0 ? w / sum : 0.0) : w) * (double)a.scale);
 }
 
 __device__ __forceinline__ float exponential(float v) { return expf(v); }
@@ -94,7 +102,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
         if (!(total > 0)) total = 1;
     } else {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) p[i] = S(1) / (S(1) + exponential(-S(logit[i])));
+        for (int i = 0; i < NL; ++i) {
+            if constexpr (kByScore)
+                p[i] = S(1) / (S(1) + exponential(-S(logit[i])));
+            else
+                p[i] = logit[i];
+        }
     }
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -189,11 +202,18 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
         sum += w;
         if (lane == j) id = at, mine = w;
     }
-    if constexpr (!kByScore) mine = mine / total, sum = sum / total;
-    if (a.renormalize) mine = sum > 0 ? mine / sum : S(0);
+    float weight;
+    if (!kByScore && a.score == W4A8_SCORE_SIGMOID) {
+        const double w = chosen_sigmoid(id, (float)mine);
+        weight = scaled_share(w, wave_reduce(w, Add()), a);
+    } else {
+        if constexpr (!kByScore) mine = mine / total, sum = sum / total;
+        if (a.renormalize) mine = sum > 0 ? mine / sum : S(0);
+        weight = (float)(mine * S(a.scale));
+    }
     if (lane < a.top_k) {
         a.ids[token * a.top_k + lane] = id;
-        a.weights[token * a.top_k + lane] = (float)(mine * S(a.scale));
+        a.weights[token * a.top_k + lane] = weight;
     }
 }
 
@@ -230,9 +250,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_rows_kernel(RouteArgs 
         }
         total = row_reduce(total, Add());
         if (!(total > 0.0f)) total = 1.0f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) p[i] = 1.0f / (1.0f + expf(-p[i]));
     }
     int id = -1;
     float mine = 0.0f, sum = 0.0f;
@@ -253,16 +270,22 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_rows_kernel(RouteArgs 
                 key[i] = 0;
                 w = p[i];
             }
-        w = row_reduce(w, Add());   // of one lane, and zeros
+        w = row_reduce(w, Add());   // of one lane (its logit, for a sigmoid), and zeros
         if (best == 0) w = 0.0f;
         sum += w;
         if (sub == j && best) id = (int)~which, mine = w;
     }
-    mine = mine / total, sum = sum / total;
-    if (a.renormalize) mine = sum > 0.0f ? mine / sum : 0.0f;
+    if (a.score == W4A8_SCORE_SIGMOID) {
+        const double q = chosen_sigmoid(id, mine);
+        mine = scaled_share(q, row_reduce(q, Add()), a);
+    } else {
+        mine = mine / total, sum = sum / total;
+        if (a.renormalize) mine = sum > 0.0f ? mine / sum : 0.0f;
+        mine *= a.scale;
+    }
     if (sub < a.top_k && token < a.tokens) {
         a.ids[token * a.top_k + sub] = id;
-        a.weights[token * a.top_k + sub] = mine * a.scale;
+        a.weights[token * a.top_k + sub] = mine;
     }
 }
 
