@@ -64,6 +64,8 @@ PyObject* residual_norm(PyObject* const* a, Py_ssize_t n) {
     const double scale = number(a[5]), eps = number(a[6]);
     const bool values = truth(a[7]), fp8 = truth(a[8]);
     if (!values && !fp8 && !r && a[9] == Py_None) refuse(PyExc_ValueError, "nothing to compute: values, fp8 or a residual");
+    if (!values && a[10] != Py_None) refuse(PyExc_ValueError, "out needs values=True");
+    if (!fp8 && (a[11] != Py_None || a[12] != Py_None)) refuse(PyExc_ValueError, "x_fp8 and x_scale need fp8=True");
     on_gpu(y, "y");
     const c10::DeviceGuard guard(dev);
     at::Tensor ro, out, x8, xs;

@@ -49,7 +49,7 @@ def residual_norm(y: torch.Tensor, residual: torch.Tensor | None = None, weight:
 
     Returns (residual_out, out, x_fp8, x_scale), None for what was not asked for; without a
     residual the sum is stored only where residual_out is given.  residual_out may be
-    residual itself, and out y."""
+    residual itself, and out y.  An output given for what is not asked for is refused."""
     return _native().residual_norm(y, residual, weight, post_weight, gate, scale, eps, values, fp8, residual_out, out, x_fp8,
                                    x_scale)
 
