@@ -29,6 +29,8 @@
 //                                                             inter is long and hidden short)
 //
 // The partial sums of a token are added in the order of j, K parts of a slot first: no atomics.
+#include <math.h>
+
 #include <type_traits>
 
 #include "w4a8_internal.h"
@@ -605,6 +607,7 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
 // their own; the second all MT: those without slots cost products that the weights' arrival
 // hides, conditions on them cost copies of the sums.
 constexpr int kTileThreads = 512;
+constexpr int kUpColumns = 64;      // of the first product's units
 
 template <int OPSEL>
 __device__ __forceinline__ v4f product_at(v8i w, v8i x, v4f c, uint32_t sw, uint32_t sx) {
@@ -688,12 +691,12 @@ __device__ __forceinline__ void hold(v4f (&acc)[Q][MT]) {
         for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[q][j]));
 }
 
-// R weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk
-template <int R, int D, int HINT>
+// Two weight tiles of a wave: codes of D steps (2 or 4) and scale dwords of a chunk
+template <int D, int HINT>
 struct Tiles {
-    __amdgpu_buffer_rsrc_t w[R], s[R];
-    uint4 q[D][R];
-    uint32_t sc[R], next[R];
+    __amdgpu_buffer_rsrc_t w[2], s[2];
+    uint4 q[D][2];
+    uint32_t sc[2], next[2];
     __device__ __forceinline__ void at(int r, const uint8_t* wt, const uint8_t* st, int64_t tile, int c_pad) {
         w[r] = resource(wt + tile * c_pad * 4096, c_pad * 4096);
         s[r] = resource(st + tile * c_pad * 256, c_pad * 256);
@@ -701,18 +704,18 @@ struct Tiles {
     __device__ __forceinline__ void load(int step, int to) {   // to: step % D
         const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < 2; ++r)
             q[to][r] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w[r], 16 * lane, step * 1024, HINT));
     }
     __device__ __forceinline__ void load_scales(int chunk) {
         const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int r = 0; r < R; ++r) next[r] = __builtin_amdgcn_raw_buffer_load_b32(s[r], 4 * lane, chunk * 256, 0);
+        for (int r = 0; r < 2; ++r) next[r] = __builtin_amdgcn_raw_buffer_load_b32(s[r], 4 * lane, chunk * 256, 0);
     }
     // of the chunk that was asked for; then the next one's asked for
     __device__ __forceinline__ void take_scales() {
 #pragma unroll
-        for (int r = 0; r < R; ++r) sc[r] = next[r];
+        for (int r = 0; r < 2; ++r) sc[r] = next[r];
     }
 };
 
@@ -730,18 +733,17 @@ struct WideReader {
     }
 };
 
-// An item of the first product: the unit's NT column tiles, 8 R of inter to a wave.  R = 2: the waves of a pair agree on
-// their block's largest value through LDS.
-template <int R, int MT, int NT, int D, int HINT>
+// An item of the first product: the unit's NT column tiles.  A wave has 16 of inter, a tile each of the gate's and the up
+// rows, and the waves of a pair agree on their block's largest value through LDS.
+template <int NT, int HINT>
 __device__ __forceinline__ void up_item(const UpArgs& a, const MoePlan& p, uint8_t* lds, float* scale, __amdgpu_buffer_rsrc_t x,
-                                        int64_t t0, uint32_t u, int blk, int blocks) {
-    constexpr int kBuf = 16 * MT * 512;
+                                        int64_t t0, uint32_t u, int blk) {
+    constexpr int kBuf = kUpColumns * 512, D = 2;   // steps of weights in flight
     const MoeShape& m = a.m;
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const WideReader cr;
     const int first = unit_first(u), cols = unit_slots(u), steps = m.h_steps, chunks = (steps + 3) / 4;
     const int64_t tiles_i = m.inter / 16;
-    const bool live = blk < blocks;   // a wave past the last block computes that one again
     Stage<NT> st;
     uint32_t row[NT];
 #pragma unroll
@@ -752,16 +754,15 @@ __device__ __forceinline__ void up_item(const UpArgs& a, const MoePlan& p, uint8
     st.load(x, row, 0, (int)m.hidden);
     float sx = 0.0f;
     if ((int)threadIdx.x < cols) sx = a.xs[t0 + m.by_top_k.quotient(p.list[first + threadIdx.x])];
-    Tiles<R, D, HINT> w;
+    Tiles<D, HINT> w;
 #pragma unroll
-    for (int q = 0; q < R; ++q)
-        w.at(q, a.w, a.s, (2 * unit_expert(u) + q / (R / 2)) * tiles_i + R / 2 * (live ? blk : blocks - 1) + q % (R / 2), chunks);
+    for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (2 * unit_expert(u) + q) * tiles_i + blk, chunks);
     w.load_scales(0);
 #pragma unroll
     for (int s = 0; s < D; ++s) w.load(min(s, steps - 1), s);
-    v4f acc[R][NT];
+    v4f acc[2][NT];
 #pragma unroll
-    for (int q = 0; q < R; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[q][j] = v4f{0.f, 0.f, 0.f, 0.f};
     st.store_first(lds, lds + kBuf, cols);
@@ -769,20 +770,20 @@ __device__ __forceinline__ void up_item(const UpArgs& a, const MoePlan& p, uint8
     __syncthreads();
     const auto products = [&](const uint8_t* buf, auto step) {
         constexpr int s = decltype(step)::value;
-        float sw[R];
+        float sw[2];
 #pragma unroll
-        for (int q = 0; q < R; ++q) sw[q] = scale_at(w.sc[q], s);
+        for (int q = 0; q < 2; ++q) sw[q] = scale_at(w.sc[q], s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {   // eight of a lane's 32 k
-            v8bf wide[R];
+            v8bf wide[2];
 #pragma unroll
-            for (int q = 0; q < R; ++q) wide[q] = widen_fp4((&w.q[s % D][q].x)[i], sw[q]);
+            for (int q = 0; q < 2; ++q) wide[q] = widen_fp4((&w.q[s % D][q].x)[i], sw[q]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const uint2 codes = cr.read(buf, j, s, i);
                 const v8bf b = widen_fp8(codes.x, codes.y);
 #pragma unroll
-                for (int q = 0; q < R; ++q) acc[q][j] = product_wide(wide[q], b, acc[q][j]);
+                for (int q = 0; q < 2; ++q) acc[q][j] = product_wide(wide[q], b, acc[q][j]);
                 __builtin_amdgcn_sched_barrier(0);   // no more than a tile's columns in registers
             }
         }
@@ -816,50 +817,40 @@ __device__ __forceinline__ void up_item(const UpArgs& a, const MoePlan& p, uint8
         if constexpr (s + D < 4) w.load(min(4 * (chunks - 1) + s + D, steps - 1), s % D);
     });
     __syncthreads();   // before the next item's first columns
-    if constexpr (R == 2) {   // blocks in pairs: every wave is live
-        uint32_t* tops = reinterpret_cast<uint32_t*>(lds);   // [wave][column]
-        Quad v[NT];
+    uint32_t* tops = reinterpret_cast<uint32_t*>(lds);   // [wave][column]
+    Quad v[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            v[j] = quad_of(acc[0][j], acc[1][j], scale[16 * j + n], a.act);
-            v[j].top = column_top(v[j].top);
-            if (g == 0) tops[wave * 16 * NT + 16 * j + n] = v[j].top;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const uint32_t top = max(v[j].top, tops[(wave ^ 1) * 16 * NT + 16 * j + n]);
-            if (16 * j + n >= cols) continue;
-            const int64_t at = t0 * m.top_k + p.list[first + 16 * j + n];
-            store_quad(m, v[j], top, at, 16 * blk + 4 * g);
-            if (g == 0 && !(wave & 1)) store_power(m, top, at, blk >> 1);
-        }
-        __syncthreads();
-    } else if (live) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (16 * j >= cols) continue;
-            const v4f r[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
-            store_v(m, r, scale[16 * j + n], a.act, t0 * m.top_k + p.list[first + min(16 * j + n, cols - 1)], blk, g,
-                    16 * j + n < cols);
-        }
+    for (int j = 0; j < NT; ++j) {
+        v[j] = quad_of(acc[0][j], acc[1][j], scale[16 * j + n], a.act);
+        v[j].top = column_top(v[j].top);
+        if (g == 0) tops[wave * 16 * NT + 16 * j + n] = v[j].top;
     }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const uint32_t top = max(v[j].top, tops[(wave ^ 1) * 16 * NT + 16 * j + n]);
+        if (16 * j + n >= cols) continue;
+        const int64_t at = t0 * m.top_k + p.list[first + 16 * j + n];
+        store_quad(m, v[j], top, at, 16 * blk + 4 * g);
+        if (g == 0 && !(wave & 1)) store_power(m, top, at, blk >> 1);
+    }
+    __syncthreads();
 }
 
-// R = 4: a wave takes 32 of inter, two tiles each of the gate's and the up rows; R = 2: 16 of inter, one
-// of each.  R = 2 leaves registers for more columns (four sums of four tiles and two steps of weights are the 128 that two
-// workgroups to a CU leave a wave).
-template <int R, int MT, int D, int HINT>
+// Units of up to 64 slots and 128 of inter to a workgroup, whose waves are all live (inter is a multiple of 128).  Sums of
+// two times four tiles, two steps of weights and half a chunk's columns fill the 128 registers that two
+// workgroups to a CU leave a wave.
+template <int HINT>
 __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     MoePlan& p = *reinterpret_cast<MoePlan*>(lds + a.plan_at);
     const MoeShape& m = a.m;
     const int64_t t0 = (int64_t)blockIdx.y * m.chunk;
     const int tokens = (int)min((int64_t)m.chunk, m.tokens - t0), slots = tokens * m.top_k;
-    make_plan<kTileThreads, 16 * MT>(p, lds, a.ids + t0 * m.top_k, slots, m.experts,
-                                     blockIdx.x == gridDim.x - 1 ? a.plans + blockIdx.y : nullptr, a.plan_slots);
+    make_plan<kTileThreads, kUpColumns>(p, lds, a.ids + t0 * m.top_k, slots, m.experts,
+                                        blockIdx.x == gridDim.x - 1 ? a.plans + blockIdx.y : nullptr, a.plan_slots);
 
-    const int blocks = (int)(m.inter / (8 * R)), groups = (blocks + 7) / 8, items = p.units * groups;   // blocks of a wave
+    const int items = p.units * (int)(m.inter / 128);
     const __amdgpu_buffer_rsrc_t x = resource(a.x8 + t0 * m.hidden, (uint32_t)(tokens * m.hidden));
     float* scale = p.scale[1];
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -868,11 +859,11 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
         const uint32_t u = uniform(p.unit[of]);
         const int tiles = (unit_slots(u) + 15) / 16;   // the same for all threads
         if (tiles == 1)
-            up_item<R, MT, 1, D, HINT>(a, p, lds, scale, x, t0, u, blk, blocks);
-        else if (MT == 2 || tiles == 2)
-            up_item<R, MT, 2, D, HINT>(a, p, lds, scale, x, t0, u, blk, blocks);
-        else if constexpr (MT == 4)
-            up_item<R, MT, 4, D, HINT>(a, p, lds, scale, x, t0, u, blk, blocks);
+            up_item<1, HINT>(a, p, lds, scale, x, t0, u, blk);
+        else if (tiles == 2)
+            up_item<2, HINT>(a, p, lds, scale, x, t0, u, blk);
+        else
+            up_item<4, HINT>(a, p, lds, scale, x, t0, u, blk);
     }
 }
 
@@ -915,7 +906,7 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
         u32x4 er{};
         st.load(x, row, c0, (int)m.inter);
         if (has_e) er = exponents(ep, c0, steps);
-        Tiles<2, D, HINT> w;
+        Tiles<D, HINT> w;
 #pragma unroll
         for (int q = 0; q < 2; ++q) w.at(q, a.w, a.s, (int64_t)unit_expert(u) * tiles + (live ? tile : tiles - 2) + q, chunks);
         w.load_scales(c0);
@@ -1041,12 +1032,20 @@ int64_t moe_plans(int64_t slots) { return slots / 2017 + 1; }
 
 struct MoeGrid {
     bool few, up_tiles;             // few: the kernels for up to 64 slots
-    int up_mt, down_mt;             // column tiles of the tile kernels' units
+    int down_mt;                    // column tiles of the second product's units
     bool up_shared, down_shared;    // several units of an expert read its weights
-    int kw, rows, ks, up_groups;
+    int kw, rows, ks;
     unsigned up, down, join, chunks;
     size_t up_at, down_at;          // LDS of the kernels before the plan
 };
+
+// Units of w slots that an expert takes, were its slots normal about `each` with that variance: the mean of ceil(c / w)
+double expected_units(double each, int w) {
+    if (each > 8.0 * w) return each / w + 0.5;
+    double units = 0.0;
+    for (int j = 0; j * w < each + 6.0 * sqrt(each) + 1.0; ++j) units += 0.5 * erfc((j * w + 0.5 - each) / sqrt(2.0 * each));
+    return units;
+}
 
 MoeGrid moe_grid(const MoeArgs& a) {
     MoeGrid g{};
@@ -1057,28 +1056,43 @@ MoeGrid moe_grid(const MoeArgs& a) {
     double missed = 1.0;
     for (int64_t s = 0; s < slots && missed > 1e-3; ++s) missed *= 1.0 - 1.0 / (double)experts;
     const int64_t met = (int64_t)((double)experts * (1.0 - missed) + 0.5);
-    const int64_t blocks = a.e.inter / 32, down_groups = (a.e.hidden / 16 + 15) / 16;
-    const int64_t each = slots / experts;   // slots of an expert, on average
+    const int64_t down_groups = (a.e.hidden / 16 + 15) / 16;
+    const int64_t each = slots / experts;   // slots of an expert, on average, were none left out
     const bool small = slots <= kWaveSlots;
-    // The first product: units of 64 slots and 16 of inter to a wave, which are more items for the same weights,
-    // or of 32 slots and 32 of inter, whose columns are read and staged half as often.  Microseconds (32 | 64) by
-    // tiles (16 of inter of an expert that is met) and slots of an expert: 1024 tiles, 6 slots 14.7 | 12.9;
-    // 3900, 1 23.1 | 24.7; 4096, 6 16.3 | 18.2; 4400, 1 21.2 | 23.4; 5400, 2 36.4 | 35.3; 6100, 4 38.6 | 36.5;
-    // 704, 47 17.6 | 14.1; 2048, 25 41.7 | 35.6; 4096, 16 54.1 | 51.3; 4096, 128 158 | 113.
-    // (Units of 128: 77 to 94 us for 74 to 76 with 8 experts, 63 slots each, hidden 4096, inter 8192.)
-    const int64_t tiles_up = met * (a.e.inter / 16);
-    g.up_mt = each < 8 && tiles_up > 2048 && tiles_up < 4800 ? 2 : 4;
-    // The second product, units of 32 or 64: the wider where they take an expert's slots in one for two or
-    // three (slots of an expert, 32 | 64: 16 31.5 | 30.9; 45 8.8 | 8.3, the call 30.1 | 31.7; 50 13.2 | 14.9;
-    // 62 38.6 | 36.8; 63 53 | 44; 128 69 | 74; 256 110 | 113)
-    g.down_mt = each >= 56 && each <= 80 ? 4 : 2;
-    // Weights that several units read are left in the caches, the others' loads have the hint (hidden 4096,
-    // inter 8192, 8 experts, both products, with | without: 63 slots of an expert 127 | 117; 128 223 | 178; 128
-    // experts, 4 slots each, hidden 2048, inter 768: 61 | 67)
-    g.up_shared = each >= 48, g.down_shared = each >= 24;
-    g.up_groups = (int)(g.up_mt == 2 ? (blocks + 7) / 8 : blocks / 4);
-    // with few items the tile kernel leaves CUs idle
-    g.up_tiles = !small && met * (each / (16 * g.up_mt) + 1) * g.up_groups >= 80;
+    // The second product's K parts, 2 or 4 within moe_sum_rows, while items are fewer than the CUs: parts cost their partial
+    // sums (microseconds of the call with 1, 2 and 4: 32 items, inter 8192 53, 44, 42; 60, 7936 57, 50, 50; 128, 4096
+    // 42, 45, 46; 128, 8192 92, 93, 94, and with units of 64 136, 142, 157)
+    const int64_t chunks_k = (a.e.inter + 511) / 512;
+    const auto parts = [&](int mt) {
+        const int64_t items = met * (each / (16 * mt) + 1) * down_groups;
+        int ks = 1;
+        while (ks < 4 && 2 * ks * items < cus && 2 * ks * a.tokens * a.top_k <= kSumRows && 4 * ks <= chunks_k) ks *= 2;
+        return ks;
+    };
+    // Its units, of 32 slots, two workgroups to a CU, or of 64, one: by the rounds that the items take.  As times of a K part's
+    // chunk, two workgroups of 32 side by side are 1, one alone 0.6, one of 64 0.84.  Over 418 sizes (4 to 256 experts of 1 to
+    // 250 slots, hidden 1024 to 8192, inter 512 to 14336) the calls come out 0.5 % over the better of the two on average and 7 %
+    // at most; with 32 always 1.2 % and 11 %.  Times of the call (32 | 64): 8 experts, 4096 x 8192, 48 slots of an
+    // expert 108 | 114, 60 146 | 137, 100 183 | 174; 16 experts, 4096 x 4096, 44 slots 115 | 109, 64 142 | 146, 80 171 | 189.
+    const auto rounds = [&](int mt) {
+        const int ks = parts(mt);
+        const double items = (double)experts * expected_units((double)slots / (double)experts, 16 * mt) * (double)(down_groups * ks);
+        const double chunks = (double)chunks_k / ks;
+        if (mt == 4) return chunks * 0.84 * ceil(items / (double)cus);
+        const double pairs = items / (double)(2 * cus), whole = floor(pairs), rest = pairs - whole;
+        return chunks * (whole + (rest == 0.0 ? 0.0 : rest <= 0.5 ? 0.6 : 1.0));
+    };
+    g.down_mt = rounds(4) < rounds(2) ? 4 : 2;
+    // Weights that several units read are left in the caches, the others' loads have the hint.  First product (with | without):
+    // 60 slots of an expert, 16 experts, 2048 x 1408 44.8 | 46.4, 80 56.1 | 55.8, 8 experts 37.3 | 36.2; 72, 8 experts,
+    // 4096 x 8192 -2 %.  Second, units of 32: 20 slots, 32 experts, 4096 x 4096 172 | 176, 28 188 | 188, 32 200 | 193,
+    // 48 252 | 226.
+    g.up_shared = each >= kUpColumns, g.down_shared = each >= 24;
+    // With few items the tile kernel leaves CUs idle, which up_kernel's K parts fill (microseconds of the call, tiles | K parts:
+    // 64 items, 4096 x 512, 150 tokens 37 | 30; 96, 4096 x 1536, 100 43 | 39, 1024 x 1024, 300 26.0 | 26.2; 128,
+    // 1024 x 1024, 66 19 | 21; 192, 4096 x 1536, 150 44 | 54)
+    const int64_t up_items = met * (each / kUpColumns + 1) * (a.e.inter / 128);
+    g.up_tiles = !small && up_items >= 112;
     const auto units = [&](int64_t columns) {
         const int64_t most = slots < experts ? slots : experts + slots / columns;
         return most < slots ? most : slots;
@@ -1094,10 +1108,10 @@ MoeGrid moe_grid(const MoeArgs& a) {
     // as many workgroups of the tile kernels as the CUs hold at once: each lists the slots only once
     const auto grid = [&](int64_t groups, int64_t room) { return (unsigned)(groups < room ? groups : room); };
     if (g.up_tiles) {
-        g.up = grid(units(16 * g.up_mt) * g.up_groups, 2 * cus);
-        g.up_at = at(2 * 16 * g.up_mt * 512);
+        g.up = grid(units(kUpColumns) * (a.e.inter / 128), 2 * cus);
+        g.up_at = at(2 * kUpColumns * 512);
     } else {
-        const int64_t items = units(16) * blocks, steps = a.e.hidden / 128;
+        const int64_t items = units(16) * (a.e.inter / 32), steps = a.e.hidden / 128;
         // K parts while there is about a workgroup for each CU, and four where a wave would have eight steps or more
         // (microseconds with 1, 2, 4 and 8: hidden 2048, one token of eight experts 14.4, 10.9, 10.2, 5.9, four
         // 15.5, 12.3, 13.4, 12.9, eight 18.5, 22.0, 19.9, 20.6; hidden 2688, 73 workgroups 24.4, 17.9, 12.9,
@@ -1113,13 +1127,7 @@ MoeGrid moe_grid(const MoeArgs& a) {
         g.rows = (int)(16 * slots);
         g.down_at = (size_t)g.rows * 64 + (size_t)slots * 4;
     } else {
-        // 2 or 4 parts of K, within moe_sum_rows, while items are fewer than the CUs: parts cost their partial sums
-        // (microseconds of the call with 1, 2 and 4: 32 items, inter 8192 53, 44, 42; 60, 7936 57, 50, 50; 128, 4096
-        // 42, 45, 46; 128, 8192 92, 93, 94, and with units of 64 136, 142, 157)
-        const int64_t chunks_k = (a.e.inter + 511) / 512, items = met * (each / (16 * g.down_mt) + 1) * down_groups;
-        g.ks = 1;
-        while (g.ks < 4 && 2 * g.ks * items < cus && 2 * g.ks * a.tokens * a.top_k <= kSumRows && 4 * g.ks <= chunks_k)
-            g.ks *= 2;
+        g.ks = parts(g.down_mt);
         g.down = grid(units(16 * g.down_mt) * down_groups * g.ks, 2 * cus);
         g.down_at = (size_t)(2 * 16 * g.down_mt * (512 + 16));
         g.join = (unsigned)((a.tokens * (a.e.hidden / 4) + 255) / 256);
@@ -1144,10 +1152,7 @@ hipError_t launch_up(const MoeGrid& g, UpArgs a, hipStream_t stream) {
     if (g.few) return launch_one(up_kernel<true>, g.up, 1, kUpThreads, g.up_at, stream, a);
     const size_t bytes = g.up_at + sizeof(MoePlan);
     if (!g.up_tiles) return launch_one(up_kernel<false>, g.up, g.chunks, kUpThreads, bytes, stream, a);
-    return launch_one(g.up_mt == 2   ? up_tile_kernel<4, 2, 2, kOnce>
-                      : g.up_shared ? up_tile_kernel<2, 4, 2, 0>
-                                    : up_tile_kernel<2, 4, 2, kOnce>,
-                      g.up, g.chunks, kTileThreads, bytes, stream, a);
+    return launch_one(g.up_shared ? up_tile_kernel<0> : up_tile_kernel<kOnce>, g.up, g.chunks, kTileThreads, bytes, stream, a);
 }
 
 hipError_t launch_down(const MoeGrid& g, const DownArgs& a, float* sums, const StoredPlan* plans, hipStream_t stream) {
@@ -1186,7 +1191,7 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
     m.v = a.ws, m.ve = a.ws + slots * a.e.inter;
     float* sums = reinterpret_cast<float*>(m.ve + slots * m.e_stride);
     StoredPlan* plans = reinterpret_cast<StoredPlan*>(sums + moe_sum_rows(slots) * a.e.hidden);
-    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(g.up_tiles ? g.up_groups : a.e.inter / 32),
+    const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(a.e.inter / (g.up_tiles ? 128 : 32)),
                                        Divisor(g.up_tiles ? 1 : g.kw), 0, plans, 16 * g.down_mt}, stream);
     if (e != hipSuccess) return e;
     return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows}, sums, plans, stream);
