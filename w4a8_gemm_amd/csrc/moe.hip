@@ -1053,12 +1053,16 @@ MoeGrid moe_grid(const MoeArgs& a) {
     g.chunks = (unsigned)((a.tokens + chunk - 1) / chunk);
     const int64_t slots = (a.tokens < chunk ? a.tokens : chunk) * a.top_k, experts = a.e.experts;
     // experts met, about: were the slots spread at random
-    double missed = 1.0;
-    for (int64_t s = 0; s < slots && missed > 1e-3; ++s) missed *= 1.0 - 1.0 / (double)experts;
-    const int64_t met = (int64_t)((double)experts * (1.0 - missed) + 0.5);
+    const int64_t met = (int64_t)((double)experts * (1.0 - pow(1.0 - 1.0 / (double)experts, (double)slots)) + 0.5);
     const int64_t down_groups = (a.e.hidden / 16 + 15) / 16;
     const int64_t each = slots / experts;   // slots of an expert, on average, were none left out
     const bool small = slots <= kWaveSlots;
+    // Up to 64 slots: the down kernel's workgroups, one for each 16 columns, read inter of each expert met at some
+    // 30 GB/s, the tile kernels' together at 5.5 TB/s, but with a list of the slots and a third launch, 6 us
+    // (seven tokens of 7 in 60 experts, hidden 512, inter 7936: 72 us for 15 + 5; hidden 2048, inter 768,
+    // eight tokens of 8 in 128: 17 us for 11 + 5)
+    const double read = (double)met * (double)a.e.inter * 8.5;   // bytes of 16 columns
+    g.few = small && read / 30e3 < read * (double)(a.e.hidden / 16) / 5.5e6 + 6.0;
     // The second product's K parts, 2 or 4 within moe_sum_rows, while items are fewer than the CUs: parts cost their partial
     // sums (microseconds of the call with 1, 2 and 4: 32 items, inter 8192 53, 44, 42; 60, 7936 57, 50, 50; 128, 4096
     // 42, 45, 46; 128, 8192 92, 93, 94, and with units of 64 136, 142, 157)
@@ -1082,7 +1086,7 @@ MoeGrid moe_grid(const MoeArgs& a) {
         const double pairs = items / (double)(2 * cus), whole = floor(pairs), rest = pairs - whole;
         return chunks * (whole + (rest == 0.0 ? 0.0 : rest <= 0.5 ? 0.6 : 1.0));
     };
-    g.down_mt = rounds(4) < rounds(2) ? 4 : 2;
+    g.down_mt = !g.few && rounds(4) < rounds(2) ? 4 : 2;
     // Weights that several units read are left in the caches, the others' loads have the hint.  First product (with | without):
     // 60 slots of an expert, 16 experts, 2048 x 1408 44.8 | 46.4, 80 56.1 | 55.8, 8 experts 37.3 | 36.2; 72, 8 experts,
     // 4096 x 8192 -2 %.  Second, units of 32: 20 slots, 32 experts, 4096 x 4096 172 | 176, 28 188 | 188, 32 200 | 193,
@@ -1097,12 +1101,6 @@ MoeGrid moe_grid(const MoeArgs& a) {
         const int64_t most = slots < experts ? slots : experts + slots / columns;
         return most < slots ? most : slots;
     };
-    // Up to 64 slots: the down kernel's workgroups, one for each 16 columns, read inter of each expert met at some
-    // 30 GB/s, the tile kernels' together at 5.5 TB/s, but with a list of the slots and a third launch, 6 us
-    // (seven tokens of 7 in 60 experts, hidden 512, inter 7936: 72 us for 15 + 5; hidden 2048, inter 768,
-    // eight tokens of 8 in 128: 17 us for 11 + 5)
-    const double read = (double)met * (double)a.e.inter * 8.5;   // bytes of 16 columns
-    g.few = small && read / 30e3 < read * (double)(a.e.hidden / 16) / 5.5e6 + 6.0;
     const size_t scratch = g.few ? 0 : (plan_scratch(slots, experts) + 15) / 16 * 16;
     const auto at = [&](int64_t bytes) { return (size_t)bytes > scratch ? (size_t)bytes : scratch; };
     // as many workgroups of the tile kernels as the CUs hold at once: each lists the slots only once
@@ -1172,15 +1170,17 @@ size_t moe_workspace_bytes(int64_t slots, int64_t hidden, int64_t inter) {
     return (size_t)(slots * (inter + exponent_stride(inter)) + moe_sum_rows(slots) * hidden * 4) + (size_t)moe_plans(slots) * sizeof(StoredPlan);
 }
 
-int64_t moe_threads(const MoeArgs& a) {
-    const MoeGrid g = moe_grid(a);
+static int64_t threads(const MoeGrid& g) {
     const int64_t up = (int64_t)g.chunks * g.up * kUpThreads, down = (int64_t)g.chunks * g.down * kDownThreads;
     const int64_t join = (int64_t)g.join * 256, most = up > down ? up : down;
     return most > join ? most : join;
 }
 
-hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
+w4a8_status launch_moe(const MoeArgs& a, size_t ws_bytes, hipStream_t stream) {
     const MoeGrid g = moe_grid(a);
+    if (threads(g) >= kGridThreads) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    if (!a.ws || ws_bytes < moe_workspace_bytes(a.tokens * a.top_k, a.e.hidden, a.e.inter) || (uintptr_t)a.ws % 256 != 0)
+        return W4A8_ERR_WORKSPACE;
     MoeShape m{};
     m.tokens = a.tokens, m.hidden = a.e.hidden, m.inter = a.e.inter;
     m.by_top_k = Divisor(a.top_k);
@@ -1193,8 +1193,8 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
     StoredPlan* plans = reinterpret_cast<StoredPlan*>(sums + moe_sum_rows(slots) * a.e.hidden);
     const hipError_t e = launch_up(g, {m, a.e.up_w, a.e.up_s, a.x8, a.xs, a.ids, a.act, g.kw, Divisor(a.e.inter / (g.up_tiles ? 128 : 32)),
                                        Divisor(g.up_tiles ? 1 : g.kw), 0, plans, 16 * g.down_mt}, stream);
-    if (e != hipSuccess) return e;
-    return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows}, sums, plans, stream);
+    if (e != hipSuccess) return W4A8_ERR_HIP;
+    return launch_down(g, {m, a.e.down_w, a.e.down_s, a.ids, a.weights, a.out, g.rows}, sums, plans, stream) == hipSuccess ? W4A8_OK : W4A8_ERR_HIP;
 }
 
 }  // namespace w4a8

@@ -108,10 +108,7 @@ w4a8_status w4a8_moe_mxfp4(const w4a8_experts_mxfp4* experts, const uint8_t* d_x
     a.x8 = d_x_fp8, a.xs = d_x_scale, a.tokens = tokens;
     a.ids = d_ids, a.weights = d_weights, a.top_k = top_k, a.act = (int)act;
     a.out = d_out, a.ws = static_cast<uint8_t*>(d_ws);
-    if (moe_threads(a) >= kGridThreads) return W4A8_ERR_UNSUPPORTED_SHAPE;
-    if (!d_ws || ws_bytes < moe_workspace_bytes(tokens * top_k, experts->hidden, experts->inter) || !aligned(d_ws, 256))
-        return W4A8_ERR_WORKSPACE;
-    return hip_status(launch_moe(a, as_stream(stream)));
+    return launch_moe(a, ws_bytes, as_stream(stream));
 }
 
 }  // extern "C"

@@ -307,8 +307,8 @@ struct MoeArgs {
 constexpr int kMoeSlots = 2048;
 inline int64_t moe_chunk_tokens(int top_k) { return kMoeSlots / top_k; }
 size_t moe_workspace_bytes(int64_t slots, int64_t hidden, int64_t inter);
-int64_t moe_threads(const MoeArgs& a);
-hipError_t launch_moe(const MoeArgs& a, hipStream_t stream);
+// refuses a launch of too many threads and a workspace that is not enough, before anything is enqueued
+w4a8_status launch_moe(const MoeArgs& a, size_t ws_bytes, hipStream_t stream);
 
 // GEMM plans: the host picks the band, the tile and the K split.
 struct GemmPlan {
