@@ -29,7 +29,7 @@ def _logits(tokens, experts, seed):
     return x
 
 
-# up to 1023 tokens a wave to each, from 1024 on 16 lanes (up to 256 experts, 16 chosen)
+# a wave to a token, and 16 lanes
 @pytest.mark.parametrize("tokens,experts,top_k", [(40, 8, 3), (40, 128, 8), (17, 1000, 32), (1040, 16, 16), (1040, 128, 8),
                                                   (1030, 256, 1), (1030, 300, 5)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["fp32", "bf16", "fp16"])

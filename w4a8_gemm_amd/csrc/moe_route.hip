@@ -217,9 +217,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
     }
 }
 
-// Many tokens whose choice goes by the logits: four to a wave, 16 lanes each, lane L of them with the
-// experts L, L + 16, ...; a round's instructions serve four tokens (16384 tokens, 8 of 128 experts:
-// 8.6 us, a wave per token 11.8, both bound by their instructions).
+// Many tokens or few experts, where the choice goes by the logits: four tokens to a wave, 16 lanes each, lane L of
+// them with the experts L, L + 16, ...; a round's instructions serve four tokens (16384 tokens, 8 of 128
+// experts, one launch after another: 8.4 us, a wave per token 11.5, both bound by their instructions).
 template <w4a8_float TYPE, int NL>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_rows_kernel(RouteArgs a) {
     const int sub = threadIdx.x & 15;
@@ -289,7 +289,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_rows_kernel(RouteArgs 
     }
 }
 
-bool by_rows(const RouteArgs& a) { return !a.bias && a.groups == 1 && a.experts <= 256 && a.top_k <= 16 && a.tokens >= 1024; }
+// 16 lanes to a token hold up to 16 experts each, one after the other, where a wave holds 4: with more experts it takes more
+// tokens than the CUs' waves for them to be ahead.  Time of 16 lanes over a wave's: up to 32 experts 0.80 to 0.97 for any tokens;
+// 64 experts 1.02 to 1.04 for 1024 tokens, 0.97 to 1.02 for 2048, 0.54 to 0.63 for 16384; 128 1.15 for 1024, 1.00 to 1.06 for
+// 3001, 0.91 to 0.99 for 4096, 0.72 to 0.74 for 16384; 256 1.3 for 1024, 1.05 for 4096, 0.91 to 0.93 for 8192.
+bool by_rows(const RouteArgs& a) {
+    return !a.bias && a.groups == 1 && a.experts <= 256 && a.top_k <= 16 &&
+           (a.experts <= 32 || a.tokens >= (a.experts <= 64 ? 2048 : a.experts <= 128 ? 4096 : 8192));
+}
 
 template <w4a8_float TYPE>
 hipError_t launch_rows(const RouteArgs& a, hipStream_t stream) {
