@@ -3,8 +3,8 @@
 //   g, u = x W_up[e]^T (halves),  v = act(g) u,  out[t] = sum_j w[t, j] v[t, j] W_down[e]^T
 //
 // with up to some hundreds of tokens per expert: both products read each weight of the experts
-// met, and are bound by that, not by the matrix instructions (8 experts, hidden 4096, inter 8192: their 428 MB
-// take 69 us at 6.2 TB/s, the products of 502 slots 29 us at 3.5 PFLOP/s).  The weights are in the
+// met, and are bound by that until units are full (8 experts, hidden 4096, inter 8192: their 428 MB
+// take 69 us at 6.2 TB/s, the products of 502 slots 49 us at 1.4 PFLOP/s in bf16 and 10 at 3.2 in fp8).  The weights are in the
 // fragment order of the prepared linears (gemm_prepared.hip), so a wave's 16-row tile of 128 k is one
 // 1 KiB load.  The second product takes it as the e2m1 operand of one block-scaled 16x16x128 instruction, whose e4m3
 // operand is 16 slots' v (a slot: token t, j); the first widens it and the slots' activations to bf16.
@@ -320,8 +320,8 @@ __device__ __forceinline__ float activated(float g, int act) {
 // step of a large value is that token's error (up to 0.0135 of its result, 0.0018 with widened operands;
 // 77 tokens, 3 of 32 experts, 640 x 384), and large products that cancel take the small ones with them.  It costs
 // four instructions of half the time for one, and the conversions, which the weights' arrival hides but for full
-// units (64 tokens, 8 of 128 experts, 2048 x 768: 62.7 us cut, 60.2 widened, with the empty column tiles left out;
-// 251 tokens, 2 of 8, 4096 x 8192: 113 cut, 134 widened).
+// units (64 tokens, 8 of 128 experts, 2048 x 768: 63 us cut, 61 widened, with the empty column tiles left out;
+// 251 tokens, 2 of 8, 4096 x 8192: 113 cut, 130 to 139 widened).
 __device__ __forceinline__ v8bf widen_fp8(uint32_t a, uint32_t b) {
     const auto two = [](uint32_t codes, auto high) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, decltype(high)::value));
@@ -408,8 +408,8 @@ __device__ __forceinline__ void store_v(const MoeShape& m, const v4f (&r)[4], fl
 //
 // WAVE: up to 64 slots, listed by every wave; else listed in LDS.  Bound by how many bytes a CU has under way:
 // two steps of 5 KiB to a wave, two workgroups to a CU, of the registers that the widening leaves (one token
-// of eight experts, hidden 2048, inter 768: 13 MB in 5.9 us, of which 3 are the start, the list and the first loads' way;
-// eight tokens, 58 experts: 97 MB in 18.5 us, 5.2 TB/s).
+// of eight experts, hidden 2048, inter 768: 13.5 MB in 7.5 us, of which 3 are the start, the list and the first loads' way;
+// eight tokens, 78.8 MB in 20.2 us, 3.9 TB/s).
 template <bool WAVE>
 __global__ __launch_bounds__(kUpThreads, 4) void up_kernel(UpArgs a) {
     constexpr int D = 2;
@@ -517,8 +517,8 @@ struct DownStep {
 
 // Up to 64 slots.  A workgroup has 16 columns of the output and all slots: no partial sum leaves the CU, and no
 // third launch is needed.  Its waves take the units, or K parts of them where units are few; six steps in
-// flight.  Bound like the first product (one token of eight experts: 5.4 us; eight tokens, 58 experts:
-// 48 MB in 17.4 us, as the 128 workgroups of hidden 2048 fill half the CUs).
+// flight.  Bound like the first product (one token of eight experts: 7.0 MB in 6.2 us; eight tokens:
+// 40.6 MB in 16.5 us, as the 128 workgroups of hidden 2048 fill half the CUs).
 __global__ __launch_bounds__(kDownThreads) void down_kernel(DownArgs a) {
     constexpr int D = 6, kWaves = kDownThreads / 64;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -839,7 +839,10 @@ __device__ __forceinline__ void up_item(const UpArgs& a, const MoePlan& p, uint8
 
 // Units of up to 64 slots and 128 of inter to a workgroup, whose waves are all live (inter is a multiple of 128).  Sums of
 // two times four tiles, two steps of weights and half a chunk's columns fill the 128 registers that two
-// workgroups to a CU leave a wave.
+// workgroups to a CU leave a wave.  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 179 MB in 35.0 us, 5.1 TB/s; 251 tokens
+// of 2 in 8, hidden 4096, inter 8192: 383 MB (some experts have two units) in 85 us, 4.5 TB/s, the matrix pipe a third
+// and the vector pipe a quarter of the time: waves wait for columns, weights and each other in turn, which neither more
+// weights in flight nor columns widened once on their way to LDS change much (131 for 134 us of the call; 64 tokens 62 for 60).
 template <int HINT>
 __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -869,8 +872,8 @@ __global__ __launch_bounds__(kTileThreads, 4) void up_tile_kernel(UpArgs a) {
 
 // The second product's share of K part k of every slot, to partial sums [K part][slot][hidden] in
 // device memory: fp32, as the sum over the slots that follows is of terms of both signs.  A wave has two tiles of
-// output columns.  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 107 MB in 20 us, 5.3 TB/s; 8 experts,
-// hidden 4096, inter 8192: 143 MB in 39 to 44 us.
+// output columns.  64 tokens of 8 in 128 experts, hidden 2048, inter 768: 95.9 MB in 20.8 us, 4.6 TB/s; 251
+// tokens of 2 in 8, hidden 4096, inter 8192: 177 MB in 40.4 us, 4.4 TB/s.
 template <int MT, int D, int WAVES, int HINT>
 __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTileArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -985,7 +988,7 @@ __global__ __launch_bounds__(kTileThreads, WAVES) void down_tile_kernel(DownTile
 }
 
 // out from the partial sums: four columns of a token to a thread, its slots in order.  They come from the L2
-// that the last kernel left them in, or from memory (512 x 2048: 4.4 us, 502 x 4096: 4.8, of which some 3 are the launch).
+// that the last kernel left them in, or from memory (512 x 2048: 4.7 us, 502 x 4096: 5.2, of which some 3 are the launch).
 __global__ __launch_bounds__(256) void join_kernel(DownTileArgs a) {
     const MoeShape& m = a.m;
     const int64_t quads = m.hidden / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;

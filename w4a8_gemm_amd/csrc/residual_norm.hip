@@ -282,7 +282,8 @@ struct NormShape {
 };
 // Many rows: two runs to a thread (16384 rows of 5120: 106 us, with one 129, with four 111), but one where a
 // row has no more than a wave's (16384 rows of 256: 15 us, with two 23).  Few rows wait for their latency:
-// one run (a row of 5120: 4.1 us, with two 4.6).  More where 16 waves are too few.
+// one run (a row of 5120: 3.5 us, with two 4.0).  Between, two runs take of one's time 1.00 to 1.12 at 512 rows, 0.85 to 1.09 at
+// 1024 and 0.89 to 1.05 at 2048 (hidden 520 to 8192).  More where 16 waves are too few.
 NormShape norm_shape(const NormArgs& a) {
     const int runs = (a.hidden + 7) / 8;
     int r = runs <= 64 || a.tokens < 1024 ? 1 : 2;

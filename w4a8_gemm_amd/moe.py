@@ -5,6 +5,7 @@ block, its choice of each token's experts, and the experts' products on MXFP4 we
 As in attention.py, nothing is computed here: the compiled module _moe
 (csrc/moe_bind.cpp) turns tensors into pointers, the current torch stream into the
 HIP stream and status codes into exceptions.  Ids live on the GPU and are bounded there.
+Inference only, as the library: results carry no gradient, whatever the inputs require.
 """
 from __future__ import annotations
 
