@@ -25,8 +25,8 @@ def _want(c, act="silu"):
 
 
 # tokens, experts, top_k, hidden, inter: few slots; lists in LDS with the columns from the cache; columns in
-# LDS, 32 or 16 of inter to a wave, hidden of 1 to 17 steps of 128 (whole and partial chunks of four),
-# inter whose blocks fill the last workgroup's waves or not; few large units and many small ones
+# LDS, hidden of 1 to 17 steps of 128 (whole and partial chunks of four), units of one column tile to
+# four; few large units and many small ones
 SHAPES = [(1, 8, 8, 1152, 640), (7, 9, 7, 128, 3968), (8, 64, 8, 512, 384), (64, 1, 1, 128, 1152), (33, 8, 2, 2048, 1408),
           (100, 64, 2, 640, 768), (100, 64, 2, 768, 896), (90, 48, 2, 896, 1152), (60, 60, 4, 1152, 640), (120, 64, 3, 384, 1408),
           (70, 32, 4, 640, 1408), (100, 16, 4, 1152, 1408), (77, 32, 3, 640, 384), (30, 64, 4, 640, 640), (200, 4, 2, 640, 2176),

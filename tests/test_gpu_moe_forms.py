@@ -19,7 +19,7 @@ def _gpu():
     w4.lib()
 
 
-# many small experts (32 or 16 of inter to a wave) and few large ones, hidden of five steps
+# many small experts and few large ones, hidden of five steps
 STAGED = [(100, 64, 2, 640, 768), (100, 64, 2, 640, 1408), (300, 4, 2, 640, 1408), (1100, 4, 2, 640, 1408)]
 
 
@@ -79,3 +79,56 @@ def test_gelu_is_the_tanh_form(tokens, experts, top_k, inter):
     want, other = tight.experts(*args, "gelu_tanh"), tight.experts(*args, "gelu_erf")[0]
     _, bound = tight.check(c.run(act="gelu_tanh"), want)
     assert float((other - want[0]).norm() / want[0].norm()) > 2 * bound      # the other form would have failed
+
+
+@pytest.mark.parametrize("shape", STAGED, ids=lambda s: "x".join(map(str, s)))
+def test_tokens_that_are_no_numbers_and_slots_without_experts(shape):
+    say("moe_mxfp4 staged, no numbers, no experts", shape)
+    tokens, experts, top_k, hidden, inter = shape
+    c = Case(*shape, seed=2)
+    usual = c.run()
+    bad = [0, 7, tokens - 1]
+    c.xs[0], c.xs[7] = float("nan"), float("inf")
+    c.x8[tokens - 1, hidden - 1] = 0x7F                  # a code that is no number, in the last of five steps
+    got = c.run()
+    others = [t for t in range(tokens) if t not in bad]
+    assert bool(got[bad].isnan().all())
+    assert torch.equal(got[others], usual[others])
+    # slots without an expert, the bad tokens' among them: their weights are not looked at
+    c.ids[::3] = torch.tensor([-1, experts], dtype=torch.int32, device="cuda")
+    c.ids[bad] = -1
+    c.w[(c.ids < 0) | (c.ids >= experts)] = float("nan")
+    got = c.run()
+    assert not got[::3].any() and not got[bad].any()
+    c.xs[bad], c.x8[bad] = 1.0, 0
+    tight.check(got, tight.experts(c.x8, c.xs, c.ids, c.w.nan_to_num(0.0), c.up, c.down, c.n, "silu"))
+    c.ids.fill_(-1)
+    out = torch.full((tokens + 1, hidden), 5.0, dtype=torch.bfloat16, device="cuda")
+    c.run(out=out[:tokens])
+    assert not out[:tokens].any() and bool((out[tokens] == 5).all())
+
+
+@pytest.mark.parametrize("shape", STAGED, ids=lambda s: "x".join(map(str, s)))
+def test_one_expert_takes_every_slot(shape):
+    say("moe_mxfp4 staged, one expert", shape)
+    c = Case(*shape, seed=4)
+    c.ids.fill_(shape[1] - 1)                            # for every token, top_k times
+    tight.check(c.run(), tight.experts(c.x8, c.xs, c.ids, c.w, c.up, c.down, c.n, "silu"))
+
+
+def test_staged_calls_on_two_streams():
+    say("moe_mxfp4 staged, two streams")
+    cases = [Case(*STAGED[1], seed=5), Case(*STAGED[2], seed=6)]
+    want = [c.run() for c in cases]
+    spaces = [w4.MoEWorkspace(s[0], s[2], s[1], s[3], s[4]) for s in STAGED[1:3]]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(8):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(c.run(workspace=spaces[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for x in got[i]:
+            assert torch.equal(x, want[i]), i
